@@ -588,7 +588,7 @@ __global__ __launch_bounds__(BWD_THREADS, 1) void k_bwd_ffn(BwdArgs a) {
   const int C = a.n_cons, tid = threadIdx.x;
   if (blockIdx.x == 0 && tid == 0)  // the W-tile counter starts at zero for this launch
     __hip_atomic_store(a.wclaim, (uint64_t)a.wstamp << 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (load_status(a.status) != 0) return;
+  if (any_failed(a.status)) return;
   if ((a.join || C > 0) && blockIdx.x == 0) consumer_stamp(a.cons);
   const int n_mt = a.scalars[a.sc_nmt];
   // H, G and X items: round-robin over every workgroup, consecutive items on the workgroups of one XCD

@@ -64,6 +64,12 @@ __device__ __forceinline__ int32_t load_status(const int32_t* status) {
   return __hip_atomic_load(status, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// Whether a kernel or workgroup before reported an error: one answer for the whole workgroup, all of whose threads call
+// it.  Another workgroup of the same launch may report one between two waves' loads of the word; a wave that left alone
+// would leave the others to barriers and shared words that it no longer serves (without the first wave, the consumer
+// role copies the same unit for ever).
+__device__ __forceinline__ bool any_failed(const int32_t* status) { return __syncthreads_or(load_status(status) != 0) != 0; }
+
 // One thread: waits until the n flags fl[0 .. n) all equal epoch, taking them one at a time and sleeping longer while
 // one stays unset (up to max_nap + 1 sleeps of ~512 clocks between loads), so that a long wait sends few loads to the flags' lines (every
 // workgroup of a launch polls a handful of lines: polling every flag of a segment from every thread each ~0.1 us

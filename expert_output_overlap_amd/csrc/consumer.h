@@ -63,7 +63,7 @@ __device__ __forceinline__ void consumer_role(const ConsumerArgs& a) {
   __shared__ uint32_t s_cur;
   __shared__ int s_hit, s_stop;
   const int tid = threadIdx.x, nthr = blockDim.x;
-  if (load_status(a.status) != 0) return;
+  if (any_failed(a.status)) return;
   const int n_segs = a.scalars[SC_NSEGS];
   const uint64_t t0 = moe_clock();
   uint32_t next = 0;  // thread 0: the unit claimed for the next round

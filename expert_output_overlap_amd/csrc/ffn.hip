@@ -106,7 +106,7 @@ __global__ __launch_bounds__(WGM* WGN * 64) void k_gemm(GemmArgs a) {
     consumer_role(a.cons);
     return;
   }
-  if (load_status(a.status) != 0) return;
+  if (any_failed(a.status)) return;
   const int n_mt = a.scalars[a.sc_nmt];
   const int n_items = n_mt * a.n_nt;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -885,7 +885,7 @@ __global__ __launch_bounds__(FFN_THREADS, 1) void k_ffn_bf16(FusedArgs a) {
   __shared__ int s_land_u, s_land_p[LAND_ROWS], s_land_t[LAND_ROWS];
 
   launch_acquire();  // drop cache lines older than this launch (the publish protocol in common.h)
-  if (load_status(a.status) != 0) return;
+  if (any_failed(a.status)) return;
   const int n_mt = a.scalars[a.sc_nmt];
   // this batch's routed and returned rows (the layout's per-owner counts)
   int64_t m_real = 0, m_self = 0;
