@@ -25,7 +25,12 @@ EXPORTS = ["moe_last_error", "moe_version", "moe_route", "moe_layout_capacity_ro
            "moe_pick_consumer_cus_observed",
            "moe_expert_ffn_overlap", "moe_expert_ffn_overlap_noalloc", "moe_ffn_schedule",
            "moe_combine", "moe_set_kernel_timing", "moe_kernel_times", "moe_bwd_flags_count",
-           "moe_expert_ffn_backward", "moe_combine_backward"]
+           "moe_expert_ffn_backward", "moe_combine_backward",
+           "moe_layer_norm", "moe_layer_norm_workspace_bytes", "moe_layer_norm_backward", "moe_shared_ffn_row",
+           "moe_shared_ffn_workspace_bytes", "moe_shared_ffn", "moe_shared_ffn_backward", "moe_adamw_workspace_bytes",
+           "moe_adamw_bind", "moe_adamw_step", "moe_adamw_read_states"]
+MOE_ADAMW_BLOCK = 32
+MOE_NORM_MAX_D = 16384
 
 
 class moe_shape(ctypes.Structure):
@@ -56,6 +61,44 @@ BWD_FIELDS = ["topk_idx", "topk_w", "x_pad", "w_gate_up", "w_down", "d_out", "dy
 
 class moe_bwd_args(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in BWD_FIELDS]
+
+
+class moe_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64)]
+
+
+class moe_shared_shape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("d", ctypes.c_int32), ("f", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+SHARED_BWD_FIELDS = ["x", "w_gate_up", "w_down", "h", "gu", "dy", "residual", "dgu_ws", "dx", "dw_gate_up", "dw_down"]
+
+
+class moe_shared_bwd_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in SHARED_BWD_FIELDS]
+
+
+ADAMW_POINTERS = ["param", "copy", "grad", "m", "v", "m_scale", "v_scale", "m_values", "root_values"]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ADAMW_POINTERS] + [
+        ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("weight_decay", ctypes.c_float), ("lr_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_cfg(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("step", ctypes.c_int64), ("grad_scale", ctypes.c_void_p), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p)]
+
+
+class moe_adamw_plan(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_chunks", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
+                ("states8", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -93,6 +136,12 @@ def lib():
             "moe_bwd_flags_count": ([ps], i64),
             "moe_expert_ffn_backward": ([ps, pl, ctypes.POINTER(moe_bwd_args), vp, pc, vp], i32),
             "moe_combine_backward": ([ps, pl, vp, vp, vp, vp, vp, vp], i32),
+            "moe_layer_norm": ([vp] * 8, i32), "moe_layer_norm_workspace_bytes": ([vp], i64),
+            "moe_layer_norm_backward": ([vp] * 11 + [i64, vp], i32),
+            "moe_shared_ffn_row": ([vp], i64), "moe_shared_ffn_workspace_bytes": ([vp, i32], i64),
+            "moe_shared_ffn": ([vp] * 9 + [i64, vp], i32), "moe_shared_ffn_backward": ([vp, vp, vp, i64, vp], i32),
+            "moe_adamw_workspace_bytes": ([vp, i32], i64), "moe_adamw_bind": ([vp, i32, vp, i64, vp, vp], i32),
+            "moe_adamw_step": ([vp, vp, vp], i32), "moe_adamw_read_states": ([vp, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -241,3 +290,64 @@ def moe_combine_backward(shape: moe_shape, layout: moe_layout, d_out, y_recv, dx
     return _check("moe_combine_backward", lib().moe_combine_backward(
         ctypes.byref(shape), ctypes.byref(layout), _ptr(d_out), _ptr_array(y_recv), _ptr_array(dx_recv), _ptr(dx),
         _ptr(dw_route), _stream(stream)))
+
+
+# ---- the operators around the routed experts ---------------------------------------------------------------------
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def moe_layer_norm(shape: moe_norm_shape, x, weight, bias, y, mean=None, rstd=None, stream=None) -> int:
+    return _check("moe_layer_norm", lib().moe_layer_norm(ctypes.byref(shape), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                                         _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def moe_layer_norm_workspace_bytes(shape: moe_norm_shape) -> int:
+    return lib().moe_layer_norm_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_layer_norm_backward(shape: moe_norm_shape, dy, x, weight, mean, rstd, residual, dx, dweight, dbias, workspace,
+                            stream=None) -> int:
+    return _check("moe_layer_norm_backward", lib().moe_layer_norm_backward(
+        ctypes.byref(shape), _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(residual), _ptr(dx),
+        _ptr(dweight), _ptr(dbias), _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def moe_shared_ffn_row(shape: moe_shared_shape) -> int:
+    return lib().moe_shared_ffn_row(ctypes.byref(shape))
+
+
+def moe_shared_ffn_workspace_bytes(shape: moe_shared_shape, backward: bool) -> int:
+    return lib().moe_shared_ffn_workspace_bytes(ctypes.byref(shape), int(bool(backward)))
+
+
+def moe_shared_ffn(shape: moe_shared_shape, x, w_gate_up, w_down, residual, h, gu, y, workspace, stream=None) -> int:
+    return _check("moe_shared_ffn", lib().moe_shared_ffn(
+        ctypes.byref(shape), _ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(residual), _ptr(h), _ptr(gu), _ptr(y),
+        _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def moe_shared_ffn_backward(shape: moe_shared_shape, tensors: dict, workspace, stream=None) -> int:
+    """tensors: the moe_shared_bwd_args fields, as device tensors ("residual" optional)."""
+    a = moe_shared_bwd_args(*[_ptr(tensors.get(k) if k == "residual" else tensors[k]) for k in SHARED_BWD_FIELDS])
+    return _check("moe_shared_ffn_backward", lib().moe_shared_ffn_backward(
+        ctypes.byref(shape), ctypes.byref(a), _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def moe_adamw_workspace_bytes(tensors) -> int:
+    """tensors: a ctypes array of moe_adamw_tensor."""
+    return lib().moe_adamw_workspace_bytes(tensors, len(tensors))
+
+
+def moe_adamw_bind(tensors, workspace, plan: moe_adamw_plan, stream=None) -> int:
+    return _check("moe_adamw_bind", lib().moe_adamw_bind(tensors, len(tensors), _ptr(workspace), _bytes(workspace),
+                                                         ctypes.byref(plan), _stream(stream)))
+
+
+def moe_adamw_step(plan: moe_adamw_plan, cfg: moe_adamw_cfg, stream=None) -> int:
+    return _check("moe_adamw_step", lib().moe_adamw_step(ctypes.byref(plan), ctypes.byref(cfg), _stream(stream)))
+
+
+def moe_adamw_read_states(plan: moe_adamw_plan, stream=None) -> int:
+    return _check("moe_adamw_read_states", lib().moe_adamw_read_states(ctypes.byref(plan), _stream(stream)))

@@ -141,6 +141,8 @@ int timing_begin(CallEvents* ce) {
 
 }  // namespace
 
+int moe_fail(int code, const char* msg) { return fail(code, msg); }
+
 extern "C" {
 
 int moe_set_kernel_timing(int enable) {

@@ -1,0 +1,357 @@
+// C ABI of the operators around the routed experts: layer norm, the shared expert's block, AdamW (declarations and
+// contracts in include/moe_overlap.h).  Host side only: argument checks and launches on the caller's stream.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "../../include/moe_overlap.h"
+#include "launch.h"
+
+namespace {
+
+int64_t elem(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
+
+bool is_dtype(int t) { return t == MOE_BF16 || t == MOE_F32; }
+
+bool off(const void* p, uintptr_t align) { return (uintptr_t)p % align != 0; }
+
+// Bytes [p, p + n) of two buffers in common
+bool meet(const void* p, int64_t n, const void* q, int64_t m) {
+  return p && q && n > 0 && m > 0 && (uintptr_t)p < (uintptr_t)q + (uintptr_t)m && (uintptr_t)q < (uintptr_t)p + (uintptr_t)n;
+}
+
+const char* check_norm(const moe_norm_shape* s) {
+  if (!s) return "null shape";
+  if (s->rows < 0 || s->rows > (1ll << 40)) return "rows must be in [0, 2^40]";
+  if (s->d < 1 || s->d > MOE_NORM_MAX_D) return "d must be in [1, MOE_NORM_MAX_D]";
+  if (!is_dtype(s->dtype) || !is_dtype(s->param_dtype)) return "dtype must be MOE_BF16 or MOE_F32";
+  if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return "eps must be positive and finite";
+  for (const int64_t stride : {s->x_stride, s->y_stride, s->dx_stride})
+    if (stride != 0 && (stride < s->d || stride > (1ll << 40))) return "a row stride must be 0 or in [d, 2^40]";
+  return nullptr;
+}
+
+NormLaunch norm_of(const moe_norm_shape* s) {
+  NormLaunch a{};
+  a.rows = s->rows;
+  a.d = s->d;
+  a.dtype = s->dtype;
+  a.param_dtype = s->param_dtype;
+  a.eps = s->eps;
+  a.x_stride = s->x_stride ? s->x_stride : s->d;
+  a.y_stride = s->y_stride ? s->y_stride : s->d;
+  a.dx_stride = s->dx_stride ? s->dx_stride : s->d;
+  return a;
+}
+
+const char* check_shared(const moe_shared_shape* s) {
+  if (!s) return "null shape";
+  if (s->tokens < 0 || s->tokens > (1ll << 27)) return "tokens must be in [0, 2^27]";
+  if (s->d < 1 || s->d > 65536) return "d must be in [1, 65536]";
+  if (s->f < 1 || s->f > 65536) return "f must be in [1, 65536]";
+  if (!is_dtype(s->dtype)) return "dtype must be MOE_BF16 or MOE_F32";
+  return nullptr;
+}
+
+int shared_row(const moe_shared_shape* s) { return (s->f + 7) / 8 * 8; }
+
+const char* check_adamw(const moe_adamw_tensor* t, int32_t n) {
+  if (n < 0 || (n > 0 && !t)) return "null tensors";
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    const moe_adamw_tensor& a = t[i];
+    if (a.n < 0 || a.n > (1ll << 40)) return "elements must be in [0, 2^40]";
+    if (!is_dtype(a.param_dtype) || !is_dtype(a.grad_dtype)) return "dtype must be MOE_BF16 or MOE_F32";
+    if (a.state_bits != 32 && a.state_bits != 8) return "state_bits must be 32 or 8";
+    if (!std::isfinite(a.weight_decay) || !std::isfinite(a.lr_scale)) return "weight_decay and lr_scale must be finite";
+    if (a.n == 0) continue;
+    if (!a.param || !a.grad || !a.m || !a.v) return "null pointer";
+    if (a.state_bits == 8 && (!a.m_scale || !a.v_scale)) return "8-bit states need their scales";
+    if (a.state_bits == 32 && (a.m_scale || a.v_scale || a.m_values || a.root_values))
+      return "scales and values are for 8-bit states";
+    if (off(a.param, elem(a.param_dtype)) || off(a.grad, elem(a.grad_dtype)) || off(a.copy, 2) || off(a.m_values, 2) ||
+        off(a.root_values, 2) || (a.state_bits == 32 && (off(a.m, 4) || off(a.v, 4))))
+      return "a tensor must be aligned to its elements";
+    chunks += (a.n + ADAMW_CHUNK - 1) / ADAMW_CHUNK;
+  }
+  return chunks > 0x7fffffff ? "too many elements for one plan" : nullptr;
+}
+
+int64_t adamw_chunks(const moe_adamw_tensor* t, int32_t n) {
+  int64_t c = 0;
+  for (int i = 0; i < n; ++i) c += (t[i].n + ADAMW_CHUNK - 1) / ADAMW_CHUNK;
+  return c;
+}
+
+int64_t chunk_bytes(int64_t n_chunks) { return (n_chunks * (int64_t)sizeof(AdamwChunk) + 255) / 256 * 256; }
+
+AdamwStep adamw_of(const moe_adamw_plan* p) {
+  AdamwStep a{};
+  a.chunks = (const AdamwChunk*)p->table;
+  a.tensors = (const AdamwDesc*)((const char*)p->table + chunk_bytes(p->n_chunks));
+  return a;
+}
+
+const char* check_plan(const moe_adamw_plan* p) {
+  if (!p || p->n_chunks < 0 || p->n_chunks > 0x7fffffff || (p->n_chunks > 0 && !p->table)) return "plan not bound";
+  return nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* weight, const void* bias, void* y, float* mean,
+                   float* rstd, void* stream) {
+  if (const char* e = check_norm(s)) return moe_fail(MOE_EINVAL, e);
+  if (s->rows > 0 && (!x || !y)) return moe_fail(MOE_EINVAL, "null pointer");
+  if (!mean != !rstd) return moe_fail(MOE_EINVAL, "mean and rstd go together");
+  if (off(x, elem(s->dtype)) || off(y, elem(s->dtype)) || off(weight, elem(s->param_dtype)) ||
+      off(bias, elem(s->param_dtype)) || off(mean, 4) || off(rstd, 4))
+    return moe_fail(MOE_EINVAL, "a tensor must be aligned to its elements");
+  NormLaunch a = norm_of(s);
+  if (s->rows > 0) {
+    const int64_t es = elem(s->dtype), nx = ((s->rows - 1) * a.x_stride + s->d) * es, ny = ((s->rows - 1) * a.y_stride + s->d) * es;
+    if (meet(x, nx, y, ny) && !(x == y && a.x_stride == a.y_stride)) return moe_fail(MOE_EINVAL, "y overlaps x");
+  }
+  a.x = x;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  return launch_norm(a, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "layer norm launch failed") : MOE_OK;
+}
+
+int64_t moe_layer_norm_workspace_bytes(const moe_norm_shape* s) {
+  return check_norm(s) ? -1 : 4 * norm_partial_floats(s->rows, s->d, s->dtype);
+}
+
+int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void* x, const void* weight, const float* mean,
+                            const float* rstd, const void* residual, void* dx, void* dweight, void* dbias,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+  if (const char* e = check_norm(s)) return moe_fail(MOE_EINVAL, e);
+  if (s->rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return moe_fail(MOE_EINVAL, "null pointer");
+  if (off(x, elem(s->dtype)) || off(dy, elem(s->dtype)) || off(residual, elem(s->dtype)) || off(dx, elem(s->dtype)) ||
+      off(weight, elem(s->param_dtype)) || off(dweight, elem(s->param_dtype)) || off(dbias, elem(s->param_dtype)) ||
+      off(mean, 4) || off(rstd, 4) || off(workspace, 16))
+    return moe_fail(MOE_EINVAL, "a tensor must be aligned to its elements, the workspace to 16 bytes");
+  NormLaunch a = norm_of(s);
+  const bool params = dweight || dbias;
+  if (params) {
+    const int64_t need = moe_layer_norm_workspace_bytes(s);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
+  }
+  if (s->rows > 0) {
+    const int64_t es = elem(s->dtype), r = s->rows - 1;
+    const int64_t nx = (r * a.x_stride + s->d) * es, ny = (r * a.y_stride + s->d) * es, nd = (r * a.dx_stride + s->d) * es;
+    if (meet(x, nx, dx, nd)) return moe_fail(MOE_EINVAL, "dx overlaps x");
+    if (meet(dy, ny, dx, nd) && !(dy == dx && a.y_stride == a.dx_stride)) return moe_fail(MOE_EINVAL, "dx overlaps dy");
+    if (meet(residual, nd, dx, nd) && residual != dx) return moe_fail(MOE_EINVAL, "dx overlaps residual");
+  }
+  a.backward = true;
+  a.dy = dy;
+  a.x = x;
+  a.weight = weight;
+  a.mean = (float*)mean;
+  a.rstd = (float*)rstd;
+  a.residual = residual;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.partial = params ? (float*)workspace : nullptr;
+  return launch_norm(a, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "layer norm backward launch failed") : MOE_OK;
+}
+
+int64_t moe_shared_ffn_row(const moe_shared_shape* s) { return check_shared(s) ? -1 : shared_row(s); }
+
+int64_t moe_shared_ffn_workspace_bytes(const moe_shared_shape* s, int32_t backward) {
+  return check_shared(s) ? -1 : shared_workspace_bytes(s->tokens, s->d, s->f, s->dtype, backward != 0);
+}
+
+int moe_shared_ffn(const moe_shared_shape* s, const void* x, const void* w_gate_up, const void* w_down,
+                   const void* residual, void* h, float* gu, void* y, void* workspace, int64_t workspace_bytes,
+                   void* stream) {
+  if (const char* e = check_shared(s)) return moe_fail(MOE_EINVAL, e);
+  if (s->tokens == 0) return MOE_OK;
+  if (!x || !w_gate_up || !w_down || !h || !y) return moe_fail(MOE_EINVAL, "null pointer");
+  for (const void* p : {x, w_gate_up, w_down, residual, (const void*)h, (const void*)gu, (const void*)y,
+                        (const void*)workspace})
+    if (off(p, 16)) return moe_fail(MOE_EINVAL, "every tensor must be 16-byte aligned");
+  const int64_t need = moe_shared_ffn_workspace_bytes(s, 0);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
+  const int64_t es = elem(s->dtype), nx = s->tokens * s->d * es, nw = (int64_t)s->d * s->f * es,
+                nh = s->tokens * shared_row(s) * es, ngu = s->tokens * 2 * shared_row(s) * 4;
+  if (meet(y, nx, x, nx) || meet(y, nx, w_gate_up, 2 * nw) || meet(y, nx, w_down, nw) || meet(y, nx, h, nh) ||
+      meet(y, nx, gu, ngu) || (residual != y && meet(y, nx, residual, nx)))
+    return moe_fail(MOE_EINVAL, "y overlaps another tensor");
+  if (meet(h, nh, x, nx) || meet(h, nh, gu, ngu) || meet(gu, ngu, x, nx) || meet(h, nh, residual, nx) ||
+      meet(gu, ngu, residual, nx))
+    return moe_fail(MOE_EINVAL, "h or gu overlaps another tensor");
+  SharedLaunch a{};
+  a.tokens = s->tokens;
+  a.d = s->d;
+  a.f = s->f;
+  a.row = shared_row(s);
+  a.dtype = s->dtype;
+  a.x = x;
+  a.w_gate_up = w_gate_up;
+  a.w_down = w_down;
+  a.residual = residual;
+  a.h = h;
+  a.gu = gu;
+  a.y = y;
+  a.workspace = workspace;
+  return launch_shared(a, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "shared expert launch failed") : MOE_OK;
+}
+
+int moe_shared_ffn_backward(const moe_shared_shape* s, const moe_shared_bwd_args* b, void* workspace,
+                            int64_t workspace_bytes, void* stream) {
+  if (const char* e = check_shared(s)) return moe_fail(MOE_EINVAL, e);
+  if (!b || !b->dw_gate_up || !b->dw_down || !b->w_gate_up || !b->w_down ||
+      (s->tokens > 0 && (!b->x || !b->h || !b->gu || !b->dy || !b->dgu_ws || !b->dx)))
+    return moe_fail(MOE_EINVAL, "null pointer");
+  for (const void* p : {b->x, b->w_gate_up, b->w_down, b->h, (const void*)b->gu, b->dy, b->residual, (const void*)b->dgu_ws,
+                        (const void*)b->dx, (const void*)b->dw_gate_up, (const void*)b->dw_down, (const void*)workspace})
+    if (off(p, 16)) return moe_fail(MOE_EINVAL, "every tensor must be 16-byte aligned");
+  const int64_t need = moe_shared_ffn_workspace_bytes(s, 1);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
+  const int64_t es = elem(s->dtype), nx = s->tokens * s->d * es, nw = (int64_t)s->d * s->f * es,
+                nh = s->tokens * shared_row(s) * es, ngu = s->tokens * 2 * shared_row(s) * 4;
+  const struct { const void* p; int64_t n; } in[] = {{b->x, nx}, {b->w_gate_up, 2 * nw}, {b->w_down, nw}, {b->h, nh},
+                                                     {b->gu, ngu}, {b->dy, nx}, {b->residual, nx}},
+      out[] = {{b->dgu_ws, 2 * nh}, {b->dx, nx}, {b->dw_gate_up, 2 * nw}, {b->dw_down, nw}};
+  for (const auto& o : out)
+    for (const auto& i : in) {
+      const bool same = o.p == i.p && o.p == b->dx && i.p == b->residual;
+      if (!same && meet(o.p, o.n, i.p, i.n)) return moe_fail(MOE_EINVAL, "an output overlaps an input");
+    }
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return moe_fail(MOE_EINVAL, "two outputs overlap");
+  SharedLaunch a{};
+  a.backward = true;
+  a.tokens = s->tokens;
+  a.d = s->d;
+  a.f = s->f;
+  a.row = shared_row(s);
+  a.dtype = s->dtype;
+  a.x = b->x;
+  a.w_gate_up = b->w_gate_up;
+  a.w_down = b->w_down;
+  a.h = (void*)b->h;
+  a.gu = (float*)b->gu;
+  a.dy = b->dy;
+  a.residual = b->residual;
+  a.dgu = b->dgu_ws;
+  a.dx = b->dx;
+  a.dw_gate_up = b->dw_gate_up;
+  a.dw_down = b->dw_down;
+  a.workspace = workspace;
+  return launch_shared(a, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "shared expert backward launch failed") : MOE_OK;
+}
+
+int64_t moe_adamw_workspace_bytes(const moe_adamw_tensor* t, int32_t n_tensors) {
+  if (check_adamw(t, n_tensors)) return -1;
+  return chunk_bytes(adamw_chunks(t, n_tensors)) + n_tensors * (int64_t)sizeof(AdamwDesc);
+}
+
+int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes,
+                   moe_adamw_plan* plan, void* stream) {
+  if (const char* e = check_adamw(t, n_tensors)) return moe_fail(MOE_EINVAL, e);
+  if (!plan) return moe_fail(MOE_EINVAL, "null plan");
+  const int64_t n_chunks = adamw_chunks(t, n_tensors), need = moe_adamw_workspace_bytes(t, n_tensors);
+  if (n_tensors > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
+  if (off(workspace, 16)) return moe_fail(MOE_EINVAL, "workspace must be 16-byte aligned");
+  try {
+    struct Span {
+      uintptr_t at, end;
+      bool written;
+    };
+    std::vector<Span> spans;
+    int n8 = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+      const moe_adamw_tensor& a = t[i];
+      if (a.n == 0) continue;
+      const bool small = a.state_bits == 8;
+      n8 += small;
+      const int64_t blocks = (a.n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK, ss = small ? 1 : 4;
+      const struct { const void* p; int64_t n; } out[] = {{a.param, a.n * elem(a.param_dtype)}, {a.copy, a.n * 2},
+                                                          {a.m, a.n * ss}, {a.v, a.n * ss}, {a.m_scale, blocks},
+                                                          {a.v_scale, blocks}, {a.m_values, a.n * 2},
+                                                          {a.root_values, a.n * 2}, {workspace, need}};
+      for (const auto& o : out)
+        if (o.p && (o.p != workspace || i == 0)) spans.push_back({(uintptr_t)o.p, (uintptr_t)o.p + (uintptr_t)o.n, true});
+      spans.push_back({(uintptr_t)a.grad, (uintptr_t)a.grad + (uintptr_t)(a.n * elem(a.grad_dtype)), false});
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+    uintptr_t any = 0, written = 0;  // ends of what was seen so far, and of what of it the step writes
+    for (const Span& s : spans) {
+      if (s.at < written || (s.written && s.at < any))
+        return moe_fail(MOE_EINVAL, "a buffer that the step writes overlaps another (the same tensor twice?)");
+      any = std::max(any, s.end);
+      if (s.written) written = std::max(written, s.end);
+    }
+    if (n_tensors > 0) {
+      hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+      if (hipStreamIsCapturing((hipStream_t)stream, &cap) != hipSuccess) return moe_fail(MOE_EHIP, "stream query failed");
+      if (cap != hipStreamCaptureStatusNone) return moe_fail(MOE_EINVAL, "a plan cannot be bound under capture");
+      std::vector<char> host((size_t)need, 0);
+      AdamwChunk* c = (AdamwChunk*)host.data();
+      for (int i = 0; i < n_tensors; ++i)
+        for (int64_t k = 0; k < (t[i].n + ADAMW_CHUNK - 1) / ADAMW_CHUNK; ++k) *c++ = {i, (int32_t)k};
+      std::copy(t, t + n_tensors, (AdamwDesc*)(host.data() + chunk_bytes(n_chunks)));
+      if (hipMemcpyAsync(workspace, host.data(), (size_t)need, hipMemcpyHostToDevice, (hipStream_t)stream) != hipSuccess ||
+          hipStreamSynchronize((hipStream_t)stream) != hipSuccess)
+        return moe_fail(MOE_EHIP, "plan copy failed");
+    }
+    plan->table = workspace;
+    plan->n_chunks = n_chunks;
+    plan->n_tensors = n_tensors;
+    plan->states8 = n8;
+  } catch (const std::bad_alloc&) {
+    return moe_fail(MOE_EINVAL, "out of host memory");
+  }
+  return MOE_OK;
+}
+
+int moe_adamw_step(const moe_adamw_plan* plan, const moe_adamw_cfg* cfg, void* stream) {
+  if (const char* e = check_plan(plan)) return moe_fail(MOE_EINVAL, e);
+  if (!cfg) return moe_fail(MOE_EINVAL, "null cfg");
+  if (!std::isfinite(cfg->lr) || cfg->lr < 0 || !std::isfinite(cfg->eps) || cfg->eps < 0)
+    return moe_fail(MOE_EINVAL, "lr and eps must be finite and not negative");
+  if (!(cfg->beta1 >= 0 && cfg->beta1 < 1) || !(cfg->beta2 >= 0 && cfg->beta2 < 1))
+    return moe_fail(MOE_EINVAL, "betas must be in [0, 1)");
+  if (cfg->step < 1 && !cfg->step_dev) return moe_fail(MOE_EINVAL, "step must be >= 1");
+  if (off(cfg->grad_scale, 4) || off(cfg->lr_dev, 4) || off(cfg->step_dev, 8))
+    return moe_fail(MOE_EINVAL, "a device number must be aligned to its size");
+  AdamwStep a = adamw_of(plan);
+  a.lr = (float)cfg->lr;
+  a.beta1 = (float)cfg->beta1;
+  a.beta2 = (float)cfg->beta2;
+  a.one1 = (float)(1.0 - cfg->beta1);
+  a.one2 = (float)(1.0 - cfg->beta2);
+  a.eps = (float)cfg->eps;
+  a.log_beta1 = std::log(cfg->beta1);
+  a.log_beta2 = std::log(cfg->beta2);
+  const double t = (double)std::max<int64_t>(cfg->step, 1);
+  a.inv_c1 = (float)(1.0 / -std::expm1(t * a.log_beta1));
+  a.inv_root_c2 = (float)(1.0 / std::sqrt(-std::expm1(t * a.log_beta2)));
+  a.grad_scale = cfg->grad_scale;
+  a.lr_dev = cfg->lr_dev;
+  a.step_dev = cfg->step_dev;
+  return launch_adamw(a, plan->n_chunks, false, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "AdamW launch failed") : MOE_OK;
+}
+
+int moe_adamw_read_states(const moe_adamw_plan* plan, void* stream) {
+  if (const char* e = check_plan(plan)) return moe_fail(MOE_EINVAL, e);
+  if (plan->states8 == 0) return MOE_OK;
+  return launch_adamw(adamw_of(plan), plan->n_chunks, true, (hipStream_t)stream)
+             ? moe_fail(MOE_EHIP, "AdamW state launch failed")
+             : MOE_OK;
+}
+
+}  // extern "C"

@@ -133,3 +133,52 @@ int launch_bwd_combine(const BwdLaunch& p, int T_o, int G, const int32_t* plan, 
                        float* dw, hipStream_t st);
 // A nonzero value distinct for every launch that opens a copy-unit counter.
 uint32_t next_stamp();
+
+// ---- the operators around the routed experts --------------------------------------------------------------------
+
+// Records the calling thread's error message and returns the code (api.cpp).
+int moe_fail(int code, const char* msg);
+
+// Layer norm (norm.hip); strides in elements, all given.
+struct NormLaunch {
+  int64_t rows, x_stride, y_stride, dx_stride;
+  int d, dtype, param_dtype;
+  bool backward;
+  float eps;
+  const void *x, *weight, *bias, *dy, *residual;
+  void *y, *dx, *dweight, *dbias;
+  float *mean, *rstd;
+  float* partial;  // backward: the workgroups' sums, or null where neither dweight nor dbias is wanted
+};
+int64_t norm_partial_floats(int64_t rows, int d, int dtype);
+int launch_norm(const NormLaunch& a, hipStream_t st);
+
+// AdamW (adamw.hip): the plan's device table is the chunks, then the tensors' descriptors.
+#define ADAMW_CHUNK 4096  // elements of one workgroup; a multiple of MOE_ADAMW_BLOCK and of 1024
+typedef moe_adamw_tensor AdamwDesc;
+struct AdamwChunk {
+  int32_t tensor, index;
+};
+struct AdamwStep {
+  const AdamwChunk* chunks;
+  const AdamwDesc* tensors;
+  float lr, beta1, beta2, one1, one2, eps, inv_c1, inv_root_c2;  // one: 1 - beta; inv_c1: 1 / (1 - beta1^t)
+  double log_beta1, log_beta2;
+  const float *grad_scale, *lr_dev;
+  const int64_t* step_dev;
+};
+int launch_adamw(const AdamwStep& a, int64_t n_chunks, bool read, hipStream_t st);
+
+// The shared expert's block (shared.hip); row: elements in a row of h and in each half of gu and dgu.
+struct SharedLaunch {
+  int64_t tokens;
+  int d, f, row, dtype;
+  bool backward;
+  const void *x, *w_gate_up, *w_down, *residual, *dy;
+  void *h, *y;
+  float* gu;
+  void *dgu, *dx, *dw_gate_up, *dw_down;
+  void* workspace;
+};
+int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool backward);
+int launch_shared(const SharedLaunch& s, hipStream_t st);

@@ -159,6 +159,263 @@ class MoePath:
                 "n_remote_mtiles": sc[4 + self.R]}
 
 
+# ---- the operators around the routed experts ---------------------------------------------------------------------
+
+TORCH_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+MOE_DTYPES = {"bf16": B.MOE_BF16, "f32": B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float32: B.MOE_F32}
+
+
+def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device, strided=False):
+    """A tensor that a kernel reads or writes through its address alone: anything else than what it takes is an error."""
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        raise ValueError("%s: %s %s on %s, wanted %s %s on %s" % (name, t.dtype, tuple(t.shape), t.device, dtype, tuple(shape),
+                                                                  device))
+    if strided:
+        if t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
+            raise ValueError("%s: rows must hold their elements side by side and not overlap" % name)
+    elif not t.is_contiguous():
+        raise ValueError("%s: not contiguous" % name)
+
+
+def _device(device) -> torch.device:
+    device = torch.device(device)
+    return torch.device(device.type, torch.cuda.current_device()) if device.type == "cuda" and device.index is None else device
+
+
+def _workspace(nbytes: int, fn: str, device):
+    if nbytes < 0:
+        raise B.MoeError(fn, B.MOE_EINVAL, "invalid shape")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+class LayerNorm:
+    """Layer norm over up to ``rows`` rows of ``d`` elements (moe_layer_norm, moe_layer_norm_backward), with the buffers of
+    its results: y, and for training dx, dweight, dbias and what the backward call needs.  Rows may lie apart (a slice of
+    a wider tensor).  A call's results stay until the next call of the same kind."""
+
+    def __init__(self, rows, d, dtype="bf16", param_dtype="f32", eps=1e-5, train=True, device="cuda"):
+        self.device = _device(device)
+        self.rows, self.d, self.train = rows, d, train
+        self.dtype, self.param_dtype = TORCH_DTYPES[dtype], TORCH_DTYPES[param_dtype]
+        self.shape = B.moe_norm_shape(rows, d, MOE_DTYPES[dtype], MOE_DTYPES[param_dtype], eps, 0, 0, 0)
+        z = dict(device=self.device)
+        ws = _workspace(B.moe_layer_norm_workspace_bytes(self.shape), "moe_layer_norm_workspace_bytes", self.device)
+        self.y = torch.empty(rows, d, dtype=self.dtype, **z)
+        self.mean = self.rstd = None
+        if train:
+            self.workspace = ws
+            self.mean, self.rstd = (torch.empty(rows, dtype=torch.float32, **z) for _ in range(2))
+            self.dx = torch.empty(rows, d, dtype=self.dtype, **z)
+            self.dweight, self.dbias = (torch.empty(d, dtype=self.param_dtype, **z) for _ in range(2))
+
+    def _rows(self, x):
+        if x.shape[0] > self.rows:
+            raise ValueError("%d rows, made for up to %d" % (x.shape[0], self.rows))
+        return x.shape[0]
+
+    def _stride(self, t):
+        return t.stride(0) if t.shape[0] > 1 else 0
+
+    def _params(self, **params):
+        for name, t in params.items():
+            if t is not None:
+                _need(t, name, (self.d,), self.param_dtype, self.device)
+
+    def forward(self, x, weight=None, bias=None, y=None, stream=None):
+        n = self._rows(x)
+        y = self.y[:n] if y is None else y
+        _need(x, "x", (n, self.d), self.dtype, self.device, strided=True)
+        _need(y, "y", (n, self.d), self.dtype, self.device, strided=True)
+        self._params(weight=weight, bias=bias)
+        s = self.shape
+        s.rows, s.x_stride, s.y_stride = n, self._stride(x), self._stride(y)
+        with torch.cuda.device(self.device):
+            B.moe_layer_norm(s, x, weight, bias, y, self.mean, self.rstd, stream)
+        return y
+
+    def backward(self, dy, x, weight=None, residual=None, dx=None, stream=None):
+        """dx (added to ``residual`` where given), and dweight and dbias in their buffers, for the rows x of the last
+        forward call."""
+        if not self.train:
+            raise RuntimeError("made without train=True")
+        n = self._rows(x)
+        dx = self.dx[:n] if dx is None else dx
+        for name, t in (("x", x), ("dy", dy), ("dx", dx)):
+            _need(t, name, (n, self.d), self.dtype, self.device, strided=True)
+        if residual is not None:
+            _need(residual, "residual", (n, self.d), self.dtype, self.device, strided=True)
+            if self._stride(residual) != self._stride(dx):
+                raise ValueError("residual and dx: their rows must lie equally far apart")
+        self._params(weight=weight)
+        s = self.shape
+        s.rows, s.x_stride, s.y_stride, s.dx_stride = n, self._stride(x), self._stride(dy), self._stride(dx)
+        with torch.cuda.device(self.device):
+            B.moe_layer_norm_backward(s, dy, x, weight, self.mean, self.rstd, residual, dx, self.dweight, self.dbias,
+                                      self.workspace, stream)
+        return dx
+
+
+class SharedFFN:
+    """The shared expert's gated feed-forward block over up to ``tokens`` tokens (moe_shared_ffn, moe_shared_ffn_backward),
+    with the buffers of its results and workspaces.  A call's results stay until the next call of the same kind."""
+
+    def __init__(self, tokens, d, f, dtype="bf16", train=True, device="cuda"):
+        self.device = _device(device)
+        self.tokens, self.d, self.f, self.train = tokens, d, f, train
+        self.dtype = TORCH_DTYPES[dtype]
+        self.shape = B.moe_shared_shape(tokens, d, f, MOE_DTYPES[dtype])
+        row = B.moe_shared_ffn_row(self.shape)
+        if row < 0:
+            raise B.MoeError("moe_shared_ffn_row", B.MOE_EINVAL, "invalid shape")
+        need = max(B.moe_shared_ffn_workspace_bytes(self.shape, b) for b in ((False, True) if train else (False,)))
+        self.workspace = _workspace(need, "moe_shared_ffn_workspace_bytes", self.device)
+        z = dict(dtype=self.dtype, device=self.device)
+        self.y, self.h = torch.empty(tokens, d, **z), torch.empty(tokens, row, **z)
+        self.gu = None
+        if train:
+            self.gu = torch.empty(tokens, 2 * row, dtype=torch.float32, device=self.device)
+            self.dgu = torch.empty(tokens, 2 * row, **z)
+            self.dx = torch.empty(tokens, d, **z)
+            self.dw_gate_up, self.dw_down = torch.empty(2 * f, d, **z), torch.empty(d, f, **z)
+
+    def _check(self, x, w_gate_up, w_down, **rows):
+        n = x.shape[0]
+        if n > self.tokens:
+            raise ValueError("%d tokens, made for up to %d" % (n, self.tokens))
+        for name, t in (("x", x), *rows.items()):
+            if t is not None:
+                _need(t, name, (n, self.d), self.dtype, self.device)
+        _need(w_gate_up, "w_gate_up", (2 * self.f, self.d), self.dtype, self.device)
+        _need(w_down, "w_down", (self.d, self.f), self.dtype, self.device)
+        self.shape.tokens = n
+        return n
+
+    def forward(self, x, w_gate_up, w_down, residual=None, y=None, stream=None):
+        y = self.y[: x.shape[0]] if y is None else y
+        self._check(x, w_gate_up, w_down, residual=residual, y=y)
+        with torch.cuda.device(self.device):
+            B.moe_shared_ffn(self.shape, x, w_gate_up, w_down, residual, self.h, self.gu, y, self.workspace, stream)
+        return y
+
+    def backward(self, dy, x, w_gate_up, w_down, residual=None, dx=None, stream=None):
+        """dx (added to ``residual`` where given), and dw_gate_up and dw_down in their buffers, for the x and the weights of
+        the last forward call."""
+        if not self.train:
+            raise RuntimeError("made without train=True")
+        dx = self.dx[: x.shape[0]] if dx is None else dx
+        self._check(x, w_gate_up, w_down, dy=dy, residual=residual, dx=dx)
+        t = {"x": x, "w_gate_up": w_gate_up, "w_down": w_down, "h": self.h, "gu": self.gu, "dy": dy, "residual": residual,
+             "dgu_ws": self.dgu, "dx": dx, "dw_gate_up": self.dw_gate_up, "dw_down": self.dw_down}
+        with torch.cuda.device(self.device):
+            B.moe_shared_ffn_backward(self.shape, t, self.workspace, stream)
+        return dx
+
+
+class AdamW:
+    """AdamW over many tensors in one launch (moe_adamw_*).  tensors: dicts of device tensors with equal numbers of elements,
+    "p" (bf16 or fp32), "g", "m" and "v" (fp32, or uint8 codes with "m_scale" and "v_scale", see ``states``), optionally
+    "copy" (bf16, the new p), "m_values" and "root_values" (bf16, what ``read_states`` fills), and numbers "weight_decay" and
+    "lr_scale".  The tensors' addresses are bound: their contents may change between steps, not they themselves."""
+
+    FIELDS = dict(param="p", copy="copy", grad="g", m="m", v="v", m_scale="m_scale", v_scale="v_scale", m_values="m_values",
+                  root_values="root_values")
+
+    def __init__(self, tensors, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, stream=None):
+        self.tensors = [dict(t) for t in tensors]
+        self.device = self.tensors[0]["p"].device if self.tensors else _device("cuda")
+        self.betas, self.eps = betas, eps
+        table = (B.moe_adamw_tensor * len(self.tensors))()
+        for i, (q, t) in enumerate(zip(table, self.tensors)):
+            n, bits = t["p"].numel(), 8 if t["m"].dtype is torch.uint8 else 32
+            state = torch.uint8 if bits == 8 else torch.float32
+            blocks = -(-n // B.MOE_ADAMW_BLOCK)
+            wanted = dict(copy=(torch.bfloat16, n), m=(state, n), v=(state, n), m_scale=(torch.uint8, blocks),
+                          v_scale=(torch.uint8, blocks), m_values=(torch.bfloat16, n), root_values=(torch.bfloat16, n))
+            for field, key in self.FIELDS.items():
+                x = t.get(key)
+                if x is None:
+                    continue
+                dtype, k = wanted.get(key, (x.dtype, n))
+                if x.dtype is not dtype or x.numel() != k or not x.is_contiguous() or x.device != self.device:
+                    raise ValueError("tensor %d, %s: %d %s on %s, wanted %d contiguous %s on %s" % (
+                        i, key, x.numel(), x.dtype, x.device, k, dtype, self.device))
+                setattr(q, field, x.data_ptr())
+            if t["p"].dtype not in MOE_DTYPES or t["g"].dtype not in MOE_DTYPES:
+                raise ValueError("tensor %d: p and g must be bf16 or fp32" % i)
+            q.n, q.param_dtype, q.grad_dtype, q.state_bits = n, MOE_DTYPES[t["p"].dtype], MOE_DTYPES[t["g"].dtype], bits
+            q.weight_decay, q.lr_scale = t.get("weight_decay", weight_decay), t.get("lr_scale", 1.0)
+        self.workspace = _workspace(B.moe_adamw_workspace_bytes(table), "moe_adamw_workspace_bytes", self.device)
+        self.plan = B.moe_adamw_plan()
+        with torch.cuda.device(self.device):
+            B.moe_adamw_bind(table, self.workspace, self.plan, stream)
+
+    @staticmethod
+    def states(p: torch.Tensor, bits: int = 32) -> dict:
+        """The states of a tensor before its first step: zeros."""
+        n, z = p.numel(), dict(device=p.device)
+        if bits == 32:
+            return {k: torch.zeros(n, **z) for k in ("m", "v")}
+        blocks = -(-n // B.MOE_ADAMW_BLOCK)
+        return {k: torch.zeros(k.endswith("scale") and blocks or n, dtype=torch.uint8, **z)
+                for k in ("m", "v", "m_scale", "v_scale")}
+
+    def step(self, step, lr, grad_scale=None, stream=None):
+        """step: 1, 2, ..., or an int64 tensor on the device; lr: a number, or an fp32 tensor on the device (both: what a
+        captured step reads anew at each replay); grad_scale: None, or an fp32 tensor on the device."""
+        cfg = B.moe_adamw_cfg(0.0, *self.betas, self.eps, 1, None, None, None)
+        for field, value, dtype in (("step", step, torch.int64), ("lr", lr, torch.float32),
+                                    ("grad_scale", grad_scale, torch.float32)):
+            if isinstance(value, torch.Tensor):
+                if value.dtype is not dtype or value.numel() != 1 or value.device != self.device:
+                    raise ValueError("%s: one %s on %s wanted" % (field, dtype, self.device))
+                setattr(cfg, "grad_scale" if field == "grad_scale" else field + "_dev", value.data_ptr())
+            elif value is not None:
+                setattr(cfg, field, value)
+        with torch.cuda.device(self.device):
+            B.moe_adamw_step(self.plan, cfg, stream)
+
+    def read_states(self, stream=None):
+        """The 8-bit states' values into the tensors' "m_values" and "root_values", where given."""
+        with torch.cuda.device(self.device):
+            B.moe_adamw_read_states(self.plan, stream)
+
+
+class MoeBlock:
+    """A pre-norm MoE block of one rank: n = norm(x); out = combine(routed experts(n)) + shared expert(n), and its backward.
+    The router's product is the caller's: ``norm`` gives the rows its logits come from, ``experts`` takes the logits;
+    ``experts_backward`` gives the gradient of n (and path.bwd_buffers()["dw_route"] that of the routing weights), to which
+    the caller adds the router's part before ``norm_backward``.  w: norm_weight, norm_bias, w_gate_up, w_down (the routed
+    experts' [E_l, ...]), shared_gate_up, shared_down."""
+
+    def __init__(self, path: MoePath, shared_f: int, eps=1e-5, train=True):
+        self.path, self.train = path, train
+        self.norm_op = LayerNorm(path.T, path.d, path.dtype, "f32", eps, train, path.device)
+        self.shared = SharedFFN(path.T, path.d, shared_f, path.dtype, train, path.device)
+
+    def norm(self, x, w, stream=None):
+        self.n = self.norm_op.forward(x, w["norm_weight"], w["norm_bias"], stream=stream)
+        return self.n
+
+    def experts(self, logits, w, stream=None):
+        p, out = self.path, self.path.out[: self.path.T]
+        p.route(logits, stream)
+        p.layout(self.n, stream=stream)
+        p.ffn(w["w_gate_up"], w["w_down"], gu_out=p.gu_buffer() if self.train else None, stream=stream)
+        p.combine(stream=stream)
+        return self.shared.forward(self.n, w["shared_gate_up"], w["shared_down"], residual=out, y=out, stream=stream)
+
+    def experts_backward(self, d_out, w, stream=None):
+        p = self.path
+        p.backward(d_out, w["w_gate_up"], w["w_down"], gu=p.gu_buffer(), stream=stream)
+        p.combine_backward(d_out, stream=stream)
+        dn = p.bwd_buffers()["dx"][: p.T]
+        return self.shared.backward(d_out, self.n, w["shared_gate_up"], w["shared_down"], residual=dn, dx=dn, stream=stream)
+
+    def norm_backward(self, dn, x, w, residual=None, stream=None):
+        """dx; residual: the gradient that reaches x past the block."""
+        return self.norm_op.backward(dn, x, w["norm_weight"], residual=residual, stream=stream)
+
+
 def to_device(a, dtype: str, device="cuda") -> torch.Tensor:
     """Host array from moe_inputs (bf16 bits as uint16, or fp32/int32) to a device tensor of the right type."""
     import numpy as np

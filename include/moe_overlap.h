@@ -351,6 +351,161 @@ int moe_expert_ffn_backward(const moe_shape* s, const moe_layout* L, const moe_b
 int moe_combine_backward(const moe_shape* s, const moe_layout* L, const void* d_out, void* const* y_recv,
                          void* const* dx_recv, void* dx, float* dw_route, void* stream);
 
+/* ---- layer norm ---------------------------------------------------------------------------------
+ * The norm in front of an MoE layer, whose rows moe_layout_build gathers and the router's logits come from.  Per row
+ * of d elements, with mu = mean(x), var = mean((x - mu)^2), rstd = 1 / sqrt(var + eps), n = (x - mu) rstd:
+ *   y = n weight + bias
+ * and backward, with a = dy weight:
+ *   dx = rstd (a - mean(a) - n mean(a n)) [+ residual],   dweight = sum over rows of dy n,   dbias = sum of dy.
+ * Statistics and sums in fp32 (the variance from the differences to the mean), each result rounded once.  The rows'
+ * sums of the weight's gradient run in a fixed order, so equal calls on equal devices give equal bits.
+ * Any alignment and any row stride >= d; elements between rows are neither read nor written.  An output may not overlap
+ * an input, except that y may be x and dx may be dy or residual (with the same row stride). */
+typedef struct {
+  int64_t rows;         /* T >= 0 (0: dweight and dbias become 0, nothing else is written) */
+  int32_t d;            /* 1 .. MOE_NORM_MAX_D */
+  int32_t dtype;        /* moe_dtype of x, y, dy, dx, residual */
+  int32_t param_dtype;  /* moe_dtype of weight, bias, dweight, dbias */
+  float eps;            /* > 0, finite */
+  int64_t x_stride;     /* elements from a row of x to the next; 0 = d */
+  int64_t y_stride;     /* of y (forward) and dy (backward); 0 = d */
+  int64_t dx_stride;    /* of dx and residual; 0 = d */
+} moe_norm_shape;
+#define MOE_NORM_MAX_D 16384
+
+/* x (device) [rows, d]; weight, bias (device) [d], NULL = 1 and 0; y (device) [rows, d]; mean, rstd (device) fp32 [rows],
+ * what the backward call takes, or both NULL. */
+int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* weight, const void* bias, void* y, float* mean,
+                   float* rstd, void* stream);
+
+/* Bytes of the backward call's workspace (the workgroups' partial sums of dweight and dbias); -1 for an invalid shape.
+ * It needs no initial contents; calls that may run at the same time need one each. */
+int64_t moe_layer_norm_workspace_bytes(const moe_norm_shape* s);
+
+/* dy, x, weight, mean, rstd: the forward's; residual (device) [rows, d] or NULL: added to dx before it is rounded (the
+ * gradient that reaches x past the norm); dx (device) [rows, d]; dweight, dbias (device) [d], written, either may be NULL;
+ * workspace (device), 16-byte aligned, >= moe_layer_norm_workspace_bytes (may be NULL if dweight and dbias are). */
+int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void* x, const void* weight, const float* mean,
+                            const float* rstd, const void* residual, void* dx, void* dweight, void* dbias,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- shared expert ------------------------------------------------------------------------------
+ * The gated feed-forward block that every token goes through beside its routed experts (no layout, no routing):
+ *   g = x Wg^T, u = x Wu^T, h = silu(g) u, y = h Wd^T [+ residual]      Wg = rows [0, f), Wu = rows [f, 2f) of w_gate_up
+ * and backward, given dy:
+ *   dh = dy Wd, du = dh silu(g), dg = dh u silu'(g),
+ *   dx = (dg | du) w_gate_up [+ residual],  dw_gate_up = (dg | du)^T x,  dw_down = dy^T h.
+ * bf16: products on bf16 operands with fp32 sums; h, dg and du, operands of the next products, are rounded to bf16, the
+ * results once; g and u are kept in fp32 (in bf16 they would add a third rounding of the size of the result's own to every
+ * gradient).  f32: everything in fp32. */
+typedef struct {
+  int64_t tokens;  /* T in [0, 2^27] (0: the backward's weight gradients become 0, nothing else is written) */
+  int32_t d;       /* 1 .. 65536 */
+  int32_t f;       /* 1 .. 65536 */
+  int32_t dtype;   /* moe_dtype */
+} moe_shared_shape;
+
+/* Elements in a row of h and of each half of gu and dgu_ws in the buffers below: f rounded up to a multiple of 8, so that every row starts at
+ * 16 bytes; the elements past f are the library's.  -1 for an invalid shape. */
+int64_t moe_shared_ffn_row(const moe_shared_shape* s);
+
+/* Bytes of the workspace of a forward (backward = 0) or backward (1) call; -1 for an invalid shape.  It holds k-split
+ * partial sums and, for bf16 operands whose rows do not start at 16 bytes (d or f not a multiple of 8), copies of them whose
+ * rows do.  It needs no initial contents; calls that may run at the same time need one each.  0 = may be NULL. */
+int64_t moe_shared_ffn_workspace_bytes(const moe_shared_shape* s, int32_t backward);
+
+/* x (device) [T, d]; w_gate_up (device) [2f, d]; w_down (device) [d, f]; residual (device) [T, d] or NULL, added to y
+ * before it is rounded (the routed experts' combined output); h (device) [T, F] with F = moe_shared_ffn_row, written;
+ * gu (device) fp32 [T, 2F] or NULL: g | u for a backward call; y (device) [T, d], may be residual itself, overlaps nothing else.
+ * x, w_gate_up, w_down, residual, y: rows side by side, 16-byte aligned; h, gu, workspace 16-byte aligned. */
+int moe_shared_ffn(const moe_shared_shape* s, const void* x, const void* w_gate_up, const void* w_down,
+                   const void* residual, void* h, float* gu, void* y, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+
+typedef struct {
+  const void* x;         /* (device) [T, d] the forward's input */
+  const void* w_gate_up; /* (device) [2f, d] */
+  const void* w_down;    /* (device) [d, f] */
+  const void* h;         /* (device) [T, F] as the forward wrote it */
+  const float* gu;       /* (device) [T, 2F] as the forward wrote it */
+  const void* dy;        /* (device) [T, d] */
+  const void* residual;  /* (device) [T, d] or NULL: added to dx before it is rounded */
+  void* dgu_ws;          /* (device) [T, 2F] workspace: dg | du */
+  void* dx;              /* (device) [T, d], may be residual itself, overlaps nothing else */
+  void* dw_gate_up;      /* (device) [2f, d] in the element type, written, not accumulated */
+  void* dw_down;         /* (device) [d, f] in the element type, written */
+} moe_shared_bwd_args;   /* every pointer 16-byte aligned */
+
+int moe_shared_ffn_backward(const moe_shared_shape* s, const moe_shared_bwd_args* b, void* workspace,
+                            int64_t workspace_bytes, void* stream);
+
+/* ---- AdamW --------------------------------------------------------------------------------------
+ * One optimizer step over many tensors in one launch.  Per element, with g = grad (times *grad_scale):
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, p rounded to its type at the end, copy = the new p in bf16 (the weights that the FFN calls read).
+ * States in 32 bits: m and v fp32.  States in 8 bits, in blocks of MOE_ADAMW_BLOCK elements from each tensor's start, with a
+ * scale byte b per block and state standing for 2^(b - 127):
+ *   m: e4m3 codes (no infinities, 0x7f and 0xff NaN), nearest, ties to even; b the smallest >= 1 at which the block's largest
+ *      |m| is at most 448 scales;
+ *   v: codes of its root, sqrt(v): 16 e + k for (1 + k/16) 2^(e - 15) scales, 0 for zero, 255 for a value that is not finite;
+ *      nearest, ties to even, but a positive value is never below code 1, so that rounding makes no divisor zero; b the
+ *      smallest >= 16 at which the block's largest root is at most 1.875 scales.
+ * The root rather than v: it halves the exponent range that a block has to cover and is what the update divides by.  Elements
+ * that are not finite do not count for a block's scale, and stay NaN.  A step of an 8-bit state that is smaller than half
+ * the distance of two codes leaves the code as it is.  All zero bytes are states of zero. */
+#define MOE_ADAMW_BLOCK 32
+typedef struct {
+  void* param;         /* (device) [n] updated */
+  void* copy;          /* (device) [n] bf16, written, or NULL */
+  const void* grad;    /* (device) [n] */
+  void* m;             /* (device) [n] fp32, or uint8 codes */
+  void* v;             /* (device) [n] fp32, or uint8 codes of the root */
+  uint8_t* m_scale;    /* (device) [ceil(n / MOE_ADAMW_BLOCK)] for 8-bit states, else NULL */
+  uint8_t* v_scale;
+  void* m_values;      /* (device) [n] bf16 or NULL: where moe_adamw_read_states writes m of 8-bit states */
+  void* root_values;   /* (device) [n] bf16 or NULL: and the root of v */
+  int64_t n;           /* elements, >= 0 */
+  int32_t param_dtype; /* moe_dtype */
+  int32_t grad_dtype;  /* moe_dtype */
+  int32_t state_bits;  /* 32 or 8 */
+  float weight_decay;
+  float lr_scale;      /* factor of the step's lr for this tensor, 1 for none */
+  int32_t reserved;    /* 0 */
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0, 1), eps >= 0, all finite */
+  int64_t step;                /* t >= 1 */
+  const float* grad_scale;     /* (device) factor of every gradient, e.g. a clipping coefficient; NULL = 1 */
+  const float* lr_dev;         /* (device) overrides lr, or NULL; with step_dev: for a captured call that is replayed */
+  const int64_t* step_dev;     /* (device) overrides step, or NULL */
+} moe_adamw_cfg;
+
+/* A bound list of tensors: host values, and the descriptors in the caller's workspace. */
+typedef struct {
+  void* table;       /* (device) */
+  int64_t n_chunks;
+  int32_t n_tensors;
+  int32_t states8;   /* tensors with 8-bit states */
+} moe_adamw_plan;
+
+/* Bytes of the workspace that moe_adamw_bind fills; -1 for invalid tensors. */
+int64_t moe_adamw_workspace_bytes(const moe_adamw_tensor* t, int32_t n_tensors);
+
+/* Check the tensors, write their descriptors into `workspace` (device, 16-byte aligned, kept as long as the plan) and fill
+ * *plan.  Waits for the copy on `stream`; not for a stream under capture.  MOE_EINVAL where two of the buffers that the step
+ * writes overlap each other or a gradient (the same tensor twice). */
+int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes,
+                   moe_adamw_plan* plan, void* stream);
+
+/* One step over the plan's tensors. */
+int moe_adamw_step(const moe_adamw_plan* plan, const moe_adamw_cfg* cfg, void* stream);
+
+/* The values of the plan's 8-bit states into m_values and root_values, where given (a checkpoint, a look at them).  bf16
+ * holds each value exactly. */
+int moe_adamw_read_states(const moe_adamw_plan* plan, void* stream);
+
 /* While enabled (nonzero), every moe_expert_ffn_overlap and moe_expert_ffn_backward call of this process times
  * each of its launches with a pair of HIP events that the launch itself records (hipExtLaunchKernel: the kernel's start and end, no marker
  * in the caller's stream).  Disabled by default.  Returns MOE_OK. */

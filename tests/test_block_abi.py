@@ -1,0 +1,179 @@
+"""Argument checks of the operators around the routed experts: each refusal happens on the host, before any launch, so these
+run without a GPU on made-up addresses."""
+import ctypes
+
+import pytest
+
+from expert_output_overlap_amd import binding as B
+
+A = 1 << 30  # made-up device addresses, far apart
+P = [A + k * (1 << 28) for k in range(16)]
+
+
+def refused(rc, words):
+    assert rc == B.MOE_EINVAL and words in B.moe_last_error(), (rc, B.moe_last_error())
+
+
+def norm_shape(**kw):
+    v = dict(rows=4, d=64, dtype=B.MOE_BF16, param_dtype=B.MOE_F32, eps=1e-5, x_stride=0, y_stride=0, dx_stride=0)
+    return B.moe_norm_shape(**{**v, **kw})
+
+
+@pytest.mark.parametrize("kw", [dict(rows=-1), dict(d=0), dict(d=B.MOE_NORM_MAX_D + 1), dict(dtype=2), dict(param_dtype=-1),
+                                dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x_stride=63),
+                                dict(y_stride=-64), dict(dx_stride=1)])
+def test_norm_shapes(kw):
+    s = norm_shape(**kw)
+    assert B.moe_layer_norm_workspace_bytes(s) == -1
+    assert B.lib().moe_layer_norm(ctypes.byref(s), P[0], P[1], P[2], P[3], None, None, None) == B.MOE_EINVAL
+    assert B.moe_last_error()
+
+
+def test_norm_arguments():
+    L, s = B.lib(), norm_shape()
+    f = lambda x=P[0], w=P[1], b=P[2], y=P[3], m=P[4], r=P[5]: L.moe_layer_norm(ctypes.byref(s), x, w, b, y, m, r, None)
+    refused(f(x=None), "null")
+    refused(f(y=None), "null")
+    refused(f(m=None), "go together")
+    refused(f(x=P[0] + 1), "aligned")
+    refused(f(w=P[1] + 2), "aligned")
+    refused(f(y=P[0] + 64), "overlaps")
+    need = B.moe_layer_norm_workspace_bytes(s)
+    assert need > 0
+    b = lambda **kw: L.moe_layer_norm_backward(ctypes.byref(s), *[kw.get(k, d) for k, d in (
+        ("dy", P[0]), ("x", P[1]), ("w", P[2]), ("mean", P[3]), ("rstd", P[4]), ("res", P[5]), ("dx", P[6]), ("dw", P[7]),
+        ("db", P[8]), ("ws", P[9]), ("n", need), ("st", None))])
+    refused(b(mean=None), "null")
+    refused(b(dx=None), "null")
+    refused(b(n=need - 1), "too small")
+    refused(b(ws=None), "too small")
+    refused(b(ws=P[9] + 8), "aligned")
+    refused(b(dx=P[1]), "overlaps x")
+    refused(b(dx=P[0] + 2), "overlaps dy")
+    refused(b(dx=P[5] + 128), "overlaps residual")
+    assert L.moe_layer_norm(None, P[0], P[1], P[2], P[3], None, None, None) == B.MOE_EINVAL
+
+
+def test_norm_workspace_grows_with_rows_to_a_limit():
+    sizes = [B.moe_layer_norm_workspace_bytes(norm_shape(rows=r, d=7168)) for r in (1, 10, 1000, 10 ** 6, 10 ** 9)]
+    assert sizes == sorted(sizes) and sizes[-1] == sizes[-2] <= 64 << 20
+
+
+def shared_shape(**kw):
+    return B.moe_shared_shape(**{**dict(tokens=8, d=64, f=128, dtype=B.MOE_BF16), **kw})
+
+
+@pytest.mark.parametrize("kw", [dict(tokens=-1), dict(tokens=(1 << 27) + 1), dict(d=0), dict(d=65537), dict(f=0),
+                                dict(f=65537), dict(dtype=3)])
+def test_shared_shapes(kw):
+    s = shared_shape(**kw)
+    assert B.moe_shared_ffn_row(s) == -1
+    assert B.moe_shared_ffn_workspace_bytes(s, False) == -1 and B.moe_shared_ffn_workspace_bytes(s, True) == -1
+    assert B.lib().moe_shared_ffn(ctypes.byref(s), *P[:8], 0, None) == B.MOE_EINVAL
+
+
+def test_shared_arguments():
+    L, s = B.lib(), shared_shape()
+    big = 1 << 27
+
+    def f(**kw):
+        return L.moe_shared_ffn(ctypes.byref(s), *[kw.get(k, d) for k, d in (
+            ("x", P[0]), ("wgu", P[1]), ("wd", P[2]), ("res", P[3]), ("h", P[4]), ("gu", P[5]), ("y", P[6]), ("ws", P[7]),
+            ("n", big), ("st", None))])
+
+    for k in ("x", "wgu", "wd", "h", "y"):
+        refused(f(**{k: None}), "null")
+    for k, p in (("x", P[0]), ("wgu", P[1]), ("wd", P[2]), ("res", P[3]), ("h", P[4]), ("gu", P[5]), ("y", P[6]), ("ws", P[7])):
+        refused(f(**{k: p + 8}), "aligned")
+    for other in (P[0], P[1], P[2], P[4], P[5], P[3] + 16):
+        refused(f(y=other), "y overlaps")
+    refused(f(h=P[0]), "h or gu overlaps")
+    refused(f(gu=P[4]), "h or gu overlaps")
+    s0 = shared_shape(d=100, f=36)
+    need = B.moe_shared_ffn_workspace_bytes(s0, False)
+    if need:
+        refused(L.moe_shared_ffn(ctypes.byref(s0), *P[:8], need - 1, None), "too small")
+        refused(L.moe_shared_ffn(ctypes.byref(s0), *P[:7], None, need, None), "too small")
+
+    def b(**kw):
+        a = B.moe_shared_bwd_args(**{**dict(zip(B.SHARED_BWD_FIELDS, P)), **kw})
+        return L.moe_shared_ffn_backward(ctypes.byref(s), ctypes.byref(a), P[12], big, None)
+
+    for k in B.SHARED_BWD_FIELDS:
+        if k != "residual":
+            refused(b(**{k: None}), "null")
+        refused(b(**{k: P[B.SHARED_BWD_FIELDS.index(k)] + 4}), "aligned")
+    at = dict(zip(B.SHARED_BWD_FIELDS, P))
+    refused(b(dx=at["x"]), "output overlaps an input")
+    refused(b(dx=at["dy"]), "output overlaps an input")
+    refused(b(dgu_ws=at["h"]), "output overlaps an input")
+    refused(b(dgu_ws=at["gu"] + 16), "output overlaps an input")
+    refused(b(dw_down=at["w_down"]), "output overlaps an input")
+    refused(b(dw_down=at["dw_gate_up"]), "two outputs")
+    assert L.moe_shared_ffn_backward(ctypes.byref(s), None, None, 0, None) == B.MOE_EINVAL
+
+
+def test_shared_rows_and_workspaces():
+    assert [B.moe_shared_ffn_row(shared_shape(f=f)) for f in (1, 8, 517, 1408)] == [8, 8, 520, 1408]
+    for backward in (False, True):
+        for d, f, dtype in ((7168, 2048, B.MOE_BF16), (100, 36, B.MOE_BF16), (333, 517, B.MOE_BF16), (333, 517, B.MOE_F32)):
+            sizes = [B.moe_shared_ffn_workspace_bytes(shared_shape(tokens=t, d=d, f=f, dtype=dtype), backward)
+                     for t in (0, 1, 2, 16, 17, 63, 64, 65, 100, 128, 129, 300, 512, 1000, 3000, 20000)]
+            assert sizes == sorted(sizes)  # buffers made for the most tokens serve fewer
+
+
+def adam(**kw):
+    v = dict(param=P[0], copy=P[1], grad=P[2], m=P[3], v=P[4], m_scale=None, v_scale=None, m_values=None, root_values=None,
+             n=100, param_dtype=B.MOE_F32, grad_dtype=B.MOE_F32, state_bits=32, weight_decay=0.1, lr_scale=1.0, reserved=0)
+    return B.moe_adamw_tensor(**{**v, **kw})
+
+
+def bind(tensors, ws=P[15], n=1 << 20):
+    table, plan = (B.moe_adamw_tensor * len(tensors))(*tensors), B.moe_adamw_plan()
+    return B.lib().moe_adamw_bind(table, len(tensors), ws, n, ctypes.byref(plan), None)
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(n=-1), "elements"), (dict(param_dtype=5), "dtype"), (dict(grad_dtype=-2), "dtype"), (dict(state_bits=16), "bits"),
+    (dict(weight_decay=float("nan")), "finite"), (dict(lr_scale=float("inf")), "finite"), (dict(param=None), "null"),
+    (dict(grad=None), "null"), (dict(m=None), "null"), (dict(state_bits=8), "scales"), (dict(m_scale=P[5]), "8-bit"),
+    (dict(param=P[0] + 2), "aligned"), (dict(m=P[3] + 1), "aligned"), (dict(copy=P[1] + 1), "aligned"),
+    (dict(copy=P[0]), "overlaps"), (dict(m=P[2]), "overlaps"), (dict(v=P[3] + 396), "overlaps"), (dict(grad=P[0] + 4), "overlaps"),
+])
+def test_adamw_tensors(kw, words):
+    refused(bind([adam(**kw)]), words)
+
+
+def test_adamw_plans():
+    t = adam()
+    refused(bind([t, adam()]), "overlaps")  # the same tensor twice
+    other = dict(param=P[5], copy=P[6], m=P[7], v=P[8])
+    refused(bind([t, adam(**other)], n=100), "too small")
+    refused(bind([t, adam(**other)], ws=None), "too small")
+    refused(bind([t], ws=P[15] + 4), "aligned")
+    refused(bind([t], ws=P[0]), "overlaps")
+    two = (B.moe_adamw_tensor * 2)(t, adam(**other, n=5000))
+    assert B.moe_adamw_workspace_bytes(two) == 256 + 2 * ctypes.sizeof(B.moe_adamw_tensor)
+    assert B.moe_adamw_workspace_bytes((B.moe_adamw_tensor * 1)(adam(n=-1))) == -1
+    plan = B.moe_adamw_plan()
+    assert B.lib().moe_adamw_bind(None, 0, None, 0, ctypes.byref(plan), None) == B.MOE_OK  # no tensors: nothing to do
+    assert B.lib().moe_adamw_step(ctypes.byref(plan), ctypes.byref(cfg()), None) == B.MOE_OK
+
+
+def cfg(**kw):
+    return B.moe_adamw_cfg(**{**dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1), **kw})
+
+
+@pytest.mark.parametrize("kw,words", [
+    (dict(lr=-1.0), "lr"), (dict(lr=float("nan")), "lr"), (dict(eps=-1e-8), "eps"), (dict(beta1=1.0), "betas"),
+    (dict(beta2=-0.1), "betas"), (dict(beta2=float("nan")), "betas"), (dict(step=0), "step"), (dict(step_dev=P[0] + 4), "aligned"),
+])
+def test_adamw_steps(kw, words):
+    plan = B.moe_adamw_plan(P[15], 1, 1, 0)
+    refused(B.lib().moe_adamw_step(ctypes.byref(plan), ctypes.byref(cfg(**kw)), None), words)
+
+
+def test_adamw_unbound_plan():
+    refused(B.lib().moe_adamw_step(None, ctypes.byref(cfg()), None), "plan")
+    refused(B.lib().moe_adamw_step(ctypes.byref(B.moe_adamw_plan(None, 3, 1, 0)), ctypes.byref(cfg()), None), "plan")
+    refused(B.lib().moe_adamw_read_states(None, None), "plan")

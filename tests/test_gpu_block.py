@@ -1,0 +1,529 @@
+"""The operators around the routed experts on the GPU against 64-bit formulas, with bounds counted from their roundings."""
+import pytest
+import torch
+
+import block_reference as ref
+from expert_output_overlap_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *s: torch.randn(*s, generator=g, device="cuda")
+
+
+def spread(t, pad):
+    """t's rows as a slice of a wider tensor, whose other elements are NaN."""
+    wide = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=t.device)
+    wide[:, : t.shape[1]] = t
+    return wide[:, : t.shape[1]]
+
+
+def check(got, want, names, tag):
+    for n in names:
+        ref.within(got[n], *want[n], (tag, n))
+
+
+# ---- layer norm --------------------------------------------------------------------------------------------------
+
+def norm_case(rows, d, dtype, params, pad=0, seed=0, residual=True):
+    from expert_output_overlap_amd.runtime import LayerNorm
+
+    rnd = gen(1000 + seed)
+    dt, pt = DT[dtype], DT[params]
+    x = (rnd(rows, d) * torch.exp(0.5 * rnd(d)) + 3 * rnd(d)).to(dt)
+    x[:, :: 37] *= 16
+    w, b = (1 + 0.2 * rnd(d)).to(pt), (0.1 * rnd(d)).to(pt)
+    dy, res = rnd(rows, d).to(dt), rnd(rows, d).to(dt) if residual else None
+    if pad:
+        x, dy = spread(x, pad), spread(dy, pad + 1)
+    op = LayerNorm(rows, d, dtype, params)
+    y = op.forward(x, w, b)
+    dx = op.backward(dy, x, w, residual=res)
+    got = {"y": y, "dx": dx, "dweight": op.dweight, "dbias": op.dbias}
+    return op, (x, w, b, dy, res), got, ref.layer_norm(x, w, b, 1e-5, dy, res)
+
+
+NORM_SIZES = [(1, 64), (1, 7168), (3, 1), (5, 7), (17, 65), (300, 512), (70, 513), (33, 1024), (40, 1407), (64, 2048),
+              (9, 2049), (700, 4096), (21, 7168), (2000, 5000), (13, 8192), (7, 8193), (6, 16383), (5, 16384), (9000, 96)]
+
+
+@pytest.mark.parametrize("rows,d", NORM_SIZES)
+@pytest.mark.parametrize("dtype,params", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")])
+def test_norm(rows, d, dtype, params):
+    _, _, got, want = norm_case(rows, d, dtype, params, pad=(rows + d) % 3)
+    check(got, want, ("y", "dx", "dweight", "dbias"), (rows, d, dtype, params))
+
+
+def test_norm_is_the_same_each_time_and_in_place():
+    op, (x, w, b, dy, res), got, _ = norm_case(1500, 1536, "bf16", "f32", residual=True)
+    first = {k: v.clone() for k, v in got.items()}
+    for _ in range(2):
+        op.forward(x, w, b)
+        op.backward(dy, x, w, residual=res)
+        assert all(torch.equal(first[k], got[k]) for k in first)
+    dy2, res2, x2 = dy.clone(), res.clone(), x.clone()
+    op.backward(dy2, x, w, residual=res, dx=dy2)
+    assert torch.equal(dy2, first["dx"])
+    op.backward(dy, x, w, residual=res2, dx=res2)
+    assert torch.equal(res2, first["dx"])
+    assert torch.equal(op.forward(x2, w, b, y=x2), first["y"])
+
+
+def test_norm_leaves_what_is_not_its_own():
+    """Fewer rows than the buffers hold, results as slices: everything else stays."""
+    from expert_output_overlap_amd.runtime import LayerNorm
+
+    rnd = gen(3)
+    op = LayerNorm(64, 96, "bf16", "f32")
+    x, w = rnd(10, 96).bfloat16(), 1 + rnd(96)
+    y = torch.full((10, 130), 7.0, device="cuda", dtype=torch.bfloat16)
+    for t in (op.y, op.dx, op.mean, op.rstd):
+        t.fill_(7.0)
+    op.forward(x, w, None, y=y[:, 17:113])
+    assert (y[:, :17] == 7).all() and (y[:, 113:] == 7).all() and (op.y == 7).all() and (op.mean[10:] == 7).all()
+    op.backward(y[:, 17:113], x, w)
+    assert (op.dx[10:] == 7).all() and not (op.dx[:10] == 7).all()
+    want = ref.layer_norm(x, w, torch.zeros(96, device="cuda"), 1e-5)
+    ref.within(y[:, 17:113], *want["y"], "y")
+
+
+def test_norm_of_nothing_and_without_parameters():
+    from expert_output_overlap_amd.runtime import LayerNorm
+
+    rnd = gen(4)
+    op = LayerNorm(8, 200, "f32", "f32")
+    none = torch.empty(0, 200, device="cuda")
+    op.dweight.fill_(5.0)
+    op.dbias.fill_(5.0)
+    assert op.forward(none).shape == (0, 200)
+    op.backward(none, none)
+    assert (op.dweight == 0).all() and (op.dbias == 0).all()
+    x, dy = rnd(8, 200), rnd(8, 200)
+    one, zero = torch.ones(200, device="cuda"), torch.zeros(200, device="cuda")
+    want = ref.layer_norm(x, one, zero, 1e-5, dy)
+    got = {"y": op.forward(x), "dx": op.backward(dy, x), "dweight": op.dweight, "dbias": op.dbias}
+    check(got, want, ("y", "dx", "dweight", "dbias"), "no parameters")
+
+
+def test_norm_of_constant_and_bad_rows():
+    """A row without variance gives its bias; a NaN or an infinity stays in its own row."""
+    from expert_output_overlap_amd.runtime import LayerNorm
+
+    rnd = gen(5)
+    x = rnd(6, 768)
+    x[1] = 3.25
+    x[3, 5] = float("nan")
+    x[4, 700] = float("inf")
+    w, b = 1 + 0.1 * rnd(768), rnd(768)
+    op = LayerNorm(6, 768, "f32", "f32")
+    y = op.forward(x, w, b)
+    assert torch.equal(y[1], b) and torch.isnan(y[3]).all() and not torch.isfinite(y[4]).any()
+    good = [0, 2, 5]
+    ref.within(y[good], *ref.layer_norm(x[good], w, b, 1e-5)["y"], "good rows")
+
+
+# ---- the shared expert -------------------------------------------------------------------------------------------
+
+def ffn_case(T, d, f, dtype, seed=0):
+    rnd = gen(2000 + seed)
+    dt = DT[dtype]
+    x, res, dy = (rnd(T, d).to(dt) for _ in range(3))
+    return x, (rnd(2 * f, d) / d ** 0.5).to(dt), (rnd(d, f) / d ** 0.5).to(dt), res, dy
+
+
+FFN_SIZES = [(1, 64, 64), (1, 1, 1), (1, 7168, 256), (2, 100, 36), (5, 333, 517), (16, 512, 200), (17, 256, 1408), (31, 65, 8),
+             (64, 1024, 512), (65, 128, 320), (100, 8, 520), (129, 72, 1032), (200, 2048, 1408), (255, 320, 257),
+             (256, 256, 256), (301, 333, 517), (512, 512, 384), (777, 640, 136), (1030, 264, 648), (2049, 136, 72)]
+
+
+@pytest.mark.parametrize("T,d,f", FFN_SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_ffn(T, d, f, dtype):
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, dtype)
+    serve = SharedFFN(T, d, f, dtype, train=False)
+    want = ref.shared_ffn(x, wgu, wd, residual=res)
+    ref.within(serve.forward(x, wgu, wd, residual=res), *want["y"], ("y + residual", T, d, f))
+    op = SharedFFN(T, d, f, dtype)
+    want = ref.shared_ffn(x, wgu, wd, residual=res, dy=dy)
+    got = {"y": op.forward(x, wgu, wd), "dx": op.backward(dy, x, wgu, wd, residual=res), "dw_gate_up": op.dw_gate_up,
+           "dw_down": op.dw_down}
+    check(got, want, ("y", "dx", "dw_gate_up", "dw_down"), (T, d, f, dtype))
+
+
+@pytest.mark.parametrize("T,d,f,dtype", [(4096, 1024, 768, "bf16"), (3, 2048, 5632, "bf16"), (40, 4096, 3000, "bf16"),
+                                         (1500, 2000, 1000, "bf16"), (600, 700, 800, "f32")])
+def test_shared_ffn_larger(T, d, f, dtype):
+    """Sizes where the products split, or fill the device several times; the same call twice gives the same bits."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, dtype, seed=1)
+    op = SharedFFN(T, d, f, dtype)
+    want = ref.shared_ffn(x, wgu, wd, residual=res, dy=dy)
+    got = {"y": op.forward(x, wgu, wd), "dx": op.backward(dy, x, wgu, wd, residual=res), "dw_gate_up": op.dw_gate_up,
+           "dw_down": op.dw_down}
+    check(got, want, ("y", "dx", "dw_gate_up", "dw_down"), (T, d, f, dtype))
+    first = {k: v.clone() for k, v in got.items()}
+    op.forward(x, wgu, wd)
+    op.backward(dy, x, wgu, wd, residual=res)
+    assert all(torch.equal(first[k], got[k]) for k in first)
+
+
+@pytest.mark.parametrize("T,d,f,dtype", [(1, 256, 512, "bf16"), (48, 200, 100, "bf16"), (300, 512, 256, "bf16"),
+                                         (50, 33, 65, "f32")])
+def test_shared_ffn_in_place_and_fewer_tokens(T, d, f, dtype):
+    """y over the residual, dx over its residual; rows behind the last token stay as they were."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, dtype, seed=2)
+    op = SharedFFN(T + 37, d, f, dtype)
+    for t in (op.y, op.h, op.gu, op.dgu, op.dx):
+        t.fill_(7.0)
+    want, wante = ref.shared_ffn(x, wgu, wd, residual=res, dy=dy), ref.shared_ffn(x, wgu, wd, residual=res)
+    y = res.clone()
+    op.forward(x, wgu, wd, residual=y, y=y)
+    ref.within(y, *wante["y"], "y over its residual")
+    dx = res.clone()
+    op.backward(dy, x, wgu, wd, residual=dx, dx=dx)
+    check({"dx": dx, "dw_gate_up": op.dw_gate_up, "dw_down": op.dw_down}, want, ("dx", "dw_gate_up", "dw_down"), "in place")
+    for t in (op.h, op.gu, op.dgu):
+        assert (t[T:] == 7).all()
+    assert (op.y == 7).all() and (op.dx == 7).all()
+
+
+def test_shared_ffn_of_nothing():
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    for dtype in ("bf16", "f32"):
+        _, wgu, wd, _, _ = ffn_case(1, 72, 40, dtype)
+        op = SharedFFN(4, 72, 40, dtype)
+        none = torch.empty(0, 72, device="cuda", dtype=DT[dtype])
+        op.dw_gate_up.fill_(3.0)
+        op.dw_down.fill_(3.0)
+        assert op.forward(none, wgu, wd).shape == (0, 72)
+        op.backward(none, none, wgu, wd)
+        assert (op.dw_gate_up == 0).all() and (op.dw_down == 0).all()
+
+
+@pytest.mark.parametrize("T,dtype", [(1, "bf16"), (20, "bf16"), (150, "bf16"), (30, "f32")])
+def test_shared_ffn_bad_tokens_stay_in_their_rows(T, dtype):
+    """A token of NaN changes no other token's output, nor what lies in buffers that no row of this call owns."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, _ = ffn_case(T, 136, 200, dtype, seed=3)
+    op = SharedFFN(T, 136, 200, dtype)
+    if op.workspace is not None:
+        op.workspace.fill_(255)  # NaN patterns
+    y = op.forward(x, wgu, wd, residual=res).clone()
+    assert torch.isfinite(y).all()
+    if T > 1:
+        x[T // 2] = float("nan")
+        z = op.forward(x, wgu, wd, residual=res)
+        keep = torch.arange(T, device="cuda") != T // 2
+        assert torch.equal(z[keep], y[keep]) and torch.isnan(z[T // 2]).all()
+
+
+def test_shared_ffn_gradients_against_differences():
+    """f32: the backward call against central differences of the forward call, in a few directions.  With a step of 2^-7 the
+    difference's own error is the third derivative's 2^-14 / 6 of the loss' size along unit directions, and the forward's
+    rounding (2^-22 of the loss' terms) over the step: 2^-12 of the loss' terms together bounds both."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    T, d, f = 37, 48, 56
+    x, wgu, wd, _, dy = ffn_case(T, d, f, "f32", seed=4)
+    op = SharedFFN(T, d, f, "f32")
+    op.forward(x, wgu, wd)
+    grads = (op.backward(dy, x, wgu, wd).clone(), op.dw_gate_up.clone(), op.dw_down.clone())
+    terms = (op.forward(x, wgu, wd).double() * dy.double()).norm().item()
+    rnd, h = gen(9), 2.0 ** -7
+    for k, grad in enumerate(grads):
+        v = rnd(*grad.shape)
+        v = v / v.norm()
+        at = [[x, wgu, wd], [x, wgu, wd]]
+        at[0][k], at[1][k] = at[0][k] + h * v, at[1][k] - h * v
+        up, down = ((op.forward(*a).double() * dy.double()).sum().item() for a in at)
+        want = (up - down) / (2 * h)
+        assert abs((grad.double() * v.double()).sum().item() - want) <= 2.0 ** -12 * (terms + abs(want)) , k
+
+
+# ---- AdamW -------------------------------------------------------------------------------------------------------
+
+def adam_tensors(sizes, bits, params, grads, seed=0, values=True):
+    """Tensors in odd places of shared buffers; steps of very different sizes."""
+    from expert_output_overlap_amd.runtime import AdamW
+
+    rnd = gen(3000 + seed)
+    got = []
+    for i, n in enumerate(sizes):
+        def at(dtype, shift):  # an address that is aligned to its elements only
+            return torch.zeros(n + 8, device="cuda", dtype=dtype)[shift: shift + n]
+
+        size = 1e-3 * torch.exp(2 * rnd(n))
+        t = {"p": at(torch.bfloat16 if params == "bf16" else torch.float32, i % 3), "g": at(DT[grads], i % 2)}
+        t["p"].copy_(rnd(n))
+        t["g"].copy_(rnd(n) * size)
+        if params == "master":
+            t["copy"] = at(torch.bfloat16, i % 5)
+        t.update(AdamW.states(t["p"], bits))
+        if bits == 32:
+            t["m"].copy_(rnd(n) * size)
+            t["v"].copy_((size * (0.5 + rnd(n).abs())) ** 2)
+        elif values:
+            t["m_values"], t["root_values"] = at(torch.bfloat16, 1), at(torch.bfloat16, 2)
+        t["weight_decay"], t["lr_scale"] = 0.1 * (i % 2), 1.0 - 0.25 * (i % 3)
+        got.append(t)
+    return got
+
+
+HYPER = dict(lr=1e-3, betas=(0.9, 0.95), eps=1e-8)
+
+
+def adam_want(t, step, scale=1.0, lr=1e-3):
+    D = torch.float64
+    if t["m"].dtype is torch.uint8:
+        m, v = ref.m_values(t["m"], t["m_scale"]), ref.root_values(t["v"], t["v_scale"]).square()
+    else:
+        m, v = t["m"].to(D), t["v"].to(D)
+    return ref.adamw(t["p"].reshape(-1).to(D), t["g"].reshape(-1).to(D), m, v, step, lr * t["lr_scale"], *HYPER["betas"], HYPER["eps"],
+                     t["weight_decay"], scale)
+
+
+def on_codes(value, scale, bits, low, most, floor, e, what, want):
+    """8-bit values: half a step of their code's binade off the 64-bit state at most (or up to the smallest code), and the
+    scale the smallest at which the block fits."""
+    n = want.numel()
+    s = ref.power(scale.long() - 127).repeat_interleave(ref.BLOCK)[:n]
+    z = want.abs() / s
+    # a value that rounds up across a binade is half a step of the lower one off at most, so the binade of z counts
+    step = 2.0 ** (torch.floor(torch.log2(z.clamp(min=1e-300))).clamp(min=low) - bits)
+    bound = s * step / 2 + e
+    if floor:
+        bound = torch.where((z > 0) & (z < 2.0 ** low * (1 + 2.0 ** -bits)), s * 2.0 ** low * (1 + 2.0 ** -bits), bound)
+    ref.within(value, want, bound, what)
+    if n:
+        pad = torch.zeros(-n % ref.BLOCK, device="cuda", dtype=torch.float64)
+        top = torch.cat([z, pad]).view(-1, ref.BLOCK).amax(1)
+        assert (top <= most * (1 + 2.0 ** -20)).all(), what
+        least = 16 if floor else 1
+        assert ((top > most / 2 * (1 - 2.0 ** -20)) | (scale == least)).all(), what
+
+
+SIZES = [1, 0, 31, 32, 33, 4096, 4097, 1000, 5, 12289, 64, 100003]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("params,grads", [("master", "f32"), ("f32", "bf16"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_adamw(bits, params, grads):
+    from expert_output_overlap_amd.runtime import AdamW
+
+    ts = adam_tensors(SIZES, bits, params, grads)
+    op = AdamW(ts, betas=HYPER["betas"], eps=HYPER["eps"])
+    clip = torch.tensor([0.37], device="cuda")
+    for step in (1, 2, 3):
+        scale = 1.0 if step == 1 else float(clip)
+        want = [adam_want(t, step, scale) for t in ts]
+        op.step(step, HYPER["lr"], grad_scale=None if step == 1 else clip)
+        op.read_states()
+        for t, ((p, ep), (m, em), (v, ev)) in zip(ts, want):
+            tag = (bits, params, grads, step, p.numel())
+            ref.within(t["p"], p, ep + ref.half_step(t["p"].dtype) * p.abs(), tag + ("p",))
+            if "copy" in t:
+                assert torch.equal(t["copy"], t["p"].bfloat16()), tag
+            if bits == 32:
+                ref.within(t["m"], m, em, tag + ("m",))
+                ref.within(t["v"], v, ev, tag + ("v",))
+                continue
+            mv, rv = ref.m_values(t["m"], t["m_scale"]), ref.root_values(t["v"], t["v_scale"])
+            assert torch.equal(t["m_values"].double(), mv) and torch.equal(t["root_values"].double(), rv), tag
+            on_codes(mv, t["m_scale"], 3, -6, 448.0, False, em, tag + ("m",), m)
+            on_codes(rv, t["v_scale"], 4, -15, 1.875, True, v.sqrt() * 6 * ref.E32, tag + ("root",), v.sqrt())
+            assert ((t["v"] > 0) == (v > 0)).all(), tag  # no divisor becomes zero
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_values_that_are_not_finite(bits):
+    """They stay where they are: the other elements of their tensor and of their block go on as without them."""
+    from expert_output_overlap_amd.runtime import AdamW
+
+    a = adam_tensors([200], bits, "f32", "f32", seed=1, values=False)[0]
+    bad = [3, 40, 41]
+    for k in ("g",) if bits == 8 else ("g", "m", "v"):
+        a[k][bad] = 0.0
+    b = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in a.items()}
+    b["g"][bad] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda")
+    ok = torch.ones(200, dtype=torch.bool, device="cuda")
+    ok[bad] = False
+    opa, opb = AdamW([a], betas=HYPER["betas"]), AdamW([b], betas=HYPER["betas"])
+    for step in (1, 2):
+        opa.step(step, 1e-3)
+        opb.step(step, 1e-3)
+        assert torch.isnan(b["p"][bad]).all()
+        for k in ("p", "m", "v"):
+            assert torch.equal(a[k][ok], b[k][ok]), k
+        if bits == 8:
+            assert ((b["m"][bad] & 0x7F) == 0x7F).all() and (b["v"][bad] == 255).all()
+            assert torch.equal(a["m_scale"], b["m_scale"]) and torch.equal(a["v_scale"], b["v_scale"])
+
+
+def test_adamw_step_from_the_device():
+    """Step and rate from device numbers give the same parameters as from the host, also for a step near 1 and beta2 near 1
+    (up to the rounding of 1 - beta^t, the same formula on both sides: one step of it in the update)."""
+    from expert_output_overlap_amd.runtime import AdamW
+
+    for step in (1, 7, 100000):
+        ts = [adam_tensors([5000], 32, "f32", "f32", seed=2)[0] for _ in range(2)]
+        ops = [AdamW([t], betas=(0.9, 0.9999)) for t in ts]
+        before = ts[0]["p"].double()
+        ops[0].step(step, 3e-4)
+        ops[1].step(torch.tensor([step], device="cuda"), torch.tensor([3e-4], device="cuda"))
+        up = (ts[0]["p"].double() - before).abs()
+        ref.within(ts[1]["p"], ts[0]["p"].double(), 6 * ref.E32 * up + 2 * ref.E32 * ts[0]["p"].double().abs(), step)
+        assert torch.equal(ts[0]["m"], ts[1]["m"]) and torch.equal(ts[0]["v"], ts[1]["v"])
+
+
+# ---- streams, graphs, all of them together -----------------------------------------------------------------------
+
+def test_captured_and_replayed():
+    """Every operator captured into one graph; each replay after new inputs equals the eager calls, with eager work between."""
+    from expert_output_overlap_amd.runtime import AdamW, LayerNorm, SharedFFN
+
+    T, d, f = 70, 264, 200
+    x, wgu, wd, res, dy = ffn_case(T, d, f, "bf16", seed=5)
+    w = torch.ones(d, device="cuda")
+
+    def make():
+        norm, ffn = LayerNorm(T, d), SharedFFN(T, d, f)
+        p = wgu.float().clone()
+        t = {"p": p, "g": ffn.dw_gate_up, "copy": torch.empty_like(wgu), **AdamW.states(p, 8)}
+        t["m_values"], t["root_values"] = (torch.zeros(p.numel(), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        opt = AdamW([t])
+        step, lr = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.full((1,), 1e-3, device="cuda")
+        out = {}
+
+        def run():
+            n = norm.forward(x, w)
+            out["y"] = ffn.forward(n, wgu, wd, residual=res)
+            out["dn"] = ffn.backward(dy, n, wgu, wd)
+            out["dx"] = norm.backward(out["dn"], x, w, residual=dy)
+            step.add_(1)
+            opt.step(step, lr)
+            opt.read_states()
+            out.update(p=p, copy=t["copy"], m=t["m_values"], r=t["root_values"], dw=ffn.dw_down, dweight=norm.dweight)
+
+        return run, out
+
+    make()[0]()
+    torch.cuda.synchronize()
+    eager, want = make()
+    captured, got = make()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        captured()
+    rnd = gen(6)
+    for _ in range(4):
+        x.copy_(rnd(T, d))
+        dy.copy_(rnd(T, d))
+        torch.cuda.synchronize()
+        graph.replay()
+        eager()
+        torch.cuda.synchronize()
+        for k in want:
+            assert torch.equal(want[k], got[k]), k
+
+
+def test_two_streams_at_once():
+    """Two sets of operators on two streams at the same time give what each gives alone."""
+    from expert_output_overlap_amd.runtime import LayerNorm, SharedFFN
+
+    sets = []
+    for k, (T, d, f) in enumerate([(300, 512, 768), (5, 2048, 1408)]):
+        x, wgu, wd, res, dy = ffn_case(T, d, f, "bf16", seed=7 + k)
+        norm, ffn, w = LayerNorm(T, d), SharedFFN(T, d, f), torch.ones(d, device="cuda")
+
+        def run(stream=None, x=x, wgu=wgu, wd=wd, dy=dy, norm=norm, ffn=ffn, w=w):
+            n = norm.forward(x, w, stream=stream)
+            ffn.forward(n, wgu, wd, stream=stream)
+            dn = ffn.backward(dy, n, wgu, wd, stream=stream)
+            return [ffn.y, norm.backward(dn, x, w, stream=stream), ffn.dw_gate_up, ffn.dw_down, norm.dweight]
+
+        sets.append((run, [t.clone() for t in run()], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(stream) for run, _, stream in sets]
+        torch.cuda.synchronize()
+        for g, (_, want, _) in zip(got, sets):
+            assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+def test_block_together():
+    """Two training steps of a pre-norm MoE block: norm, router, routed experts, combine, shared expert, their backward and
+    AdamW in 32 and in 8 bits, against float64 autograd.  Each result has passed at most eight roundings to bf16 in a row
+    (n, h, y, combine, sum; dy, dgu, dx, sums), each 2^-8 at most and of random sign: 8 x 2^-8 of its norm."""
+    from expert_output_overlap_amd.runtime import AdamW, MoeBlock, MoePath
+
+    R, T_o, G, k, d, f, fs, M = 2, 40, 4, 2, 128, 128, 192, 16
+    T, D = R * T_o, torch.float64
+    rnd = gen(11)
+    w = {"norm_weight": 1 + 0.1 * rnd(d), "norm_bias": 0.1 * rnd(d), "w_gate_up": (rnd(G, 2 * f, d) / d ** 0.5).bfloat16(),
+         "w_down": (rnd(G, d, f) / d ** 0.5).bfloat16(), "shared_gate_up": (rnd(2 * fs, d) / d ** 0.5).bfloat16(),
+         "shared_down": (rnd(d, fs) / d ** 0.5).bfloat16()}
+    router = rnd(G, d) / d ** 0.5
+    block = MoeBlock(MoePath(R, T_o, G, G, k, d, f, M), fs)
+    ffn, norm, bb = block.shared, block.norm_op, block.path.bwd_buffers()
+    grads = {"norm_weight": norm.dweight, "norm_bias": norm.dbias, "w_gate_up": bb["dw_gate_up"], "w_down": bb["dw_down"],
+             "shared_gate_up": ffn.dw_gate_up, "shared_down": ffn.dw_down}
+    master = {n: t.float().clone() for n, t in w.items()}
+    tensors = []
+    for n, t in w.items():
+        q = {"p": master[n], "g": grads[n], **AdamW.states(t, 8 if t.dim() > 1 else 32)}
+        q["weight_decay"] = 0.1 if t.dim() > 1 else 0.0
+        if t.dtype is torch.bfloat16:
+            q["copy"] = t
+        tensors.append(q)
+    opt = AdamW(tensors)
+    for step in (1, 2):
+        x, d_out = rnd(T, d).bfloat16(), rnd(T, d).bfloat16()
+        leaf = {n: t.to(D).requires_grad_() for n, t in w.items()}
+        xl = x.to(D).requires_grad_()
+        # the framework
+        n = block.norm(x, w)
+        logits = n.float() @ router.T
+        out = block.experts(logits, w).clone()
+        idx, wt = block.path.topk_idx.long(), block.path.topk_w.to(D)
+        dn = block.experts_backward(d_out, w)
+        dx = block.norm_backward(dn, x, w, residual=d_out)
+        # float64, the routing as it is
+        mu = xl.mean(1, keepdim=True)
+        nl = (xl - mu) / ((xl - mu).square().mean(1, keepdim=True) + 1e-5).sqrt() * leaf["norm_weight"] + leaf["norm_bias"]
+
+        def mlp(rows, gu, down):
+            a = rows @ gu.T
+            h = gu.shape[0] // 2
+            return (torch.nn.functional.silu(a[:, :h]) * a[:, h:]) @ down.T
+
+        want = mlp(nl, leaf["shared_gate_up"], leaf["shared_down"])
+        for e in range(G):
+            we = (wt * (idx == e)).sum(1, keepdim=True)
+            want = want + we * mlp(nl, leaf["w_gate_up"][e], leaf["w_down"][e])
+        (want * d_out.to(D)).sum().backward()
+        pairs = [("out", out, want.detach()), ("dx", dx, xl.grad + d_out.to(D))]
+        pairs += [(name, grads[name].view(t.shape), leaf[name].grad) for name, t in w.items()]
+        for name, got, exp in pairs:
+            assert (got.to(D) - exp).norm() <= 8 * 2.0 ** -8 * exp.norm(), (step, name)
+        before = {name: t.clone() for name, t in master.items()}
+        moved = [adam_want({**q, "lr_scale": 1.0}, step) for q in tensors]
+        opt.step(step, 1e-3)
+        for (name, t), ((p, ep), _, _) in zip(master.items(), moved):
+            assert not torch.equal(t, before[name])
+            ref.within(t.view(-1), p, ep + ref.E32 * p.abs(), (step, name))
+            if w[name].dtype is torch.bfloat16:
+                assert torch.equal(w[name], t.bfloat16())
+            else:
+                w[name].copy_(t)
+    assert block.path.status() == B.MOE_OK
