@@ -48,6 +48,357 @@ __device__ __forceinline__ void dglu(float dh, float g, float u, float* dg, floa
   *du = dh * g * s;
 }
 
+// ---- bf16 tiles ------------------------------------------------------------------------------------------------------
+// A BM x BN tile of C by WM x WN waves, in k-tiles of 64 that LDS-DMA loads bring from global memory into two LDS stages,
+// with 32x32x16 products.  An operand by rows is staged as rows of 64 k (16-byte chunk c of row r at slot c ^ swz(r), so
+// that the lanes of a fragment read spread over the banks), one by columns as 64 k-rows, read with the LDS transpose read
+// (lane addresses as in bwd.hip; 32-byte granule g of k-row r at granule swz_col(g, r)).  A k-tile is four k-steps; the
+// fragments of step s + 1 are read during step s, and one barrier per k-tile, between steps 2 and 3, frees its stage and
+// makes the next k-tile's visible: the loads of A for two k-tiles ahead go out in step 3, those of B in step 0.
+// Rows and columns past the matrix read row or column 0 and are not stored; k past K reads k 0 of its k-tile, and the last
+// k-tile's rest is zeroed in LDS, in both operands, before it is read.
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+
+__device__ __forceinline__ int swz_col(int g, int r) {
+  const int x = g & 7;
+  return (g & 8) | ((((x & 1) << 2) | (x >> 1)) ^ (r & 3));
+}
+__device__ __forceinline__ int unswz_col(int p, int r) {
+  const int y = (p & 7) ^ (r & 3);
+  return (p & 8) | (((y & 3) << 1) | (y >> 2));
+}
+
+// 4 columns of one row, any alignment; n: how many of them are inside the matrix
+__device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n) {
+  const u32x2_t q = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+  if (n >= 4) __builtin_memcpy(p, &q, 8);
+  else
+    for (int i = 0; i < n; ++i) p[i] = (bf16_t)(q[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ f32x4_t load4(const bf16_t* p, int n) {
+  u32x2_t q = {0, 0};
+  if (n >= 4) __builtin_memcpy(&q, p, 8);
+  else
+    for (int i = 0; i < n; ++i) q[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  return f32x4_t{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u), __uint_as_float(q[1] << 16),
+                 __uint_as_float(q[1] & 0xffff0000u)};
+}
+
+// Four neighbouring columns n .. of row m through the epilogue (sum2: GLU's up sums); columns past N: cut
+template <int EPI>
+__device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t sum, f32x4_t sum2) {
+  const int in = p.N - n;
+  if (EPI == EPI_GLU) {
+    f32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = silu_fast(sum[i]) * sum2[i];
+    store4((bf16_t*)p.c + m * p.ldc + n, h, 4);  // rows are padded to whole fours
+    if (p.gu) {
+      float* o = p.gu + m * p.ldgu + n;
+      *(f32x4_t*)o = sum;
+      *(f32x4_t*)(o + p.half) = sum2;
+    }
+  } else if (EPI == EPI_DGLU) {
+    const float* i = p.gu + m * p.ldgu + n;
+    const f32x4_t g = *(const f32x4_t*)i, u = *(const f32x4_t*)(i + p.half);
+    f32x4_t dg, du;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[k]));
+      dg[k] = sum[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
+      du[k] = sum[k] * g[k] * s;
+    }
+    bf16_t* o = (bf16_t*)p.c + m * p.ldc + n;
+    store4(o, dg, 4);
+    store4(o + p.half, du, 4);
+  } else {
+    bf16_t* o = (bf16_t*)p.c + m * p.ldc + n;
+    if (p.residual) sum += load4((const bf16_t*)p.residual + m * p.ldc + n, in);
+    store4(o, sum, in);
+  }
+}
+
+template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+struct Tile {
+  static constexpr int NW = WM * WN, THREADS = NW * 64, MI = BM / WM / 32, NI = BN / WN / 32;
+  static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
+  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads per wave and k-tile
+  static constexpr int COLS = EPI == EPI_GLU ? BN / 2 : BN;  // columns of C
+  static_assert(EPI != EPI_GLU || (NI == 2 && !BCOL), "a wave holds the gate's and the up projection's same 32 columns");
+
+  template <int C>
+  static __device__ __forceinline__ bf16x8_t frag_col(const unsigned char* st, int cb, int ks, int lane) {
+    const int gi = lane >> 4, j = lane & 15;
+    const int n = cb + 16 * (gi & 1) + 4 * (j & 3);
+    s16x4_t v[2];
+#pragma unroll
+    for (int hk = 0; hk < 2; ++hk) {
+      const int k = 16 * ks + 8 * (gi >> 1) + 4 * hk + (j >> 2);
+      const unsigned char* p = st + k * (2 * C) + ((swz_col(n >> 4, k) << 5) | ((n & 15) << 1));
+      v[hk] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)p);
+    }
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  static __device__ __forceinline__ bf16x8_t frag_row(const unsigned char* st, int rb, int ks, int lane) {
+    const int swz = (lane & 7) ^ ((lane >> 3) & 1);
+    return __builtin_bit_cast(bf16x8_t,
+                              *(const u32x4_t*)(st + (rb + (lane & 31)) * 128 + (((2 * ks + (lane >> 5)) ^ swz) << 4)));
+  }
+
+  // Rows m0 .., columns n0 .., k-tiles [t0, t0 + nk) (nk >= 1) of the product; partial: where the sums go as they are
+  // ([M][ld_partial] fp32, GLU: up sums from column ld_partial / 2 on), or null: through the epilogue
+  static __device__ __forceinline__ void run(const Gemm& p, unsigned char* smem, int m0, int n0, int t0, int nk,
+                                             float* partial, int64_t ld_partial) {
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int cnt = p.K - (t0 + nk - 1) * 64;  // k in the last k-tile; under 64: its rest is zeroed
+
+    // a lane's offset in each of its loads, from a base that moves with the k-tile; tail: what of it is its k
+    uint32_t aoff[LA], boff[LB];
+    const uint32_t lda = (uint32_t)p.lda * 2, ldb = (uint32_t)p.ldb * 2;
+    auto row_k = [&](int q) { return (uint32_t)(((lane & 7) ^ (lane >> 3) ^ (q & 1)) << 4); };  // by rows: 16-byte chunk
+    auto col_k = [&](int q, int C) { return q * (512 / C) + lane / (C / 8); };                   // by columns: k-row
+    auto col_c = [&](int q, int C) {                                                            // .. and 8-column chunk
+      const int cs = lane & (C / 8 - 1);
+      return (unswz_col(cs >> 1, col_k(q, C)) << 1) | (cs & 1);
+    };
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+      const int q = wave * LA + j;
+      if (ACOL) {
+        int c = m0 + 8 * col_c(q, BM);
+        c = c < p.M ? c : 0;
+        aoff[j] = (uint32_t)col_k(q, BM) * lda + (uint32_t)(c + (c >= p.a_seg ? p.a_jump : 0)) * 2;
+      } else {
+        const int r = 8 * q + (lane >> 3);
+        aoff[j] = (uint32_t)(m0 + r < p.M ? r : 0) * lda + row_k(q);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+      const int q = wave * LB + j;
+      if (BCOL) {
+        const int c = n0 + 8 * col_c(q, BN);
+        boff[j] = (uint32_t)col_k(q, BN) * ldb + (uint32_t)(c < p.N ? c : 0) * 2;
+      } else {
+        const int r = (8 * q + (lane >> 3)) & (COLS - 1);  // GLU: gate rows, then up rows, whose base lies further on
+        boff[j] = (uint32_t)(n0 + r < p.N ? r : 0) * ldb + row_k(q);
+      }
+    }
+    const unsigned char* abase = (const unsigned char*)p.a + (ACOL ? (int64_t)t0 * 64 * lda : (int64_t)m0 * lda + (int64_t)t0 * 128);
+    const unsigned char* bbase = (const unsigned char*)p.b + (BCOL ? (int64_t)t0 * 64 * ldb : (int64_t)n0 * ldb + (int64_t)t0 * 128);
+    const int64_t astep = ACOL ? (int64_t)64 * lda : 128, bstep = BCOL ? (int64_t)64 * ldb : 128;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
+
+    auto load = [&](int kt, int u) {  // load u of k-tile kt: A's, then B's
+      const bool tail = kt == nk - 1 && cnt < 64;
+      const uint32_t st = lds0 + (kt & 1) * STAGE;
+      if (u < LA) {
+        const int q = wave * LA + u;
+        uint32_t o = aoff[u];
+        if (tail) {
+          if (ACOL) o -= col_k(q, BM) < cnt ? 0 : (uint32_t)col_k(q, BM) * lda;
+          else o -= (int)row_k(q) < 2 * cnt ? 0 : row_k(q);
+        }
+        dma16(abase + kt * astep, o, st + q * 1024);
+      } else {
+        const int q = wave * LB + u - LA;
+        uint32_t o = boff[u - LA];
+        if (tail) {
+          if (BCOL) o -= col_k(q, BN) < cnt ? 0 : (uint32_t)col_k(q, BN) * ldb;
+          else o -= (int)row_k(q) < 2 * cnt ? 0 : row_k(q);
+        }
+        const int64_t further = EPI == EPI_GLU && 8 * q >= COLS ? (int64_t)p.up * ldb : 0;
+        dma16(bbase + kt * bstep + further, o, st + A_BYTES + q * 1024);
+      }
+    };
+    auto zero_rest = [&](int kt) {  // after the barrier that made k-tile kt visible
+      if (kt != nk - 1 || cnt >= 64) return;
+      unsigned char* st = smem + (kt & 1) * STAGE;
+      auto clear = [&](unsigned char* o, int R, bool col) {
+        for (int i = tid; i < R * 8; i += THREADS) {  // 16-byte pieces: by rows row i / 8, chunk i % 8; by columns in order
+          const int r = i >> 3, c = i & 7, k = col ? i / (R / 8) : c * 8;
+          const int at = col ? i * 16 : r * 128 + ((c ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
+          if (k >= cnt) *(u32x4_t*)(o + at) = u32x4_t{0u, 0u, 0u, 0u};
+        }
+      };
+      clear(st, BM, ACOL);
+      clear(st + A_BYTES, BN, BCOL);
+      __syncthreads();
+    };
+
+    f32x16_t acc[MI][NI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.f;
+    bf16x8_t fa[2][MI], fb[2][NI];
+    auto frag = [&](int kt, int ks, int i, bf16x8_t* A_, bf16x8_t* B_) {
+      const unsigned char* sa = smem + (kt & 1) * STAGE;
+      if (i < MI) {
+        const int rb = (wm * MI + i) * 32;
+        A_[i] = ACOL ? frag_col<BM>(sa, rb, ks, lane) : frag_row(sa, rb, ks, lane);
+      } else {
+        const int ni = i - MI, rb = EPI == EPI_GLU ? ni * COLS + wn * 32 : (wn * NI + ni) * 32;
+        B_[ni] = BCOL ? frag_col<BN>(sa + A_BYTES, rb, ks, lane) : frag_row(sa + A_BYTES, rb, ks, lane);
+      }
+    };
+    // one k-step: its products, with the next step's fragment reads in the first RS slots and the loads after them.  M1,
+    // M2: there is a next k-tile, and one after it
+    constexpr int NSLOT = MI * NI, RS = 2, RPS = (MI + NI + RS - 1) / RS;
+    constexpr int DA = (LA + NSLOT - RS - 1) / (NSLOT - RS > 0 ? NSLOT - RS : 1), DB = (LB + NSLOT - RS - 1) / (NSLOT - RS > 0 ? NSLOT - RS : 1);
+    auto step = [&](auto ks_tag, auto m1_tag, auto m2_tag, int kt) {
+      constexpr int ks = decltype(ks_tag)::value, c = ks & 1;
+      constexpr bool M1 = decltype(m1_tag)::value, M2 = decltype(m2_tag)::value;
+#pragma unroll
+      for (int i = 0; i < NSLOT; ++i) {
+        const int mi = i / NI, ni = i % NI;
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[c][mi], fb[c][ni], acc[mi][ni], 0, 0, 0);
+        if (i < RS) {
+#pragma unroll
+          for (int r = i * RPS; r < (i + 1) * RPS && r < MI + NI; ++r) {
+            if (ks < 3) frag(kt, ks + 1, r, fa[c ^ 1], fb[c ^ 1]);
+            else if (M1) frag(kt + 1, 0, r, fa[c ^ 1], fb[c ^ 1]);
+          }
+        }
+        if (i >= RS || NSLOT <= RS) {
+          const int k = NSLOT <= RS ? i : i - RS;
+          if (ks == 3 && M2) {
+#pragma unroll
+            for (int v = k * DA; v < (k + 1) * DA && v < LA; ++v) load(kt + 2, v);
+          }
+          if (ks == 0 && M1) {
+#pragma unroll
+            for (int v = k * DB; v < (k + 1) * DB && v < LB; ++v) load(kt + 1, LA + v);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (ks == 2) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (M1 && !M2) zero_rest(kt + 1);
+      }
+    };
+    auto ktile = [&](auto m1, auto m2, int kt) {
+      step(std::integral_constant<int, 0>{}, m1, m2, kt);
+      step(std::integral_constant<int, 1>{}, m1, m2, kt);
+      step(std::integral_constant<int, 2>{}, m1, m2, kt);
+      step(std::integral_constant<int, 3>{}, m1, m2, kt);
+    };
+#pragma unroll
+    for (int u = 0; u < LA + LB; ++u) load(0, u);
+    wait_loads_barrier();
+    if (nk == 1) zero_rest(0);
+#pragma unroll
+    for (int i = 0; i < MI + NI; ++i) frag(0, 0, i, fa[0], fb[0]);
+    if (nk > 1) {
+#pragma unroll
+      for (int u = 0; u < LA; ++u) load(1, u);
+    }
+    int kt = 0;
+    for (; kt + 2 < nk; ++kt) ktile(std::true_type{}, std::true_type{}, kt);
+    if (kt + 1 < nk) {
+      ktile(std::true_type{}, std::false_type{}, kt);
+      ++kt;
+    }
+    ktile(std::false_type{}, std::false_type{}, kt);
+
+    // element q of accumulator (mi, ni): row 8 (q / 4) + 4 (lane / 32) + q % 4 of its block, column lane % 32; each group of
+    // four q is transposed inside its quad of lanes, after which a lane holds four neighbouring columns of one row
+    auto quad = [&](const f32x16_t& v, int q4) {
+      return quad_transpose(f32x4_t{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]}, lane);
+    };
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4) {
+        const int m = m0 + (wm * MI + mi) * 32 + 8 * q4 + 4 * (lane >> 5) + (lane & 3);
+#pragma unroll
+        for (int ni = 0; ni < (EPI == EPI_GLU ? 1 : NI); ++ni) {
+          const int n = n0 + (EPI == EPI_GLU ? wn * 32 : (wn * NI + ni) * 32) + 4 * ((lane & 31) >> 2);
+          const f32x4_t v = quad(acc[mi][ni], q4);
+          const f32x4_t w = EPI == EPI_GLU ? quad(acc[mi][1], q4) : v;
+          if (m >= p.M || n >= p.N) continue;
+          if (partial) {
+            float* o = partial + (int64_t)m * ld_partial + n;
+            *(f32x4_t*)o = v;
+            if (EPI == EPI_GLU) *(f32x4_t*)(o + ld_partial / 2) = w;
+          } else finish4<EPI>(p, m, n, v, w);
+        }
+      }
+  }
+};
+
+// One workgroup per tile and k-split.  Workgroups go round the eight XCDs, so a run of 1/8 of the grid's tiles is one
+// XCD's, whose L2 its tiles share: bands of eight tile rows, walked column by column.
+template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bf16(Gemm p, int splits, float* partial, int64_t ld_partial) {
+  using G = Tile<BM, BN, WM, WN, ACOL, BCOL, EPI>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int mt = (p.M + BM - 1) / BM, nt = (p.N + G::COLS - 1) / G::COLS, nkt = (p.K + 63) / 64;
+  const int tiles = mt * nt, n = tiles * splits;
+  int i = blockIdx.x;
+  {  // position among the launch's tiles: XCD x takes [x n / 8, (x + 1) n / 8), rounded so that each is taken once
+    const int x = i & 7, per = n >> 3, more = n & 7;
+    i = x * per + (x < more ? x : more) + (i >> 3);
+  }
+  const int s = i / tiles;
+  i -= s * tiles;
+  const int band = i / (8 * nt), rows = min(8, mt - band * 8), r = i - band * 8 * nt;
+  const int t0 = (int)((int64_t)nkt * s / splits), t1 = (int)((int64_t)nkt * (s + 1) / splits);
+  G::run(p, smem, (band * 8 + r % rows) * BM, (r / rows) * G::COLS, t0, t1 - t0,
+         partial ? partial + (int64_t)s * p.M * ld_partial : nullptr, ld_partial);
+}
+
+// The k-splits' sums, in split order, through the epilogue: four columns per thread.
+template <int EPI>
+__global__ __launch_bounds__(256) void k_gemm_finish(Gemm p, int splits, const float* __restrict__ partial, int64_t ld) {
+  const int quads = (p.N + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / quads;
+  if (m >= p.M) return;
+  const int n = (int)(i - m * quads) * 4;
+  const float* o = partial + m * ld + n;
+  f32x4_t v = {0, 0, 0, 0}, w = {0, 0, 0, 0};
+  for (int s = 0; s < splits; ++s, o += p.M * ld) {
+    v += *(const f32x4_t*)o;
+    if (EPI == EPI_GLU) w += *(const f32x4_t*)(o + ld / 2);
+  }
+  finish4<EPI>(p, m, n, v, w);
+}
+
+// Columns of a partial sum's row
+int64_t partial_cols(const Gemm& p, int epi) { return (int64_t)(p.N + 3) / 4 * 4 * (epi == EPI_GLU ? 2 : 1); }
+
+template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+int gemm_tiles(const Gemm& p, int splits, float* partial, hipStream_t st) {
+  using G = Tile<BM, BN, WM, WN, ACOL, BCOL, EPI>;
+  const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + G::COLS - 1) / G::COLS) * splits;
+  if (tiles > 0x7fffffff) return -1;
+  const int64_t ld = partial_cols(p, EPI);
+  auto k = k_gemm_bf16<BM, BN, WM, WN, ACOL, BCOL, EPI>;
+  static const hipError_t once = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * G::STAGE);
+  if (once != hipSuccess) return -1;
+  hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(G::THREADS), 2 * G::STAGE, st, p, splits, splits > 1 ? partial : nullptr, ld);
+  if (splits > 1)
+    hipLaunchKernelGGL(k_gemm_finish<EPI>, dim3((unsigned)(((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256)), dim3(256), 0, st, p,
+                       splits, partial, ld);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <bool ACOL, bool BCOL, int EPI>
+int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
+  if (p.M == 0) return 0;
+  const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + (EPI == EPI_GLU ? 127 : 255)) / (EPI == EPI_GLU ? 128 : 256));
+  if (big >= 192) return gemm_tiles<256, 256, 2, 4, ACOL, BCOL, EPI>(p, 1, partial, st);
+  return gemm_tiles<128, 128, 2, 2, ACOL, BCOL, EPI>(p, 1, partial, st);
+}
+
 // ---- any sizes, any type: fp32 matrix instructions ------------------------------------------------------------------
 // A 128 x 64 tile of C (GLU: 32 columns of the gate and the same 32 of the up projection) by four waves of 32 x 64, in
 // k-tiles of 16: each operand's k-tile is loaded by elements of its own layout into registers one k-tile ahead, widened
@@ -240,10 +591,26 @@ int run_any(const SharedLaunch& s, hipStream_t st) {
   return gemm_any<T, EPI_STORE, true, true>(b.dw_down, st);
 }
 
+int run_bf16(const SharedLaunch& s, hipStream_t st) {
+  const Block b = block_of(s);
+  float* partial = nullptr;
+  int rc;
+  if (!s.backward) {
+    if ((rc = gemm_bf16<false, false, EPI_GLU>(b.glu, partial, st))) return rc;
+    return gemm_bf16<false, false, EPI_STORE>(b.down, partial, st);
+  }
+  if ((rc = gemm_bf16<false, true, EPI_DGLU>(b.dglu, partial, st))) return rc;
+  if ((rc = gemm_bf16<false, true, EPI_STORE>(b.dx, partial, st))) return rc;
+  if ((rc = gemm_bf16<true, true, EPI_STORE>(b.dw_gate_up, partial, st))) return rc;
+  return gemm_bf16<true, true, EPI_STORE>(b.dw_down, partial, st);
+}
+
 }  // namespace
 
 int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool backward) { return 0; }
 
 int launch_shared(const SharedLaunch& s, hipStream_t st) {
+  const bool aligned = s.d % 8 == 0 && s.f % 8 == 0;
+  if (s.dtype == MOE_BF16 && aligned && s.tokens > 0) return run_bf16(s, st);
   return s.dtype == MOE_BF16 ? run_any<bf16_t>(s, st) : run_any<float>(s, st);
 }
