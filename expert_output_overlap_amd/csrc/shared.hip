@@ -31,21 +31,223 @@ struct Gemm {
   int64_t ldgu;
   int half;  // GLU, DGLU: from a row's g to its u (and dg to du)
   int up;    // GLU: rows of B from the gate's to the up projection's
+  // STORE: rows of C from m_pad on stand m_pad - m_real earlier, those in [m_real, m_pad) nowhere (dg's padding)
+  int m_real, m_pad;
 };
-
-template <typename T>
-__device__ __forceinline__ float as_float(T v);
-template <>
-__device__ __forceinline__ float as_float(float v) { return v; }
-template <>
-__device__ __forceinline__ float as_float(bf16_t v) { return bf16_to_f32(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
 __device__ __forceinline__ void dglu(float dh, float g, float u, float* dg, float* du) {
   const float s = 1.0f / (1.0f + __expf(-g));
   *dg = dh * u * s * (1.0f + g * (1.0f - s));
   *du = dh * g * s;
+}
+
+// ---- epilogues ----
+// 4 columns of one row, any alignment; n: how many of them are inside the matrix
+__device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n) {
+  const u32x2_t q = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
+  if (n >= 4) __builtin_memcpy(p, &q, 8);
+  else
+    for (int i = 0; i < n; ++i) p[i] = (bf16_t)(q[i >> 1] >> (16 * (i & 1)));
+}
+__device__ __forceinline__ void store4(float* p, f32x4_t v, int n) {
+  if (n >= 4) __builtin_memcpy(p, &v, 16);
+  else
+    for (int i = 0; i < n; ++i) p[i] = v[i];
+}
+__device__ __forceinline__ f32x4_t load4(const bf16_t* p, int n) {
+  u32x2_t q = {0, 0};
+  if (n >= 4) __builtin_memcpy(&q, p, 8);
+  else
+    for (int i = 0; i < n; ++i) q[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  return f32x4_t{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u), __uint_as_float(q[1] << 16),
+                 __uint_as_float(q[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4_t load4(const float* p, int n) {
+  f32x4_t v = {0, 0, 0, 0};
+  if (n >= 4) __builtin_memcpy(&v, p, 16);
+  else
+    for (int i = 0; i < n; ++i) v[i] = p[i];
+  return v;
+}
+
+// 1 / (1 + exp(-g)).  bf16: with the hardware's reciprocal, 1 ulp off, in front of a rounding 2^15 times coarser
+template <typename T>
+__device__ __forceinline__ float sigmoid(float g) {
+  return sizeof(T) == 2 ? __builtin_amdgcn_rcpf(1.0f + __expf(-g)) : 1.0f / (1.0f + __expf(-g));
+}
+
+// Four neighbouring columns n .. of row m through the epilogue (sum2: GLU's up sums).  Columns past N are cut; h, gu and dgu
+// have whole fours in a row, where they become 0.
+template <typename T, int EPI>
+__device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t sum, f32x4_t sum2) {
+  const int in = p.N - n;
+  if (EPI == EPI_GLU) {
+    f32x4_t h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= in) sum[i] = sum2[i] = 0.f;
+      h[i] = sum[i] * sigmoid<T>(sum[i]) * sum2[i];
+    }
+    store4((T*)p.c + m * p.ldc + n, h, 4);
+    if (p.gu) {
+      float* o = p.gu + m * p.ldgu + n;
+      *(f32x4_t*)o = sum;
+      *(f32x4_t*)(o + p.half) = sum2;
+    }
+  } else if (EPI == EPI_DGLU) {
+    const float* i = p.gu + m * p.ldgu + n;
+    const f32x4_t g = *(const f32x4_t*)i, u = *(const f32x4_t*)(i + p.half);
+    f32x4_t dg, du;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float s = sigmoid<T>(g[k]);
+      dg[k] = k < in ? sum[k] * u[k] * s * (1.0f + g[k] * (1.0f - s)) : 0.f;
+      du[k] = k < in ? sum[k] * g[k] * s : 0.f;
+    }
+    T* o = (T*)p.c + m * p.ldc + n;
+    store4(o, dg, 4);
+    store4(o + p.half, du, 4);
+  } else {
+    if (m >= p.m_pad) m -= p.m_pad - p.m_real;
+    else if (m >= p.m_real) return;
+    T* o = (T*)p.c + m * p.ldc + n;
+    if (p.residual) sum += load4((const T*)p.residual + m * p.ldc + n, in);
+    store4(o, sum, in);
+  }
+}
+
+// ---- few tokens --------------------------------------------------------------------------------------------------------
+// Up to 32 tokens: the weights stream past once and bound the time.  A workgroup takes RT x 16 rows of the weights (GLU with
+// RT = 1: 8 of the gate's and the same 8 of the up projection's) as one operand of 16x16 products whose other is the tokens,
+// 16 per product; its eight waves share out the k in chunks of 128 bytes of each row and add their sums in wave order at the
+// end.  A lane holds 32 neighbouring bytes of its row per chunk; which k of a chunk meet in which product does not
+// matter as long as both operands agree, so the bytes go to the products as they were loaded: no LDS, no barrier before the
+// end.  SU chunks are in flight per wave.
+template <typename T>
+struct Chunk32 {  // 32 bytes of a row: 16 bf16 or 8 fp32
+  u32x4_t v[2];
+  static constexpr int N = 32 / sizeof(T);
+  __device__ __forceinline__ void load(const T* p, int n) {  // n elements are there, the rest 0
+    if (n >= N) {
+      __builtin_memcpy(v, p, 32);
+      return;
+    }
+    v[0] = v[1] = u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) {
+        if (sizeof(T) == 4) v[i / 4][i % 4] = *(const uint32_t*)(p + i);
+        else v[i / 8][i / 2 % 4] |= (uint32_t) * (const uint16_t*)(p + i) << (16 * (i & 1));
+      }
+  }
+};
+template <typename T>
+__device__ __forceinline__ f32x4_t products(const Chunk32<T>& a, const Chunk32<T>& b, f32x4_t c) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(T) == 2) {
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.v[h]), __builtin_bit_cast(bf16x8_t, b.v[h]), c,
+                                                  0, 0, 0);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.v[h][i]), __uint_as_float(b.v[h][i]), c, 0, 0, 0);
+    }
+  }
+  return c;
+}
+
+template <typename T, int EPI, int RT, int MT, int SU>
+__global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
+  constexpr int CH = 128 / sizeof(T), NW = 8;
+  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;  // columns of C
+  __shared__ f32x4_t part[NW][RT * MT][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * COLS, r = lane & 15, q = lane >> 4;
+  const T *w[RT], *x[MT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    int c = EPI == EPI_GLU ? n0 + (RT == 1 ? r & 7 : r) : n0 + 16 * t + r;
+    int64_t row = c < p.N ? c : 0;
+    if (EPI == EPI_GLU && (RT == 1 ? r >= 8 : t == 1)) row += p.up;
+    w[t] = (const T*)p.b + row * p.ldb + q * (32 / sizeof(T));
+  }
+#pragma unroll
+  for (int t = 0; t < MT; ++t) x[t] = (const T*)p.a + (int64_t)(16 * t + r < p.M ? 16 * t + r : 0) * p.lda + q * (32 / sizeof(T));
+  f32x4_t acc[RT][MT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int whole = p.K / CH;  // chunks that are full
+  auto chunks = [&](int c, auto count, bool cut) {  // chunks c, c + NW, ..
+    constexpr int U = decltype(count)::value;
+    Chunk32<T> a[U][RT], b[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = (c + u * NW) * CH, n = cut ? p.K - k - q * (int)(32 / sizeof(T)) : CH;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) a[u][t].load(w[t] + k, n);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) b[u][m].load(x[m] + k, n);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // every load goes out before the first product waits for one
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[t][m] = products(a[u][t], b[u][m], acc[t][m]);
+  };
+  int c = wave;
+  for (; c + (SU - 1) * NW < whole; c += SU * NW) chunks(c, std::integral_constant<int, SU>{}, false);
+  if (SU >= 4 && c + ((SU + 1) / 2 - 1) * NW < whole) {
+    chunks(c, std::integral_constant<int, (SU + 1) / 2>{}, false);
+    c += (SU + 1) / 2 * NW;
+  }
+  for (; c < whole; c += NW) chunks(c, std::integral_constant<int, 1>{}, false);
+  if (c == whole && p.K % CH) chunks(c, std::integral_constant<int, 1>{}, true);
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
+  __syncthreads();
+  // sums of a product's element: row 4 (lane / 16) .. + 3 of the weights, token lane % 16
+  auto sum = [&](int i, int l) {
+    f32x4_t v = part[0][i][l];
+#pragma unroll
+    for (int k = 1; k < NW; ++k) v += part[k][i][l];
+    return v;
+  };
+  if (EPI == EPI_GLU) {
+    constexpr int L = RT == 1 ? 32 : 64;
+    if (tid >= MT * L) return;
+    const int m = tid / L, l = tid % L, tok = 16 * m + (l & 15), n = n0 + 4 * (l >> 4);
+    if (tok >= p.M || n >= p.N) return;
+    finish4<T, EPI>(p, tok, n, sum(m, l), RT == 1 ? sum(m, l + 32) : sum(MT + m, l));
+  } else {
+    if (tid >= RT * MT * 64) return;
+    const int i = tid >> 6, t = i / MT, m = i % MT, tok = 16 * m + (lane & 15), n = n0 + 16 * t + 4 * (lane >> 4);
+    if (tok >= p.M || n >= p.N) return;
+    finish4<T, EPI>(p, tok, n, sum(i, lane), f32x4_t{0.f, 0.f, 0.f, 0.f});
+  }
+}
+
+template <typename T, int EPI, int RT, int MT, int SU>
+int few(const Gemm& p, hipStream_t st) {
+  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;
+  hipLaunchKernelGGL((k_gemm_few<T, EPI, RT, MT, SU>), dim3((unsigned)((p.N + COLS - 1) / COLS)), dim3(512), 0, st, p);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+// Tokens up to which the weights stream past (gemm_few).  7168 x 2048: 24 tokens 33 us, against 40 for 65 in tiles; 48 tokens
+// 51 us (three products of tokens per weight).
+constexpr int FEW = 32;
+
+template <typename T, int EPI>
+int gemm_few(const Gemm& p, hipStream_t st) {
+  if (p.M <= 16) return few<T, EPI, 1, 1, 4>(p, st);
+  return few<T, EPI, 1, 2, 2>(p, st);
 }
 
 // ---- bf16 tiles ------------------------------------------------------------------------------------------------------
@@ -69,63 +271,15 @@ __device__ __forceinline__ int unswz_col(int p, int r) {
   return (p & 8) | (((y & 3) << 1) | (y >> 2));
 }
 
-// 4 columns of one row, any alignment; n: how many of them are inside the matrix
-__device__ __forceinline__ void store4(bf16_t* p, f32x4_t v, int n) {
-  const u32x2_t q = {bf16_bits(v[0]) | (bf16_bits(v[1]) << 16), bf16_bits(v[2]) | (bf16_bits(v[3]) << 16)};
-  if (n >= 4) __builtin_memcpy(p, &q, 8);
-  else
-    for (int i = 0; i < n; ++i) p[i] = (bf16_t)(q[i >> 1] >> (16 * (i & 1)));
-}
-__device__ __forceinline__ f32x4_t load4(const bf16_t* p, int n) {
-  u32x2_t q = {0, 0};
-  if (n >= 4) __builtin_memcpy(&q, p, 8);
-  else
-    for (int i = 0; i < n; ++i) q[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  return f32x4_t{__uint_as_float(q[0] << 16), __uint_as_float(q[0] & 0xffff0000u), __uint_as_float(q[1] << 16),
-                 __uint_as_float(q[1] & 0xffff0000u)};
-}
-
-// Four neighbouring columns n .. of row m through the epilogue (sum2: GLU's up sums); columns past N: cut
-template <int EPI>
-__device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t sum, f32x4_t sum2) {
-  const int in = p.N - n;
-  if (EPI == EPI_GLU) {
-    f32x4_t h;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = silu_fast(sum[i]) * sum2[i];
-    store4((bf16_t*)p.c + m * p.ldc + n, h, 4);  // rows are padded to whole fours
-    if (p.gu) {
-      float* o = p.gu + m * p.ldgu + n;
-      *(f32x4_t*)o = sum;
-      *(f32x4_t*)(o + p.half) = sum2;
-    }
-  } else if (EPI == EPI_DGLU) {
-    const float* i = p.gu + m * p.ldgu + n;
-    const f32x4_t g = *(const f32x4_t*)i, u = *(const f32x4_t*)(i + p.half);
-    f32x4_t dg, du;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g[k]));
-      dg[k] = sum[k] * u[k] * s * (1.0f + g[k] * (1.0f - s));
-      du[k] = sum[k] * g[k] * s;
-    }
-    bf16_t* o = (bf16_t*)p.c + m * p.ldc + n;
-    store4(o, dg, 4);
-    store4(o + p.half, du, 4);
-  } else {
-    bf16_t* o = (bf16_t*)p.c + m * p.ldc + n;
-    if (p.residual) sum += load4((const bf16_t*)p.residual + m * p.ldc + n, in);
-    store4(o, sum, in);
-  }
-}
-
-template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+template <int BM, int BN, int WM, int WN, int NS, bool ACOL, bool BCOL, int EPI>
 struct Tile {
   static constexpr int NW = WM * WN, THREADS = NW * 64, MI = BM / WM / 32, NI = BN / WN / 32;
   static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KB loads per wave and k-tile
   static constexpr int COLS = EPI == EPI_GLU ? BN / 2 : BN;  // columns of C
   static_assert(EPI != EPI_GLU || (NI == 2 && !BCOL), "a wave holds the gate's and the up projection's same 32 columns");
+
+  static_assert((!ACOL || BM % 128 == 0) && (!BCOL || BN % 128 == 0), "swz_col permutes runs of 8 granules, 128 columns");
 
   template <int C>
   static __device__ __forceinline__ bf16x8_t frag_col(const unsigned char* st, int cb, int ks, int lane) {
@@ -171,7 +325,7 @@ struct Tile {
       if (ACOL) {
         int c = m0 + 8 * col_c(q, BM);
         c = c < p.M ? c : 0;
-        aoff[j] = (uint32_t)col_k(q, BM) * lda + (uint32_t)(c + (c >= p.a_seg ? p.a_jump : 0)) * 2;
+        aoff[j] = (uint32_t)col_k(q, BM) * lda + (uint32_t)c * 2;
       } else {
         const int r = 8 * q + (lane >> 3);
         aoff[j] = (uint32_t)(m0 + r < p.M ? r : 0) * lda + row_k(q);
@@ -195,7 +349,7 @@ struct Tile {
 
     auto load = [&](int kt, int u) {  // load u of k-tile kt: A's, then B's
       const bool tail = kt == nk - 1 && cnt < 64;
-      const uint32_t st = lds0 + (kt & 1) * STAGE;
+      const uint32_t st = lds0 + kt % NS * STAGE;
       if (u < LA) {
         const int q = wave * LA + u;
         uint32_t o = aoff[u];
@@ -217,7 +371,7 @@ struct Tile {
     };
     auto zero_rest = [&](int kt) {  // after the barrier that made k-tile kt visible
       if (kt != nk - 1 || cnt >= 64) return;
-      unsigned char* st = smem + (kt & 1) * STAGE;
+      unsigned char* st = smem + kt % NS * STAGE;
       auto clear = [&](unsigned char* o, int R, bool col) {
         for (int i = tid; i < R * 8; i += THREADS) {  // 16-byte pieces: by rows row i / 8, chunk i % 8; by columns in order
           const int r = i >> 3, c = i & 7, k = col ? i / (R / 8) : c * 8;
@@ -239,7 +393,7 @@ struct Tile {
         for (int q = 0; q < 16; ++q) acc[mi][ni][q] = 0.f;
     bf16x8_t fa[2][MI], fb[2][NI];
     auto frag = [&](int kt, int ks, int i, bf16x8_t* A_, bf16x8_t* B_) {
-      const unsigned char* sa = smem + (kt & 1) * STAGE;
+      const unsigned char* sa = smem + kt % NS * STAGE;
       if (i < MI) {
         const int rb = (wm * MI + i) * 32;
         A_[i] = ACOL ? frag_col<BM>(sa, rb, ks, lane) : frag_row(sa, rb, ks, lane);
@@ -248,13 +402,13 @@ struct Tile {
         B_[ni] = BCOL ? frag_col<BN>(sa + A_BYTES, rb, ks, lane) : frag_row(sa + A_BYTES, rb, ks, lane);
       }
     };
-    // one k-step: its products, with the next step's fragment reads in the first RS slots and the loads after them.  M1,
-    // M2: there is a next k-tile, and one after it
+    // one k-step: its products, with the next step's fragment reads in the first RS slots and the loads after them.  M1: there
+    // is a next k-tile; MA, MB: k-tiles kt + NS and kt + NS - 1, whose A and B loads go out in this one
     constexpr int NSLOT = MI * NI, RS = 2, RPS = (MI + NI + RS - 1) / RS;
     constexpr int DA = (LA + NSLOT - RS - 1) / (NSLOT - RS > 0 ? NSLOT - RS : 1), DB = (LB + NSLOT - RS - 1) / (NSLOT - RS > 0 ? NSLOT - RS : 1);
-    auto step = [&](auto ks_tag, auto m1_tag, auto m2_tag, int kt) {
+    auto step = [&](auto ks_tag, auto m1_tag, auto ma_tag, auto mb_tag, int kt) {
       constexpr int ks = decltype(ks_tag)::value, c = ks & 1;
-      constexpr bool M1 = decltype(m1_tag)::value, M2 = decltype(m2_tag)::value;
+      constexpr bool M1 = decltype(m1_tag)::value, MA = decltype(ma_tag)::value, MB = decltype(mb_tag)::value;
 #pragma unroll
       for (int i = 0; i < NSLOT; ++i) {
         const int mi = i / NI, ni = i % NI;
@@ -268,46 +422,50 @@ struct Tile {
         }
         if (i >= RS || NSLOT <= RS) {
           const int k = NSLOT <= RS ? i : i - RS;
-          if (ks == 3 && M2) {
+          if (ks == 3 && MA) {
 #pragma unroll
-            for (int v = k * DA; v < (k + 1) * DA && v < LA; ++v) load(kt + 2, v);
+            for (int v = k * DA; v < (k + 1) * DA && v < LA; ++v) load(kt + NS, v);
           }
-          if (ks == 0 && M1) {
+          if (ks == 0 && MB) {
 #pragma unroll
-            for (int v = k * DB; v < (k + 1) * DB && v < LB; ++v) load(kt + 1, LA + v);
+            for (int v = k * DB; v < (k + 1) * DB && v < LB; ++v) load(kt + NS - 1, LA + v);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (ks == 2) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // the next k-tile has landed (MB: the loads of the NS - 2 after it may be in flight; else nothing waits for long)
+        if (MB) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NS - 2) * (LA + LB)) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        if (M1 && !M2) zero_rest(kt + 1);
+        if (M1 && !MA) zero_rest(kt + 1);
       }
     };
-    auto ktile = [&](auto m1, auto m2, int kt) {
-      step(std::integral_constant<int, 0>{}, m1, m2, kt);
-      step(std::integral_constant<int, 1>{}, m1, m2, kt);
-      step(std::integral_constant<int, 2>{}, m1, m2, kt);
-      step(std::integral_constant<int, 3>{}, m1, m2, kt);
+    auto ktile = [&](auto m1, auto ma, auto mb, int kt) {
+      step(std::integral_constant<int, 0>{}, m1, ma, mb, kt);
+      step(std::integral_constant<int, 1>{}, m1, ma, mb, kt);
+      step(std::integral_constant<int, 2>{}, m1, ma, mb, kt);
+      step(std::integral_constant<int, 3>{}, m1, ma, mb, kt);
     };
+    // before the first: k-tiles 0 .. NS - 2 and the A loads of k-tile NS - 1
+    const std::true_type yes;
+    const std::false_type no;
 #pragma unroll
-    for (int u = 0; u < LA + LB; ++u) load(0, u);
-    wait_loads_barrier();
+    for (int t = 0; t < NS; ++t) {
+      if (t >= nk) break;
+#pragma unroll
+      for (int u = 0; u < (t < NS - 1 ? LA + LB : LA); ++u) load(t, u);
+    }
+    if (NS > 2 && nk >= NS) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NS - 2) * (LA + LB) + LA) : "memory");
+    else wait_loads_barrier();
     if (nk == 1) zero_rest(0);
 #pragma unroll
     for (int i = 0; i < MI + NI; ++i) frag(0, 0, i, fa[0], fb[0]);
-    if (nk > 1) {
-#pragma unroll
-      for (int u = 0; u < LA; ++u) load(1, u);
-    }
     int kt = 0;
-    for (; kt + 2 < nk; ++kt) ktile(std::true_type{}, std::true_type{}, kt);
-    if (kt + 1 < nk) {
-      ktile(std::true_type{}, std::false_type{}, kt);
-      ++kt;
-    }
-    ktile(std::false_type{}, std::false_type{}, kt);
+    for (; kt + NS < nk; ++kt) ktile(yes, yes, yes, kt);
+    if (kt + NS == nk) ktile(yes, no, yes, kt++);
+    for (; kt + 1 < nk; ++kt) ktile(yes, no, no, kt);
+    ktile(no, no, no, kt);
 
     // element q of accumulator (mi, ni): row 8 (q / 4) + 4 (lane / 32) + q % 4 of its block, column lane % 32; each group of
     // four q is transposed inside its quad of lanes, after which a lane holds four neighbouring columns of one row
@@ -329,7 +487,7 @@ struct Tile {
             float* o = partial + (int64_t)m * ld_partial + n;
             *(f32x4_t*)o = v;
             if (EPI == EPI_GLU) *(f32x4_t*)(o + ld_partial / 2) = w;
-          } else finish4<EPI>(p, m, n, v, w);
+          } else finish4<bf16_t, EPI>(p, m, n, v, w);
         }
       }
   }
@@ -337,9 +495,9 @@ struct Tile {
 
 // One workgroup per tile and k-split.  Workgroups go round the eight XCDs, so a run of 1/8 of the grid's tiles is one
 // XCD's, whose L2 its tiles share: bands of eight tile rows, walked column by column.
-template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+template <int BM, int BN, int WM, int WN, int NS, bool ACOL, bool BCOL, int EPI>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_bf16(Gemm p, int splits, float* partial, int64_t ld_partial) {
-  using G = Tile<BM, BN, WM, WN, ACOL, BCOL, EPI>;
+  using G = Tile<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int mt = (p.M + BM - 1) / BM, nt = (p.N + G::COLS - 1) / G::COLS, nkt = (p.K + 63) / 64;
   const int tiles = mt * nt, n = tiles * splits;
@@ -369,50 +527,94 @@ __global__ __launch_bounds__(256) void k_gemm_finish(Gemm p, int splits, const f
     v += *(const f32x4_t*)o;
     if (EPI == EPI_GLU) w += *(const f32x4_t*)(o + ld / 2);
   }
-  finish4<EPI>(p, m, n, v, w);
+  finish4<bf16_t, EPI>(p, m, n, v, w);
 }
 
 // Columns of a partial sum's row
 int64_t partial_cols(const Gemm& p, int epi) { return (int64_t)(p.N + 3) / 4 * 4 * (epi == EPI_GLU ? 2 : 1); }
 
-template <int BM, int BN, int WM, int WN, bool ACOL, bool BCOL, int EPI>
+template <int BM, int BN, int WM, int WN, int NS, bool ACOL, bool BCOL, int EPI>
 int gemm_tiles(const Gemm& p, int splits, float* partial, hipStream_t st) {
-  using G = Tile<BM, BN, WM, WN, ACOL, BCOL, EPI>;
+  using G = Tile<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
   const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + G::COLS - 1) / G::COLS) * splits;
   if (tiles > 0x7fffffff) return -1;
   const int64_t ld = partial_cols(p, EPI);
-  auto k = k_gemm_bf16<BM, BN, WM, WN, ACOL, BCOL, EPI>;
-  static const hipError_t once = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, 2 * G::STAGE);
+  auto k = k_gemm_bf16<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
+  static const hipError_t once = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, NS * G::STAGE);
   if (once != hipSuccess) return -1;
-  hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(G::THREADS), 2 * G::STAGE, st, p, splits, splits > 1 ? partial : nullptr, ld);
+  hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(G::THREADS), NS * G::STAGE, st, p, splits, splits > 1 ? partial : nullptr, ld);
   if (splits > 1)
     hipLaunchKernelGGL(k_gemm_finish<EPI>, dim3((unsigned)(((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256)), dim3(256), 0, st, p,
                        splits, partial, ld);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
-template <bool ACOL, bool BCOL, int EPI>
-int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
-  if (p.M == 0) return 0;
-  const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + (EPI == EPI_GLU ? 127 : 255)) / (EPI == EPI_GLU ? 128 : 256));
-  if (big >= 192) return gemm_tiles<256, 256, 2, 4, ACOL, BCOL, EPI>(p, 1, partial, st);
-  return gemm_tiles<128, 128, 2, 2, ACOL, BCOL, EPI>(p, 1, partial, st);
+// Floats that a product's k-splits may take, and how many splits
+constexpr int64_t PARTIAL = 512ll * 128 * 128;
+constexpr int MAX_SPLITS = 16;
+
+// Tile and k-splits of a product, by an estimate of its time from what the tiles measured (us per k-tile of 64, operands
+// from HBM).  256 x 256: 1.5 with one workgroup on each CU.  128 x 128 in two stages: 0.85 where a CU has one workgroup, 1.05
+// for two at once; in four stages (one workgroup fills a CU's LDS): 0.62, the loads' latency hidden by their depth instead
+// of by the other workgroup.  64 x 128 in three stages: 0.53 and 0.75.  So the large tile is 1.4 times as fast per product
+// once every CU has one, and the small ones win where they would leave CUs idle: 777 tokens of the skewed workload's widths
+// take 37 us forward in 64 x 128 or deep 128 x 128 tiles, 49 in 128 x 128, 82 in 256 x 256; 2048 tokens 60, 62 and 93;
+// 16384 tokens of the DeepSeek-V3-shaped widths 1310 in 256 x 256.  Splitting k costs the fp32 sums' way to memory and
+// back and a second launch; 128 tokens of those widths take 47 us in four splits and 80 in one.
+struct Choice {
+  int tile, splits;
+};
+Choice choose(int64_t M, int64_t cols, int nkt, bool a_by_cols) {
+  static const struct {
+    int bm, bn, per_cu;
+    double alone, full, fixed;  // us: a k-tile with one workgroup on the CU, with per_cu of them, and a tile's two ends
+  } tiles[] = {{256, 256, 1, 1.5, 1.5, 5.0}, {128, 128, 2, 0.85, 1.05, 3.0}, {128, 128, 1, 0.62, 0.62, 3.0}, {64, 128, 2, 0.53, 0.75, 2.5}};
+  Choice best{0, 1};
+  double least = 1e30;
+  for (int t = 0; t < 4; ++t) {
+    if (a_by_cols && tiles[t].bm % 128) continue;
+    const int64_t n = ((M + tiles[t].bm - 1) / tiles[t].bm) * ((cols + tiles[t].bn - 1) / tiles[t].bn);
+    for (int s = 1; s <= MAX_SPLITS; ++s) {
+      if (s > 1 && (nkt / s < 4 || s * M * cols > PARTIAL)) break;
+      const int64_t slots = 256 * tiles[t].per_cu, rounds = n * s / slots, rest = n * s % slots;
+      const double kt = (double)((nkt + s - 1) / s);
+      const double us = rounds * (kt * tiles[t].full + tiles[t].fixed) +
+                        (rest ? kt * (rest <= 256 ? tiles[t].alone : tiles[t].full) + tiles[t].fixed : 0.0) +
+                        (s > 1 ? 4.0 + 8.0 * s * M * cols / 3.5e6 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {t, s};
+      }
+    }
+  }
+  return best;
 }
 
-// ---- any sizes, any type: fp32 matrix instructions ------------------------------------------------------------------
+template <bool ACOL, bool BCOL, int EPI>
+int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
+  const Choice c = choose(p.M, partial_cols(p, EPI), (p.K + 63) / 64, ACOL);
+  if (c.tile == 0) return gemm_tiles<256, 256, 2, 4, 2, ACOL, BCOL, EPI>(p, c.splits, partial, st);
+  if (c.tile == 1) return gemm_tiles<128, 128, 2, 2, 2, ACOL, BCOL, EPI>(p, c.splits, partial, st);
+  if constexpr (!ACOL) {
+    if (c.tile == 3) return gemm_tiles<64, 128, 2, 2, 3, ACOL, BCOL, EPI>(p, c.splits, partial, st);
+  }
+  return gemm_tiles<128, 128, 2, 2, 4, ACOL, BCOL, EPI>(p, c.splits, partial, st);
+}
+
+// ---- fp32, any sizes --------------------------------------------------------------------------------------------------
 // A 128 x 64 tile of C (GLU: 32 columns of the gate and the same 32 of the up projection) by four waves of 32 x 64, in
-// k-tiles of 16: each operand's k-tile is loaded by elements of its own layout into registers one k-tile ahead, widened
-// to fp32 and kept in LDS as [k][m], from where a lane takes one element of A and two of B for two 32x32x2 products.
+// k-tiles of 16: each operand's k-tile is loaded by elements of its own layout into registers one k-tile ahead and kept in
+// LDS as [k][m], from where a lane takes one element of A and two of B for two 32x32x2 products.
 constexpr int GM = 128, GN = 64, GK = 16, GSUM = 256;
 
-template <typename T, int EPI, bool ACOL, bool BCOL>
-__global__ __launch_bounds__(256) void k_gemm_any(Gemm p) {
+template <int EPI, bool ACOL, bool BCOL>
+__global__ __launch_bounds__(256) void k_gemm_f32(Gemm p) {
   __shared__ float sa[2][GK][GM + 4], sb[2][GK][GN + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int BN = EPI == EPI_GLU ? GN / 2 : GN;
   const int nt = (p.N + BN - 1) / BN;
   const int m0 = (int)(blockIdx.x / nt) * GM, n0 = (int)(blockIdx.x % nt) * BN;
-  const T *A = (const T*)p.a, *B = (const T*)p.b;
+  const float *A = (const float*)p.a, *B = (const float*)p.b;
 
   // thread -> four neighbours along memory: by rows (row tid / 4, k 4 (tid % 4)), by columns (k tid / 16 or 32, m ..)
   float ra[8], rb[4];
@@ -432,7 +634,7 @@ __global__ __launch_bounds__(256) void k_gemm_any(Gemm p) {
         float v = 0.f;
         if (m < p.M && k < p.K) {
           const int c = ACOL ? m : k;
-          v = as_float(A[(int64_t)(ACOL ? k : m) * p.lda + c + (c >= p.a_seg ? p.a_jump : 0)]);
+          v = (A[(int64_t)(ACOL ? k : m) * p.lda + c + (c >= p.a_seg ? p.a_jump : 0)]);
         }
         ra[4 * h + i] = v;
       }
@@ -456,7 +658,7 @@ __global__ __launch_bounds__(256) void k_gemm_any(Gemm p) {
         in = c < p.N;
         row = n < BN ? c : (int64_t)p.up + c;
       }
-      rb[i] = in && k < p.K ? as_float(B[BCOL ? (int64_t)k * p.ldb + row : row * p.ldb + k]) : 0.f;
+      rb[i] = in && k < p.K ? (B[BCOL ? (int64_t)k * p.ldb + row : row * p.ldb + k]) : 0.f;
     }
   };
   auto keep = [&](int s) {
@@ -521,7 +723,7 @@ __global__ __launch_bounds__(256) void k_gemm_any(Gemm p) {
       const int n = n0 + (lane & 31);
       if (n >= p.N) continue;
       const float g = total[0][q], u = total[1][q];
-      put((T*)p.c + m * p.ldc + n, g / (1.0f + __expf(-g)) * u);
+      ((float*)p.c)[m * p.ldc + n] = g / (1.0f + __expf(-g)) * u;
       if (p.gu) {
         float* o = p.gu + m * p.ldgu + n;
         o[0] = g;
@@ -537,64 +739,170 @@ __global__ __launch_bounds__(256) void k_gemm_any(Gemm p) {
         const float* i = p.gu + m * p.ldgu + n;
         float dg, du;
         dglu(total[j][q], i[0], i[p.half], &dg, &du);
-        T* o = (T*)p.c + m * p.ldc + n;
-        put(o, dg);
-        put(o + p.half, du);
+        float* o = (float*)p.c + m * p.ldc + n;
+        o[0] = dg;
+        o[p.half] = du;
       } else {
         const int64_t at = m * p.ldc + n;
-        put((T*)p.c + at, total[j][q] + (p.residual ? as_float(((const T*)p.residual)[at]) : 0.f));
+        ((float*)p.c)[at] = total[j][q] + (p.residual ? ((const float*)p.residual)[at] : 0.f);
       }
     }
   }
 }
 
-template <typename T, int EPI, bool ACOL, bool BCOL>
-int gemm_any(const Gemm& p, hipStream_t st) {
+template <int EPI, bool ACOL, bool BCOL>
+int gemm_f32(const Gemm& p, hipStream_t st) {
   if (p.M == 0) return 0;
   constexpr int BN = EPI == EPI_GLU ? GN / 2 : GN;
   const int64_t tiles = (int64_t)((p.M + GM - 1) / GM) * ((p.N + BN - 1) / BN);
   if (tiles > 0x7fffffff) return -1;
-  hipLaunchKernelGGL((k_gemm_any<T, EPI, ACOL, BCOL>), dim3((unsigned)tiles), dim3(256), 0, st, p);
+  hipLaunchKernelGGL((k_gemm_f32<EPI, ACOL, BCOL>), dim3((unsigned)tiles), dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 // ---- the block --------------------------------------------------------------------------------------------------
 
-struct Block {  // one call's products
-  Gemm glu, down;                  // forward
+// bf16 operands whose rows do not start at 16 bytes, copied to rows that do: one launch for all of a call's.  Row r of a
+// copy, in parts of `padded` rows, is row (r / padded) * real + r % padded of the operand, or 0 where r % padded >= real;
+// columns past the operand's are 0.
+struct PackJob {
+  const bf16_t* src;
+  bf16_t* dst;
+  int64_t first, rows;  // first: 16-byte pieces of the jobs before
+  int cols, ld, real, padded;  // ld: of the copy, a multiple of 8; the operand's is cols
+};
+struct PackJobs {
+  PackJob job[4];
+  int n;
+  int64_t pieces;
+};
+
+__global__ __launch_bounds__(256) void k_pack(PackJobs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.pieces) return;
+  int j = 0;
+  while (j + 1 < a.n && i >= a.job[j + 1].first) ++j;
+  const PackJob& b = a.job[j];
+  const int per = b.ld / 8;
+  const int64_t r = (i - b.first) / per;
+  const int c = (int)(i - b.first - r * per) * 8, part = (int)(r / b.padded), at = (int)(r - (int64_t)part * b.padded);
+  u32x4_t v = {0u, 0u, 0u, 0u};
+  if (at < b.real) {
+    const bf16_t* s = b.src + ((int64_t)part * b.real + at) * b.cols + c;
+    if (c + 8 <= b.cols) __builtin_memcpy(&v, s, 16);
+    else
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < b.cols) v[k / 2] |= (uint32_t)s[k] << (16 * (k & 1));
+  }
+  *(u32x4_t*)(b.dst + r * b.ld + c) = v;
+}
+
+__global__ __launch_bounds__(256) void k_clear(bf16_t* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0;
+}
+
+int clear(void* p, int64_t n, hipStream_t st) {
+  hipLaunchKernelGGL(k_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (bf16_t*)p, n);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// Elements of the copies a call makes of its operands (x, w_gate_up, w_down, dy)
+void pack_sizes(int64_t tokens, int d, int f, bool backward, int64_t (&n)[4]) {
+  const bool odd_d = d % 8 != 0, odd = odd_d || f % 8 != 0;
+  const int64_t D = up8(d), F = up8(f);
+  n[0] = odd_d ? up256(tokens * D) : 0;
+  n[1] = odd ? up256(2 * F * D) : 0;
+  n[2] = odd ? up256(D * F) : 0;
+  n[3] = odd_d && backward ? up256(tokens * D) : 0;
+}
+
+// The call's products.  f32: on the operands as they are.  bf16: on rows that start at 16 bytes, widths D and F in whole
+// eights; the weights' rows and columns past d and f are 0, so that sums over a whole D or F need no care, and g, u and h
+// past f become 0.
+struct Block {
+  Gemm glu, down;                      // forward
   Gemm dglu, dx, dw_gate_up, dw_down;  // backward
 };
 
-Block block_of(const SharedLaunch& s) {
+Block block_f32(const SharedLaunch& s) {
   Block b{};
   const int T = (int)s.tokens, d = s.d, f = s.f, F = s.row, none = 0x7fffffff;
-  b.glu = {s.x, s.w_gate_up, d, d, none, 0, T, f, d, s.h, F, nullptr, s.gu, 2 * F, F, f};
-  b.down = {s.h, s.w_down, F, f, none, 0, T, d, f, s.y, d, s.residual, nullptr, 0, 0, 0};
-  b.dglu = {s.dy, s.w_down, d, f, none, 0, T, f, d, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0};
-  b.dx = {s.dgu, s.w_gate_up, 2 * F, d, f, F - f, T, d, 2 * f, s.dx, d, s.residual, nullptr, 0, 0, 0};
-  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, f, F - f, 2 * f, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0};
-  b.dw_down = {s.dy, s.h, d, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0};
+  b.glu = {s.x, s.w_gate_up, d, d, none, 0, T, f, d, s.h, F, nullptr, s.gu, 2 * F, F, f, none, none};
+  b.down = {s.h, s.w_down, F, f, none, 0, T, d, f, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dglu = {s.dy, s.w_down, d, f, none, 0, T, f, d, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
+  b.dx = {s.dgu, s.w_gate_up, 2 * F, d, f, F - f, T, d, 2 * f, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, f, F - f, 2 * f, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, none, none};
+  b.dw_down = {s.dy, s.h, d, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
   return b;
 }
 
-template <typename T>
-int run_any(const SharedLaunch& s, hipStream_t st) {
-  const Block b = block_of(s);
+Block block_bf16(const SharedLaunch& s, const void* x, const void* wgu, const void* wd, const void* dy) {
+  Block b{};
+  const int T = (int)s.tokens, d = s.d, f = s.f, F = s.row, D = (int)up8(d), none = 0x7fffffff;
+  b.glu = {x, wgu, D, D, none, 0, T, F, D, s.h, F, nullptr, s.gu, 2 * F, F, F, none, none};
+  b.down = {s.h, wd, F, F, none, 0, T, d, F, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dglu = {dy, wd, D, F, none, 0, T, F, D, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
+  b.dx = {s.dgu, wgu, 2 * F, D, none, 0, T, d, 2 * F, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dw_gate_up = {s.dgu, x, 2 * F, D, none, 0, 2 * F, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
+  b.dw_down = {dy, s.h, D, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
+  return b;
+}
+
+int run_f32(const SharedLaunch& s, hipStream_t st) {
+  const Block b = block_f32(s);
   int rc;
   if (!s.backward) {
-    if ((rc = gemm_any<T, EPI_GLU, false, false>(b.glu, st))) return rc;
-    return gemm_any<T, EPI_STORE, false, false>(b.down, st);
+    if (s.tokens <= FEW) {
+      if ((rc = gemm_few<float, EPI_GLU>(b.glu, st))) return rc;
+      return gemm_few<float, EPI_STORE>(b.down, st);
+    }
+    if ((rc = gemm_f32<EPI_GLU, false, false>(b.glu, st))) return rc;
+    return gemm_f32<EPI_STORE, false, false>(b.down, st);
   }
-  if ((rc = gemm_any<T, EPI_DGLU, false, true>(b.dglu, st))) return rc;
-  if ((rc = gemm_any<T, EPI_STORE, false, true>(b.dx, st))) return rc;
-  if ((rc = gemm_any<T, EPI_STORE, true, true>(b.dw_gate_up, st))) return rc;
-  return gemm_any<T, EPI_STORE, true, true>(b.dw_down, st);
+  if ((rc = gemm_f32<EPI_DGLU, false, true>(b.dglu, st))) return rc;
+  if ((rc = gemm_f32<EPI_STORE, false, true>(b.dx, st))) return rc;
+  if ((rc = gemm_f32<EPI_STORE, true, true>(b.dw_gate_up, st))) return rc;
+  return gemm_f32<EPI_STORE, true, true>(b.dw_down, st);
 }
 
 int run_bf16(const SharedLaunch& s, hipStream_t st) {
-  const Block b = block_of(s);
-  float* partial = nullptr;
   int rc;
+  if (s.tokens == 0) {
+    if ((rc = clear(s.dw_gate_up, 2ll * s.f * s.d, st))) return rc;
+    return clear(s.dw_down, (int64_t)s.f * s.d, st);
+  }
+  if (!s.backward && s.tokens <= FEW) {
+    const Block b = block_f32(s);  // the operands as they are
+    if ((rc = gemm_few<bf16_t, EPI_GLU>(b.glu, st))) return rc;
+    return gemm_few<bf16_t, EPI_STORE>(b.down, st);
+  }
+  int64_t n[4];
+  pack_sizes(s.tokens, s.d, s.f, s.backward, n);
+  const void* op[4] = {s.x, s.w_gate_up, s.w_down, s.dy};
+  const int D = (int)up8(s.d), T = (int)s.tokens;
+  const int cols[4] = {s.d, s.d, s.f, s.d}, ld[4] = {D, D, s.row, D}, real[4] = {T, s.f, s.d, T}, padded[4] = {T, s.row, D, T};
+  const int64_t rows[4] = {T, 2 * s.row, D, T};
+  PackJobs jobs{};
+  bf16_t* to = (bf16_t*)s.workspace;
+  for (int i = 0; i < 4; ++i)
+    if (n[i] && (s.backward || i < 3)) {
+      jobs.job[jobs.n++] = {(const bf16_t*)op[i], to, jobs.pieces, rows[i], cols[i], ld[i], real[i], padded[i]};
+      jobs.pieces += rows[i] * (ld[i] / 8);
+      op[i] = to;
+      to += n[i];
+    }
+  if (jobs.n) {
+    const int64_t blocks = (jobs.pieces + 255) / 256;
+    if (blocks > 0x7fffffff) return -1;
+    hipLaunchKernelGGL(k_pack, dim3((unsigned)blocks), dim3(256), 0, st, jobs);
+  }
+  float* partial = (float*)to;
+  const Block b = block_bf16(s, op[0], op[1], op[2], op[3]);
   if (!s.backward) {
     if ((rc = gemm_bf16<false, false, EPI_GLU>(b.glu, partial, st))) return rc;
     return gemm_bf16<false, false, EPI_STORE>(b.down, partial, st);
@@ -607,10 +915,14 @@ int run_bf16(const SharedLaunch& s, hipStream_t st) {
 
 }  // namespace
 
-int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool backward) { return 0; }
-
-int launch_shared(const SharedLaunch& s, hipStream_t st) {
-  const bool aligned = s.d % 8 == 0 && s.f % 8 == 0;
-  if (s.dtype == MOE_BF16 && aligned && s.tokens > 0) return run_bf16(s, st);
-  return s.dtype == MOE_BF16 ? run_any<bf16_t>(s, st) : run_any<float>(s, st);
+int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool backward) {
+  if (dtype != MOE_BF16 || tokens == 0) return 0;
+  int64_t n[4];
+  pack_sizes(tokens, d, f, backward, n);
+  // the k-splits' sums: at most PARTIAL floats, and MAX_SPLITS times the largest product
+  const int64_t out = backward ? std::max(std::max(tokens * up8(d), tokens * up8(f)), 2 * up8(f) * up8(d))
+                               : std::max(tokens * up8(d), tokens * 2 * up8(f));
+  return 2 * (n[0] + n[1] + n[2] + n[3]) + 4 * std::min<int64_t>(PARTIAL, MAX_SPLITS * out);
 }
+
+int launch_shared(const SharedLaunch& s, hipStream_t st) { return s.dtype == MOE_BF16 ? run_bf16(s, st) : run_f32(s, st); }
