@@ -31,15 +31,10 @@ struct Gemm {
   int64_t ldgu;
   int half;  // GLU, DGLU: from a row's g to its u (and dg to du)
   int up;    // GLU: rows of B from the gate's to the up projection's
-  // STORE: rows of C from m_pad on stand m_pad - m_real earlier, those in [m_real, m_pad) nowhere (dg's padding)
+  // STORE: rows of C from m_pad on stand m_pad - m_real earlier; those in [m_real, m_pad) and those that would then stand
+  // past 2 m_real are dg's and du's padding and stand nowhere
   int m_real, m_pad;
 };
-
-__device__ __forceinline__ void dglu(float dh, float g, float u, float* dg, float* du) {
-  const float s = 1.0f / (1.0f + __expf(-g));
-  *dg = dh * u * s * (1.0f + g * (1.0f - s));
-  *du = dh * g * s;
-}
 
 // ---- epilogues ----
 // 4 columns of one row, any alignment; n: how many of them are inside the matrix
@@ -110,6 +105,7 @@ __device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t
   } else {
     if (m >= p.m_pad) m -= p.m_pad - p.m_real;
     else if (m >= p.m_real) return;
+    if (m >= 2ll * p.m_real) return;
     T* o = (T*)p.c + m * p.ldc + n;
     if (p.residual) sum += load4((const T*)p.residual + m * p.ldc + n, in);
     store4(o, sum, in);
@@ -493,60 +489,157 @@ struct Tile {
   }
 };
 
-// One workgroup per tile and k-split.  Workgroups go round the eight XCDs, so a run of 1/8 of the grid's tiles is one
-// XCD's, whose L2 its tiles share: bands of eight tile rows, walked column by column.
-template <int BM, int BN, int WM, int WN, int NS, bool ACOL, bool BCOL, int EPI>
-__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bf16(Gemm p, int splits, float* partial, int64_t ld_partial) {
-  using G = Tile<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  const int mt = (p.M + BM - 1) / BM, nt = (p.N + G::COLS - 1) / G::COLS, nkt = (p.K + 63) / 64;
-  const int tiles = mt * nt, n = tiles * splits;
-  int i = blockIdx.x;
-  {  // position among the launch's tiles: XCD x takes [x n / 8, (x + 1) n / 8), rounded so that each is taken once
+// A product as one or several of a launch's workgroups, one per tile and k-split
+struct Part {
+  Gemm p;
+  int splits;
+  int first, blocks;  // workgroups [first, first + blocks) of the launch; first is a multiple of 8
+  float* partial;     // splits > 1: [splits][M][ld] sums
+  int64_t ld;
+};
+struct Parts {  // dx, dw_gate_up, dw_down
+  Part part[3];
+};
+
+// Workgroups go round the eight XCDs, so a run of 1/8 of a product's tiles is one XCD's, whose L2 its tiles share: bands of
+// eight tile rows, walked column by column.
+template <class G>
+__device__ __forceinline__ void bf16_tile(const Part& a, int bm, unsigned char* smem) {
+  const Gemm& p = a.p;
+  const int mt = (p.M + bm - 1) / bm, nt = (p.N + G::COLS - 1) / G::COLS, nkt = (p.K + 63) / 64;
+  const int tiles = mt * nt, n = tiles * a.splits;
+  int i = blockIdx.x - a.first;
+  {  // position among the product's tiles: XCD x takes [x n / 8, (x + 1) n / 8), rounded so that each is taken once
     const int x = i & 7, per = n >> 3, more = n & 7;
     i = x * per + (x < more ? x : more) + (i >> 3);
   }
   const int s = i / tiles;
   i -= s * tiles;
   const int band = i / (8 * nt), rows = min(8, mt - band * 8), r = i - band * 8 * nt;
-  const int t0 = (int)((int64_t)nkt * s / splits), t1 = (int)((int64_t)nkt * (s + 1) / splits);
-  G::run(p, smem, (band * 8 + r % rows) * BM, (r / rows) * G::COLS, t0, t1 - t0,
-         partial ? partial + (int64_t)s * p.M * ld_partial : nullptr, ld_partial);
+  const int t0 = (int)((int64_t)nkt * s / a.splits), t1 = (int)((int64_t)nkt * (s + 1) / a.splits);
+  G::run(p, smem, (band * 8 + r % rows) * bm, (r / rows) * G::COLS, t0, t1 - t0,
+         a.partial ? a.partial + (int64_t)s * p.M * a.ld : nullptr, a.ld);
+}
+
+template <int BM, int BN, int WM, int WN, int NS, bool BCOL, int EPI>
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bf16(Part a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  bf16_tile<Tile<BM, BN, WM, WN, NS, false, BCOL, EPI>>(a, BM, smem);
+}
+
+// The backward's last three products in one launch: none waits for another, and together they fill the last round of
+// workgroups that each of them would leave part empty.
+template <int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(WM * WN * 64) void k_grads_bf16(Parts a) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int i = blockIdx.x;
+  auto mine = [&](const Part& q) { return i >= q.first && i < q.first + q.blocks; };
+  if (mine(a.part[0])) bf16_tile<Tile<BM, BN, WM, WN, NS, false, true, EPI_STORE>>(a.part[0], BM, smem);
+  else if (mine(a.part[1]) || mine(a.part[2]))
+    bf16_tile<Tile<BM, BN, WM, WN, NS, true, true, EPI_STORE>>(a.part[mine(a.part[1]) ? 1 : 2], BM, smem);
 }
 
 // The k-splits' sums, in split order, through the epilogue: four columns per thread.
-template <int EPI>
-__global__ __launch_bounds__(256) void k_gemm_finish(Gemm p, int splits, const float* __restrict__ partial, int64_t ld) {
+template <typename T, int EPI>
+__device__ __forceinline__ void finish(const Part& a, int64_t i) {
+  const Gemm& p = a.p;
   const int quads = (p.N + 3) / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, m = i / quads;
+  const int64_t m = i / quads;
   if (m >= p.M) return;
   const int n = (int)(i - m * quads) * 4;
-  const float* o = partial + m * ld + n;
+  const float* o = a.partial + m * a.ld + n;
   f32x4_t v = {0, 0, 0, 0}, w = {0, 0, 0, 0};
-  for (int s = 0; s < splits; ++s, o += p.M * ld) {
+  for (int s = 0; s < a.splits; ++s, o += p.M * a.ld) {
     v += *(const f32x4_t*)o;
-    if (EPI == EPI_GLU) w += *(const f32x4_t*)(o + ld / 2);
+    if (EPI == EPI_GLU) w += *(const f32x4_t*)(o + a.ld / 2);
   }
-  finish4<bf16_t, EPI>(p, m, n, v, w);
+  finish4<T, EPI>(p, m, n, v, w);
+}
+template <typename T, int EPI>
+__global__ __launch_bounds__(256) void k_finish(Part a) {
+  finish<T, EPI>(a, (int64_t)blockIdx.x * 256 + threadIdx.x);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void k_finish_grads(Parts a) {  // first, blocks: of this launch
+  const int i = blockIdx.x;
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (i >= a.part[j].first && i < a.part[j].first + a.part[j].blocks)
+      finish<T, EPI_STORE>(a.part[j], (int64_t)(i - a.part[j].first) * 256 + threadIdx.x);
 }
 
 // Columns of a partial sum's row
 int64_t partial_cols(const Gemm& p, int epi) { return (int64_t)(p.N + 3) / 4 * 4 * (epi == EPI_GLU ? 2 : 1); }
 
-template <int BM, int BN, int WM, int WN, int NS, bool ACOL, bool BCOL, int EPI>
-int gemm_tiles(const Gemm& p, int splits, float* partial, hipStream_t st) {
-  using G = Tile<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
-  const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + G::COLS - 1) / G::COLS) * splits;
-  if (tiles > 0x7fffffff) return -1;
-  const int64_t ld = partial_cols(p, EPI);
-  auto k = k_gemm_bf16<BM, BN, WM, WN, NS, ACOL, BCOL, EPI>;
-  static const hipError_t once = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, NS * G::STAGE);
-  if (once != hipSuccess) return -1;
-  hipLaunchKernelGGL(k, dim3((unsigned)tiles), dim3(G::THREADS), NS * G::STAGE, st, p, splits, splits > 1 ? partial : nullptr, ld);
-  if (splits > 1)
-    hipLaunchKernelGGL(k_gemm_finish<EPI>, dim3((unsigned)(((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256)), dim3(256), 0, st, p,
-                       splits, partial, ld);
+int64_t finish_blocks(const Gemm& p) { return ((int64_t)p.M * ((p.N + 3) / 4) + 255) / 256; }
+
+// A product's part of a launch; tiles of bm rows and bn columns of B
+bool make_part(Part* a, const Gemm& p, int epi, int bm, int bn, int splits, float* partial, int64_t first) {
+  a->p = p;
+  a->splits = splits;
+  a->ld = partial_cols(p, epi);
+  a->partial = splits > 1 ? partial : nullptr;
+  const int cols = epi == EPI_GLU ? bn / 2 : bn;
+  const int64_t n = (int64_t)((p.M + bm - 1) / bm) * ((p.N + cols - 1) / cols) * splits;
+  a->first = (int)first;
+  a->blocks = (int)n;
+  return first + n + 8 <= 0x7fffffff;
+}
+
+template <class K>
+int launch_tiles(K k, int lds, int threads, int64_t blocks, const void* args, hipStream_t st) {
+  if (lds > 65536 && hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess) return -1;
+  void* params[] = {(void*)args};
+  return hipLaunchKernel((const void*)k, dim3((unsigned)blocks), dim3(threads), params, lds, st) == hipSuccess ? 0 : -1;
+}
+
+template <typename T, int EPI>
+int launch_finish(const Part& a, hipStream_t st) {
+  if (a.splits == 1) return 0;
+  hipLaunchKernelGGL((k_finish<T, EPI>), dim3((unsigned)finish_blocks(a.p)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+template <typename T>
+int launch_finish_grads(Parts g, hipStream_t st) {
+  int64_t n = 0;
+  for (Part& a : g.part) {
+    a.first = (int)n;
+    a.blocks = a.splits > 1 ? (int)finish_blocks(a.p) : 0;
+    n += a.blocks;
+  }
+  if (n == 0) return 0;
+  hipLaunchKernelGGL(k_finish_grads<T>, dim3((unsigned)n), dim3(256), 0, st, g);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <int BM, int BN, int WM, int WN, int NS, bool BCOL, int EPI>
+int gemm_tiles(const Gemm& p, int splits, float* partial, hipStream_t st) {
+  Part a;
+  if (!make_part(&a, p, EPI, BM, BN, splits, partial, 0)) return -1;
+  if (launch_tiles(k_gemm_bf16<BM, BN, WM, WN, NS, BCOL, EPI>, NS * (BM + BN) * 128, WM * WN * 64, a.blocks, &a, st)) return -1;
+  return launch_finish<bf16_t, EPI>(a, st);
+}
+
+// The three gradients' parts, those with the longest sums first; the partial sums one after another
+bool make_grads(Parts* g, const Gemm* const (&p)[3], int bm, int bn, const int (&splits)[3], float* partial, int64_t* blocks) {
+  const bool dx_first = p[0]->K >= p[1]->K;
+  const int order[3] = {dx_first ? 0 : 1, dx_first ? 1 : 2, dx_first ? 2 : 0};
+  *blocks = 0;
+  for (const int i : order) {
+    if (!make_part(&g->part[i], *p[i], EPI_STORE, bm, bn, splits[i], partial, *blocks)) return false;
+    *blocks += (g->part[i].blocks + 7) / 8 * 8;
+    if (splits[i] > 1) partial += (int64_t)splits[i] * p[i]->M * g->part[i].ld;
+  }
+  return true;
+}
+
+template <int BM, int BN, int WM, int WN, int NS>
+int grads_tiles(const Gemm* const (&p)[3], const int (&splits)[3], float* partial, hipStream_t st) {
+  Parts g;
+  int64_t blocks;
+  if (!make_grads(&g, p, BM, BN, splits, partial, &blocks)) return -1;
+  if (launch_tiles(k_grads_bf16<BM, BN, WM, WN, NS>, NS * (BM + BN) * 128, WM * WN * 64, blocks, &g, st)) return -1;
+  return launch_finish_grads<bf16_t>(g, st);
 }
 
 // Floats that a product's k-splits may take, and how many splits
@@ -564,23 +657,25 @@ constexpr int MAX_SPLITS = 16;
 struct Choice {
   int tile, splits;
 };
-Choice choose(int64_t M, int64_t cols, int nkt, bool a_by_cols) {
-  static const struct {
-    int bm, bn, per_cu;
-    double alone, full, fixed;  // us: a k-tile with one workgroup on the CU, with per_cu of them, and a tile's two ends
-  } tiles[] = {{256, 256, 1, 1.5, 1.5, 5.0}, {128, 128, 2, 0.85, 1.05, 3.0}, {128, 128, 1, 0.62, 0.62, 3.0}, {64, 128, 2, 0.53, 0.75, 2.5}};
+const struct {
+  int bm, bn, per_cu;
+  double alone, full, fixed;  // us: a k-tile with one workgroup on the CU, with per_cu of them, and a tile's two ends
+} TILES[] = {{256, 256, 1, 1.5, 1.5, 5.0}, {128, 128, 2, 0.85, 1.05, 3.0}, {128, 128, 1, 0.62, 0.62, 3.0}, {64, 128, 2, 0.53, 0.75, 2.5}};
+int64_t tiles_of(int t, int64_t M, int64_t cols) { return ((M + TILES[t].bm - 1) / TILES[t].bm) * ((cols + TILES[t].bn - 1) / TILES[t].bn); }
+double join_us(int64_t floats) { return 4.0 + 8.0 * floats / 3.5e6; }  // sums to memory and back
+
+Choice choose(int64_t M, int64_t cols, int nkt) {
   Choice best{0, 1};
   double least = 1e30;
   for (int t = 0; t < 4; ++t) {
-    if (a_by_cols && tiles[t].bm % 128) continue;
-    const int64_t n = ((M + tiles[t].bm - 1) / tiles[t].bm) * ((cols + tiles[t].bn - 1) / tiles[t].bn);
+    const int64_t n = tiles_of(t, M, cols);
     for (int s = 1; s <= MAX_SPLITS; ++s) {
       if (s > 1 && (nkt / s < 4 || s * M * cols > PARTIAL)) break;
-      const int64_t slots = 256 * tiles[t].per_cu, rounds = n * s / slots, rest = n * s % slots;
+      const int64_t slots = 256 * TILES[t].per_cu, rounds = n * s / slots, rest = n * s % slots;
       const double kt = (double)((nkt + s - 1) / s);
-      const double us = rounds * (kt * tiles[t].full + tiles[t].fixed) +
-                        (rest ? kt * (rest <= 256 ? tiles[t].alone : tiles[t].full) + tiles[t].fixed : 0.0) +
-                        (s > 1 ? 4.0 + 8.0 * s * M * cols / 3.5e6 : 0.0);
+      const double us = rounds * (kt * TILES[t].full + TILES[t].fixed) +
+                        (rest ? kt * (rest <= 256 ? TILES[t].alone : TILES[t].full) + TILES[t].fixed : 0.0) +
+                        (s > 1 ? join_us(s * M * cols) : 0.0);
       if (us < least) {
         least = us;
         best = {t, s};
@@ -590,174 +685,256 @@ Choice choose(int64_t M, int64_t cols, int nkt, bool a_by_cols) {
   return best;
 }
 
-template <bool ACOL, bool BCOL, int EPI>
-int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
-  const Choice c = choose(p.M, partial_cols(p, EPI), (p.K + 63) / 64, ACOL);
-  if (c.tile == 0) return gemm_tiles<256, 256, 2, 4, 2, ACOL, BCOL, EPI>(p, c.splits, partial, st);
-  if (c.tile == 1) return gemm_tiles<128, 128, 2, 2, 2, ACOL, BCOL, EPI>(p, c.splits, partial, st);
-  if constexpr (!ACOL) {
-    if (c.tile == 3) return gemm_tiles<64, 128, 2, 2, 3, ACOL, BCOL, EPI>(p, c.splits, partial, st);
-  }
-  return gemm_tiles<128, 128, 2, 2, 4, ACOL, BCOL, EPI>(p, c.splits, partial, st);
+// The same for the three gradients of one launch: the tile for all of them and each one's splits, towards sums of equal
+// lengths.  Their workgroups fill the CUs one after another, so their times add up, but for the last one to start.
+Choice choose_grads(const Gemm* const (&p)[3], int (&splits)[3]) {
+  double least = 1e30;
+  Choice best{0, 1};
+  int64_t longest = 1;
+  for (const Gemm* g : p) longest = std::max<int64_t>(longest, (g->K + 63) / 64);
+  for (int t = 0; t < 3; ++t)
+    for (int64_t len = longest; len >= 4 || len == longest; len = len * 3 / 4) {  // k-tiles of a sum, at most
+      double work = 0, last = 0;
+      int64_t floats = 0, n = 0;
+      int sp[3];
+      bool any = false;
+      for (int i = 0; i < 3; ++i) {
+        const int64_t nkt = (p[i]->K + 63) / 64, cols = partial_cols(*p[i], EPI_STORE);
+        int64_t s = std::min<int64_t>(MAX_SPLITS, (nkt + len - 1) / len);
+        if (s > 1 && (nkt / s < 4 || floats + s * p[i]->M * cols > PARTIAL)) s = 1;
+        if (s > 1) floats += s * p[i]->M * cols;
+        sp[i] = (int)s;
+        any |= s > 1;
+        const int64_t tiles = tiles_of(t, p[i]->M, cols) * s;
+        const double kt = (double)((nkt + s - 1) / s);
+        n += tiles;
+        work += tiles * (kt * TILES[t].full + TILES[t].fixed);
+        last = std::max(last, kt * TILES[t].alone + TILES[t].fixed);
+      }
+      const int64_t slots = 256 * TILES[t].per_cu;
+      const double us = (n <= 256 ? last : std::max(last, work / slots + 0.4 * last)) + (any ? join_us(floats) : 0.0);
+      if (us < least) {
+        least = us;
+        best.tile = t;
+        for (int i = 0; i < 3; ++i) splits[i] = sp[i];
+      }
+      if (len <= 4) break;
+    }
+  return best;
 }
 
-// ---- fp32, any sizes --------------------------------------------------------------------------------------------------
-// A 128 x 64 tile of C (GLU: 32 columns of the gate and the same 32 of the up projection) by four waves of 32 x 64, in
-// k-tiles of 16: each operand's k-tile is loaded by elements of its own layout into registers one k-tile ahead and kept in
-// LDS as [k][m], from where a lane takes one element of A and two of B for two 32x32x2 products.
-constexpr int GM = 128, GN = 64, GK = 16, GSUM = 256;
+template <bool BCOL, int EPI>
+int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
+  const Choice c = choose(p.M, partial_cols(p, EPI), (p.K + 63) / 64);
+  if (c.tile == 0) return gemm_tiles<256, 256, 2, 4, 2, BCOL, EPI>(p, c.splits, partial, st);
+  if (c.tile == 1) return gemm_tiles<128, 128, 2, 2, 2, BCOL, EPI>(p, c.splits, partial, st);
+  if (c.tile == 2) return gemm_tiles<128, 128, 2, 2, 4, BCOL, EPI>(p, c.splits, partial, st);
+  return gemm_tiles<64, 128, 2, 2, 3, BCOL, EPI>(p, c.splits, partial, st);
+}
+
+int grads_bf16(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
+  int splits[3];
+  const Choice c = choose_grads(p, splits);
+  if (c.tile == 0) return grads_tiles<256, 256, 2, 4, 2>(p, splits, partial, st);
+  if (c.tile == 1) return grads_tiles<128, 128, 2, 2, 2>(p, splits, partial, st);
+  return grads_tiles<128, 128, 2, 2, 4>(p, splits, partial, st);
+}
+
+// ---- fp32 --------------------------------------------------------------------------------------------------------------
+// A 64 x 64 tile of C (GLU: 32 columns of the gate and the same 32 of the up projection) by four waves of 32 x 32, with
+// 16x16x4 fp32 products in k-tiles of 32.  A k-tile is loaded into registers two k-tiles ahead and kept in LDS as rows of k
+// for either layout of an operand, from which a lane takes 16 bytes for four products at once (which k meet in which
+// product does not matter as long as both operands agree).  The tile is small so that four workgroups share a CU and hide
+// each other's latency.  The products take C's columns as their rows, which leaves a lane four neighbouring columns.
+constexpr int FK = 32, FLD = FK + 4;  // rows 144 bytes apart: the 16 lanes of a read phase hit 64 distinct banks
+constexpr int FSUM = 256;             // k of a partial sum: one running sum over thousands would lose a few bits
+
+struct F32Stage {
+  float a[2][64][FLD], b[2][64][FLD];
+};
 
 template <int EPI, bool ACOL, bool BCOL>
-__global__ __launch_bounds__(256) void k_gemm_f32(Gemm p) {
-  __shared__ float sa[2][GK][GM + 4], sb[2][GK][GN + 4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  constexpr int BN = EPI == EPI_GLU ? GN / 2 : GN;
-  const int nt = (p.N + BN - 1) / BN;
-  const int m0 = (int)(blockIdx.x / nt) * GM, n0 = (int)(blockIdx.x % nt) * BN;
+__device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
+  const Gemm& p = part.p;
+  auto& sa = sh.a;
+  auto& sb = sh.b;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+  constexpr int BN = EPI == EPI_GLU ? 32 : 64;
+  const int nt = (p.N + BN - 1) / BN, tiles = (p.M + 63) / 64 * nt, nkt = (p.K + FK - 1) / FK;
+  const int i0 = blockIdx.x - part.first, s = i0 / tiles, tile = i0 % tiles;
+  const int m0 = tile / nt * 64, n0 = tile % nt * BN;
+  const int t0 = (int)((int64_t)nkt * s / part.splits), t1 = (int)((int64_t)nkt * (s + 1) / part.splits);
   const float *A = (const float*)p.a, *B = (const float*)p.b;
 
-  // thread -> four neighbours along memory: by rows (row tid / 4, k 4 (tid % 4)), by columns (k tid / 16 or 32, m ..)
-  float ra[8], rb[4];
-  auto load_a = [&](int k0) {
+  // eight neighbours along memory per thread and operand: by rows, k 8 (tid % 4) .. of row tid / 4; by columns, rows
+  // 4 (tid % 16) .. of k tid / 16 and tid / 16 + 16.  Outside the matrix: 0
+  f32x4_t rega[2][2], regb[2][2];  // of two k-tiles: a load has two k-tiles' time to arrive
+  auto four = [&](const float* q, int c, int limit, int seg, int jump) {  // contiguous elements c .. c + 3 < limit at q
+    if (c + 4 <= limit && (c >= seg || c + 4 <= seg)) return load4(q + c + (c >= seg ? jump : 0), 4);
+    f32x4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < limit) v[i] = q[c + i + (c + i >= seg ? jump : 0)];
+    return v;
+  };
+  // a k-tile that ends before the last k and does not straddle a_seg: whole fours from a lane's fixed places.  Rows past the
+  // matrix read its first; columns past it read the next row (the last k is not in such a k-tile); neither is stored
+  const int ca = m0 + 4 * (tid & 15), cb = n0 + 4 * (tid & 15), row = tid >> 2;
+  const float* pa = ACOL ? A + (int64_t)(tid >> 4) * p.lda + (ca < p.M ? ca : 0)
+                         : A + (int64_t)(m0 + row < p.M ? m0 + row : 0) * p.lda + 8 * (tid & 3);
+  const int rb_row = n0 + (row & (BN - 1));
+  const float* pb = BCOL ? B + (int64_t)(tid >> 4) * p.ldb + (cb < p.N ? cb : 0)
+                         : B + ((rb_row < p.N ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
+  const bool wide = p.lda >= 4 && p.ldb >= 4;
+  auto fetch = [&](int kt, f32x4_t* ra, f32x4_t* rb) {
+    const f32x4_t zero = {0, 0, 0, 0};
+    const int k0 = kt * FK;
+    if (wide && k0 + FK < p.K && (ACOL || k0 >= p.a_seg || k0 + FK <= p.a_seg)) {
+      const float* qa = pa + (ACOL ? (int64_t)k0 * p.lda : k0 + (k0 >= p.a_seg ? p.a_jump : 0));
+      const float* qb = pb + (BCOL ? (int64_t)k0 * p.ldb : k0);
+      ra[0] = load4(qa, 4);
+      ra[1] = load4(qa + (ACOL ? 16 * p.lda : 4), 4);
+      rb[0] = load4(qb, 4);
+      rb[1] = load4(qb + (BCOL ? 16 * p.ldb : 4), 4);
+      return;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int m, k;
-        if (ACOL) {
-          k = k0 + (tid >> 5) + 8 * h;
-          m = m0 + (tid & 31) * 4 + i;
-        } else {
-          m = m0 + (tid >> 2) + 64 * h;
-          k = k0 + (tid & 3) * 4 + i;
-        }
-        float v = 0.f;
-        if (m < p.M && k < p.K) {
-          const int c = ACOL ? m : k;
-          v = (A[(int64_t)(ACOL ? k : m) * p.lda + c + (c >= p.a_seg ? p.a_jump : 0)]);
-        }
-        ra[4 * h + i] = v;
-      }
-    }
-  };
-  auto load_b = [&](int k0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      int n, k;
-      if (BCOL) {
-        k = k0 + (tid >> 4);
-        n = (tid & 15) * 4 + i;
+      if (ACOL) {
+        const int k = kt * FK + (tid >> 4) + 16 * h;
+        ra[h] = k < p.K ? four(A + (int64_t)k * p.lda, ca, p.M, 0x7fffffff, 0) : zero;
       } else {
-        n = tid >> 2;
-        k = k0 + (tid & 3) * 4 + i;
+        const int m = m0 + (tid >> 2);
+        ra[h] = m < p.M ? four(A + (int64_t)m * p.lda, kt * FK + 8 * (tid & 3) + 4 * h, p.K, p.a_seg, p.a_jump) : zero;
       }
-      int64_t row = n0 + n;
-      bool in = row < p.N;
-      if (EPI == EPI_GLU) {
-        const int c = n0 + (n & (BN - 1));
-        in = c < p.N;
-        row = n < BN ? c : (int64_t)p.up + c;
+      if (BCOL) {
+        const int k = kt * FK + (tid >> 4) + 16 * h;
+        rb[h] = k < p.K ? four(B + (int64_t)k * p.ldb, cb, p.N, 0x7fffffff, 0) : zero;
+      } else {
+        const int64_t at = rb_row + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0);
+        rb[h] = rb_row < p.N ? four(B + at * p.ldb, kt * FK + 8 * (tid & 3) + 4 * h, p.K, 0x7fffffff, 0) : zero;
       }
-      rb[i] = in && k < p.K ? (B[BCOL ? (int64_t)k * p.ldb + row : row * p.ldb + k]) : 0.f;
     }
   };
-  auto keep = [&](int s) {
+  auto keep = [&](int st, const f32x4_t* ra, const f32x4_t* rb) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+      if (ACOL) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (ACOL) sa[s][(tid >> 5) + 8 * h][(tid & 31) * 4 + i] = ra[4 * h + i];
-        else sa[s][(tid & 3) * 4 + i][(tid >> 2) + 64 * h] = ra[4 * h + i];
-      }
+        for (int i = 0; i < 4; ++i) sa[st][4 * (tid & 15) + i][(tid >> 4) + 16 * h] = ra[h][i];
+      } else *(f32x4_t*)&sa[st][tid >> 2][8 * (tid & 3) + 4 * h] = ra[h];
+      if (BCOL) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (BCOL) sb[s][tid >> 4][(tid & 15) * 4 + i] = rb[i];
-      else sb[s][(tid & 3) * 4 + i][tid >> 2] = rb[i];
+        for (int i = 0; i < 4; ++i) sb[st][4 * (tid & 15) + i][(tid >> 4) + 16 * h] = rb[h][i];
+      } else *(f32x4_t*)&sb[st][tid >> 2][8 * (tid & 3) + 4 * h] = rb[h];
     }
   };
 
-  // sums of GSUM k each, added up: one running sum over thousands of products would lose a few bits that sums of sums keep
-  f32x16_t acc[2], total[2];
+  // [16 columns of C (GLU: of the gate, of the up projection)][16 rows]
+  f32x4_t acc[2][2], total[2][2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int q = 0; q < 16; ++q) acc[j][q] = total[j][q] = 0.f;
-  const int nk = (p.K + GK - 1) / GK;
-  if (nk > 0) {
-    load_a(0);
-    load_b(0);
-    keep(0);
-  }
-  for (int kt = 0; kt < nk; ++kt) {
+    for (int i = 0; i < 2; ++i) acc[j][i] = total[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int r = lane & 15, q = lane >> 4;
+  const int brow[2] = {EPI == EPI_GLU ? wn * 16 : wn * 32, EPI == EPI_GLU ? 32 + wn * 16 : wn * 32 + 16};
+  auto ktile = [&](auto parity, int kt) {  // stage and registers of k-tile kt - t0 even or odd
+    constexpr int st = decltype(parity)::value;
     __syncthreads();
-    const int s = kt & 1;
-    if (kt + 1 < nk) {
-      load_a((kt + 1) * GK);
-      load_b((kt + 1) * GK);
-    }
+    if (kt + 2 < t1) fetch(kt + 2, rega[st], regb[st]);
 #pragma unroll
-    for (int k = 0; k < GK; k += 2) {
-      const float a = sa[s][k + (lane >> 5)][wave * 32 + (lane & 31)];
+    for (int k = 0; k < FK; k += 16) {
+      f32x4_t a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = *(const f32x4_t*)&sa[st][wm * 32 + i * 16 + r][k + 4 * q];
+        b[i] = *(const f32x4_t*)&sb[st][brow[i] + r][k + 4 * q];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[j][e], a[i][e], acc[j][i], 0, 0, 0);
+    }
+    if (kt + 1 < t1) keep(st ^ 1, rega[st ^ 1], regb[st ^ 1]);  // its last readers passed this k-tile's barrier
+    if (kt % (FSUM / FK) == FSUM / FK - 1 || kt + 1 == t1) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, sb[s][k + (lane >> 5)][j * 32 + (lane & 31)], acc[j], 0, 0, 0);
-    }
-    if (kt + 1 < nk) keep(s ^ 1);  // its last readers passed this k-tile's barrier
-    if (kt % (GSUM / GK) == GSUM / GK - 1 || kt + 1 == nk) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          total[j][q] += acc[j][q];
-          acc[j][q] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          total[j][i] += acc[j][i];
+          acc[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
     }
+  };
+  if (t0 < t1) {
+    fetch(t0, rega[0], regb[0]);
+    if (t0 + 1 < t1) fetch(t0 + 1, rega[1], regb[1]);
+    keep(0, rega[0], regb[0]);
   }
-
-  // element q of an accumulator: row 8 (q / 4) + 4 (lane / 32) + q % 4, column lane % 32
+  for (int kt = t0; kt < t1; kt += 2) {
+    ktile(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < t1) ktile(std::integral_constant<int, 1>{}, kt + 1);
+  }
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int m = m0 + wave * 32 + 8 * (q >> 2) + 4 * (lane >> 5) + (q & 3);
-    if (m >= p.M) continue;
-    if (EPI == EPI_GLU) {
-      const int n = n0 + (lane & 31);
-      if (n >= p.N) continue;
-      const float g = total[0][q], u = total[1][q];
-      ((float*)p.c)[m * p.ldc + n] = g / (1.0f + __expf(-g)) * u;
-      if (p.gu) {
-        float* o = p.gu + m * p.ldgu + n;
-        o[0] = g;
-        o[p.half] = u;
-      }
-      continue;
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int m = m0 + wm * 32 + i * 16 + r;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int n = n0 + j * 32 + (lane & 31);
-      if (n >= p.N) continue;
-      if (EPI == EPI_DGLU) {
-        const float* i = p.gu + m * p.ldgu + n;
-        float dg, du;
-        dglu(total[j][q], i[0], i[p.half], &dg, &du);
-        float* o = (float*)p.c + m * p.ldc + n;
-        o[0] = dg;
-        o[p.half] = du;
-      } else {
-        const int64_t at = m * p.ldc + n;
-        ((float*)p.c)[at] = total[j][q] + (p.residual ? ((const float*)p.residual)[at] : 0.f);
-      }
+    for (int j = 0; j < (EPI == EPI_GLU ? 1 : 2); ++j) {
+      const int n = n0 + brow[j] + 4 * q;
+      if (m >= p.M || n >= p.N) continue;
+      if (part.partial) {
+        float* o = part.partial + ((int64_t)s * p.M + m) * part.ld + n;
+        *(f32x4_t*)o = total[j][i];
+        if (EPI == EPI_GLU) *(f32x4_t*)(o + part.ld / 2) = total[1][i];
+      } else finish4<float, EPI>(p, m, n, total[j][i], total[1][i]);
     }
   }
 }
 
-template <int EPI, bool ACOL, bool BCOL>
-int gemm_f32(const Gemm& p, hipStream_t st) {
-  if (p.M == 0) return 0;
-  constexpr int BN = EPI == EPI_GLU ? GN / 2 : GN;
-  const int64_t tiles = (int64_t)((p.M + GM - 1) / GM) * ((p.N + BN - 1) / BN);
-  if (tiles > 0x7fffffff) return -1;
-  hipLaunchKernelGGL((k_gemm_f32<EPI, ACOL, BCOL>), dim3((unsigned)tiles), dim3(256), 0, st, p);
-  return hipGetLastError() == hipSuccess ? 0 : -1;
+template <int EPI, bool BCOL>
+__global__ __launch_bounds__(256) void k_gemm_f32(Part a) {
+  __shared__ __align__(16) F32Stage sh;
+  f32_tile<EPI, false, BCOL>(a, sh);
+}
+
+__global__ __launch_bounds__(256) void k_grads_f32(Parts a) {
+  __shared__ __align__(16) F32Stage sh;
+  const int i = blockIdx.x;
+  auto mine = [&](const Part& q) { return i >= q.first && i < q.first + q.blocks; };
+  if (mine(a.part[0])) f32_tile<EPI_STORE, false, true>(a.part[0], sh);
+  else if (mine(a.part[1]) || mine(a.part[2])) f32_tile<EPI_STORE, true, true>(a.part[mine(a.part[1]) ? 1 : 2], sh);
+}
+
+// splits of a product of which a launch has `tiles` tiles in all: up to four workgroups for each CU, of 256 k at least
+int f32_splits(const Gemm& p, int epi, int64_t tiles, int64_t room) {
+  return (int)std::max<int64_t>(1, std::min(std::min(1024 / tiles, room / (p.M * partial_cols(p, epi))), std::min<int64_t>(MAX_SPLITS, p.K / 256)));
+}
+
+template <int EPI, bool BCOL>
+int gemm_f32(const Gemm& p, float* partial, hipStream_t st) {
+  Part a;
+  if (!make_part(&a, p, EPI, 64, 64, 1, partial, 0)) return -1;
+  if (!make_part(&a, p, EPI, 64, 64, f32_splits(p, EPI, a.blocks, PARTIAL), partial, 0)) return -1;
+  hipLaunchKernelGGL((k_gemm_f32<EPI, BCOL>), dim3((unsigned)a.blocks), dim3(256), 0, st, a);
+  if (hipGetLastError() != hipSuccess) return -1;
+  return launch_finish<float, EPI>(a, st);
+}
+
+int grads_f32(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
+  Parts g;
+  int64_t blocks, room = PARTIAL;
+  int splits[3] = {1, 1, 1};
+  if (!make_grads(&g, p, 64, 64, splits, partial, &blocks)) return -1;
+  for (int i = 0; i < 3; ++i) {
+    if (p[i]->M > 0) splits[i] = f32_splits(*p[i], EPI_STORE, blocks, room);
+    if (splits[i] > 1) room -= splits[i] * p[i]->M * partial_cols(*p[i], EPI_STORE);
+  }
+  if (!make_grads(&g, p, 64, 64, splits, partial, &blocks)) return -1;
+  hipLaunchKernelGGL(k_grads_f32, dim3((unsigned)blocks), dim3(256), 0, st, g);
+  if (hipGetLastError() != hipSuccess) return -1;
+  return launch_finish_grads<float>(g, st);
 }
 
 // ---- the block --------------------------------------------------------------------------------------------------
@@ -836,7 +1013,7 @@ Block block_f32(const SharedLaunch& s) {
   b.down = {s.h, s.w_down, F, f, none, 0, T, d, f, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
   b.dglu = {s.dy, s.w_down, d, f, none, 0, T, f, d, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
   b.dx = {s.dgu, s.w_gate_up, 2 * F, d, f, F - f, T, d, 2 * f, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
-  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, f, F - f, 2 * f, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, none, none};
+  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, none, 0, 2 * F, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
   b.dw_down = {s.dy, s.h, d, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
   return b;
 }
@@ -855,19 +1032,18 @@ Block block_bf16(const SharedLaunch& s, const void* x, const void* wgu, const vo
 
 int run_f32(const SharedLaunch& s, hipStream_t st) {
   const Block b = block_f32(s);
+  float* partial = (float*)s.workspace;
   int rc;
   if (!s.backward) {
     if (s.tokens <= FEW) {
       if ((rc = gemm_few<float, EPI_GLU>(b.glu, st))) return rc;
       return gemm_few<float, EPI_STORE>(b.down, st);
     }
-    if ((rc = gemm_f32<EPI_GLU, false, false>(b.glu, st))) return rc;
-    return gemm_f32<EPI_STORE, false, false>(b.down, st);
+    if ((rc = gemm_f32<EPI_GLU, false>(b.glu, partial, st))) return rc;
+    return gemm_f32<EPI_STORE, false>(b.down, partial, st);
   }
-  if ((rc = gemm_f32<EPI_DGLU, false, true>(b.dglu, st))) return rc;
-  if ((rc = gemm_f32<EPI_STORE, false, true>(b.dx, st))) return rc;
-  if ((rc = gemm_f32<EPI_STORE, true, true>(b.dw_gate_up, st))) return rc;
-  return gemm_f32<EPI_STORE, true, true>(b.dw_down, st);
+  if (s.tokens > 0 && (rc = gemm_f32<EPI_DGLU, true>(b.dglu, partial, st))) return rc;
+  return grads_f32({&b.dx, &b.dw_gate_up, &b.dw_down}, partial, st);
 }
 
 int run_bf16(const SharedLaunch& s, hipStream_t st) {
@@ -904,21 +1080,19 @@ int run_bf16(const SharedLaunch& s, hipStream_t st) {
   float* partial = (float*)to;
   const Block b = block_bf16(s, op[0], op[1], op[2], op[3]);
   if (!s.backward) {
-    if ((rc = gemm_bf16<false, false, EPI_GLU>(b.glu, partial, st))) return rc;
-    return gemm_bf16<false, false, EPI_STORE>(b.down, partial, st);
+    if ((rc = gemm_bf16<false, EPI_GLU>(b.glu, partial, st))) return rc;
+    return gemm_bf16<false, EPI_STORE>(b.down, partial, st);
   }
-  if ((rc = gemm_bf16<false, true, EPI_DGLU>(b.dglu, partial, st))) return rc;
-  if ((rc = gemm_bf16<false, true, EPI_STORE>(b.dx, partial, st))) return rc;
-  if ((rc = gemm_bf16<true, true, EPI_STORE>(b.dw_gate_up, partial, st))) return rc;
-  return gemm_bf16<true, true, EPI_STORE>(b.dw_down, partial, st);
+  if ((rc = gemm_bf16<true, EPI_DGLU>(b.dglu, partial, st))) return rc;
+  return grads_bf16({&b.dx, &b.dw_gate_up, &b.dw_down}, partial, st);
 }
 
 }  // namespace
 
 int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool backward) {
-  if (dtype != MOE_BF16 || tokens == 0) return 0;
-  int64_t n[4];
-  pack_sizes(tokens, d, f, backward, n);
+  if (tokens == 0) return 0;
+  int64_t n[4] = {0, 0, 0, 0};
+  if (dtype == MOE_BF16) pack_sizes(tokens, d, f, backward, n);
   // the k-splits' sums: at most PARTIAL floats, and MAX_SPLITS times the largest product
   const int64_t out = backward ? std::max(std::max(tokens * up8(d), tokens * up8(f)), 2 * up8(f) * up8(d))
                                : std::max(tokens * up8(d), tokens * 2 * up8(f));

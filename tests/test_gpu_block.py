@@ -195,6 +195,32 @@ def test_shared_ffn_in_place_and_fewer_tokens(T, d, f, dtype):
     assert (op.y == 7).all() and (op.dx == 7).all()
 
 
+@pytest.mark.parametrize("d,f", [(100, 36), (7, 9), (104, 41), (65, 8)])
+@pytest.mark.parametrize("T,dtype", [(2, "bf16"), (70, "bf16"), (40, "f32")])
+def test_shared_ffn_writes_only_its_outputs(T, d, f, dtype):
+    """Outputs inside larger buffers: what lies before and behind them stays (odd widths, whose padding has no place)."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, dtype, seed=6)
+    op = SharedFFN(T, d, f, dtype)
+    wide = []
+
+    def inside(t):
+        at = torch.full((t.numel() + 8192,), 7.0, dtype=t.dtype, device="cuda")
+        wide.append((at, 4096, t.numel()))
+        return at[4096: 4096 + t.numel()].view(t.shape)
+
+    op.y, op.dx, op.dw_gate_up, op.dw_down, op.h, op.gu, op.dgu = (
+        inside(t) for t in (op.y, op.dx, op.dw_gate_up, op.dw_down, op.h, op.gu, op.dgu))
+    op.forward(x, wgu, wd)
+    op.backward(dy, x, wgu, wd, residual=res)
+    for at, a, n in wide:
+        assert (at[:a] == 7).all() and (at[a + n:] == 7).all()
+    want = ref.shared_ffn(x, wgu, wd, residual=res, dy=dy)
+    check({"y": op.y, "dx": op.dx, "dw_gate_up": op.dw_gate_up, "dw_down": op.dw_down}, want,
+          ("y", "dx", "dw_gate_up", "dw_down"), (T, d, f, dtype))
+
+
 def test_shared_ffn_of_nothing():
     from expert_output_overlap_amd.runtime import SharedFFN
 
