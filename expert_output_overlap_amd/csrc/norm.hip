@@ -7,6 +7,7 @@
 // for all of a group's rows (as fp32 they are four times the bytes of a bf16 row: re-reading them through the L2 for every
 // row would cost more than the row itself).
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "launch.h"
@@ -64,10 +65,35 @@ struct Chunk {  // elements of one 16-byte chunk
   }
 };
 
-template <typename PT>
-__device__ __forceinline__ float param(const PT* p, int i) {
-  if (sizeof(PT) == 4) return *(const float*)(p + i);
-  return bf16_to_f32(*(const bf16_t*)(p + i));
+// N parameters from index i on, `empty` where there are none (no parameters, or past d)
+template <typename PT, int N>
+__device__ __forceinline__ void params(const PT* p, int i, int d, float empty, float* out) {
+  constexpr int C = Chunk<PT>::C;
+#pragma unroll
+  for (int k = 0; k < N; k += C) {
+    constexpr int M = N < C ? N : C;
+    u32x4 v = {0, 0, 0, 0};
+    const int n = d - i - k;
+    if (p && n > 0) v = Chunk<PT>::load(p + i + k, n < M ? n : M);
+#pragma unroll
+    for (int e = 0; e < M; ++e) out[k + e] = p && e < n ? Chunk<PT>::at(v, e) : empty;
+  }
+}
+
+// The wave's sum in every lane: shifts inside rows of 16 lanes, then over the rows (DPP moves instead of trips through LDS)
+__device__ __forceinline__ float lanes_sum(float v) {
+  auto dpp = [](float x, auto ctrl, auto rows) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value,
+                                                                 decltype(rows)::value, 0xf, false));
+  };
+  using all = std::integral_constant<int, 0xf>;
+  v += dpp(v, std::integral_constant<int, 0x111>{}, all{});  // row_shr 1, 2, 4, 8
+  v += dpp(v, std::integral_constant<int, 0x112>{}, all{});
+  v += dpp(v, std::integral_constant<int, 0x114>{}, all{});
+  v += dpp(v, std::integral_constant<int, 0x118>{}, all{});
+  v += dpp(v, std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast 15 into rows 1, 3
+  v += dpp(v, std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast 31 into rows 2, 3
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
 // Sums of N values over a group of G threads: over the wave, then over the group's waves through LDS.  `buf` alternates
@@ -75,7 +101,7 @@ __device__ __forceinline__ float param(const PT* p, int i) {
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* buf) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) v[n] = wave_sum_f(v[n]);
+  for (int n = 0; n < N; ++n) v[n] = lanes_sum(v[n]);
   if (G > 64) {
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -101,13 +127,10 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_norm(NormLaunch a) {
   float w[NV * C], b[NV * C];
   const PT *wp = (const PT*)a.weight, *bp = (const PT*)a.bias;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (j * G + t) * C + i;
-      w[j * C + i] = c < d ? (wp ? param(wp, c) : 1.f) : 0.f;
-      b[j * C + i] = c < d && bp ? param(bp, c) : 0.f;
-    }
+  for (int j = 0; j < NV; ++j) {
+    params<PT, C>(wp, (j * G + t) * C, d, 1.f, w + j * C);
+    params<PT, C>(bp, (j * G + t) * C, d, 0.f, b + j * C);
+  }
   const int64_t step = (int64_t)gridDim.x * PER;
   int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / G;
   u32x4 next[NV];
@@ -177,13 +200,11 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_norm_bwd(NormLaunch a) {
   const PT* wp = (const PT*)a.weight;
   float w[NV * C], dw[NV * C], db[NV * C];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    params<PT, C>(wp, (j * G + t) * C, d, 1.f, w + j * C);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int c = (j * G + t) * C + i;
-      w[j * C + i] = c < d ? (wp ? param(wp, c) : 1.f) : 0.f;
-      dw[j * C + i] = db[j * C + i] = 0.f;
-    }
+    for (int i = 0; i < C; ++i) dw[j * C + i] = db[j * C + i] = 0.f;
+  }
   const int64_t step = (int64_t)gridDim.x * PER;
   int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / G;
   u32x4 nx[NV], ny[NV];
@@ -282,83 +303,92 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_norm_bwd(NormLaunch a) {
   }
 }
 
-// dweight | dbias from the workgroups' partial sums: 64 columns per workgroup, its four waves take every fourth partial
-// row, and their sums are added in wave order.
+// dweight | dbias from the workgroups' partial sums: 64 columns per workgroup, its 16 waves take every 16th partial row, and
+// their sums are added in wave order.
 template <typename PT>
-__global__ __launch_bounds__(256) void k_norm_params(const float* __restrict__ partial, int n, int d, PT* dweight,
-                                                     PT* dbias) {
-  __shared__ float red[3][64];
+__global__ __launch_bounds__(1024) void k_norm_params(const float* __restrict__ partial, int n, int d, PT* dweight,
+                                                      PT* dbias) {
+  __shared__ float red[15][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
   float s = 0.f;
   if (c < 2 * d) {
     const float* p = partial + c;
-    int k = wave;
-    for (; k + 28 < n; k += 32) {
+    for (int k = wave; k < n; k += 128) {
       float v[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = p[(int64_t)(k + 4 * u) * 2 * d];
+      for (int u = 0; u < 8; ++u) v[u] = k + 16 * u < n ? p[(int64_t)(k + 16 * u) * 2 * d] : 0.f;
 #pragma unroll
       for (int u = 0; u < 8; ++u) s += v[u];
     }
-    for (; k < n; k += 4) s += p[(int64_t)k * 2 * d];
   }
   if (wave > 0) red[wave - 1][lane] = s;
   __syncthreads();
   if (wave > 0 || c >= 2 * d) return;
-  for (int k = 0; k < 3; ++k) s += red[k][lane];
+  for (int k = 0; k < 15; ++k) s += red[k][lane];
   PT* out = c < d ? dweight : dbias;
   if (!out) return;
   if (sizeof(PT) == 4) *(float*)(out + (c < d ? c : c - d)) = s;
   else *(bf16_t*)(out + (c < d ? c : c - d)) = f32_to_bf16(s);
 }
 
-template <typename T, typename PT, int G, int NV>
+template <bool BWD, typename T, typename PT, int G, int NV>
 void go(const NormLaunch& a, int64_t groups, hipStream_t st) {
   constexpr int PER = G < 256 ? 256 / G : 1;
   const dim3 grid((unsigned)((groups + PER - 1) / PER)), block(G < 256 ? 256 : G);
-  if (a.backward) hipLaunchKernelGGL((k_norm_bwd<T, PT, G, NV>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_norm<T, PT, G, NV>), grid, block, 0, st, a);
+  if constexpr (!BWD) hipLaunchKernelGGL((k_norm<T, PT, G, NV>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_norm_bwd<T, PT, G, NV>), grid, block, 0, st, a);
 }
 
 template <typename T, typename PT>
 void pick(const NormLaunch& a, int G, int NV, int64_t groups, hipStream_t st) {
-  if (G == 64 && NV == 1) go<T, PT, 64, 1>(a, groups, st);
-  else if (G == 64 && NV == 2) go<T, PT, 64, 2>(a, groups, st);
-  else if (G == 64) go<T, PT, 64, 4>(a, groups, st);
-  else if (G == 256 && NV == 2) go<T, PT, 256, 2>(a, groups, st);
-  else if (G == 256) go<T, PT, 256, 4>(a, groups, st);
-  else if (NV == 2) go<T, PT, 1024, 2>(a, groups, st);
-  else go<T, PT, 1024, 4>(a, groups, st);
+  auto both = [&](auto g, auto nv) {
+    if (a.backward) go<true, T, PT, decltype(g)::value, decltype(nv)::value>(a, groups, st);
+    else go<false, T, PT, decltype(g)::value, decltype(nv)::value>(a, groups, st);
+  };
+  using std::integral_constant;
+  if (G == 64 && NV == 1) both(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (G == 64) both(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else if (G == 256 && NV == 1) both(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  else if (G == 256 && NV == 2) both(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  else if (G == 256) go<false, T, PT, 256, 4>(a, groups, st);
+  else if (G == 1024) go<true, T, PT, 1024, 1>(a, groups, st);
+  else if (NV == 4) both(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  else if constexpr (sizeof(T) == 4) both(integral_constant<int, 512>{}, integral_constant<int, 8>{});  // bf16: 2048 chunks
 }
 
-// Group size and chunks per thread for a row: the smallest that holds it (up to 256, 1024 and 4096 chunks)
-void plan(int d, int dtype, int* G, int* NV) {
+// Group size and chunks per thread for a row.  In the backward few chunks per thread, since it keeps three fp32 values per
+// element besides the row: 16384 bf16 rows of 7168 take 263 us by 256 threads of four chunks, 221 by 512 of two and 194 (4.85
+// TB/s) by 1024 of one.  In the forward the fewer waves of a smaller group's sums are worth more: 103 us (4.6 TB/s) by 256
+// threads of four, 110 by 512 of two, 160 by 1024 of one.
+void plan(int d, int dtype, bool backward, int* G, int* NV) {
   const int chunks = (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16;
-  *G = chunks <= 256 ? 64 : chunks <= 1024 ? 256 : 1024;
+  *G = chunks <= 128 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? (backward ? 1024 : 256) : 512;
   const int per = (chunks + *G - 1) / *G;
-  *NV = per <= 1 && *G == 64 ? 1 : per <= 2 ? 2 : 4;
+  *NV = per <= 2 ? per : per <= 4 ? 4 : 8;
 }
 
-// Groups of a launch, for 256 CUs: a thread holds a row's chunks twice (the next row's are in flight), so a CU takes about
-// 8 waves of the backward and 16 of the forward.
-int64_t norm_groups(int64_t rows, int G, bool backward) {
-  const int64_t most = 256ll * (backward ? 8 : 16) * 64 / G;
-  return std::min(rows, std::max<int64_t>(most, 1));
+// Groups of a launch on 256 CUs: about as many as their registers leave room for at once, so that a group's parameters are
+// read once for many rows and its sums written once.
+int64_t norm_groups(int64_t rows, int G, int NV, bool backward) {
+  const int waves = backward ? (NV == 1 ? 32 : NV == 2 ? 16 : 8) : (NV <= 2 ? 64 : 24);  // of a CU
+  const int64_t most = 256ll * waves * 64 / G;
+  // backward: four rows for each group's sums, while that leaves a group for every CU
+  return std::min(backward ? std::max(rows / 4, std::min<int64_t>(rows, 256)) : rows, most);
 }
 
 }  // namespace
 
 int64_t norm_partial_floats(int64_t rows, int d, int dtype) {
   int G, NV;
-  plan(d, dtype, &G, &NV);
+  plan(d, dtype, true, &G, &NV);
   const int64_t per = G < 256 ? 256 / G : 1;
-  return (norm_groups(rows, G, true) + per - 1) / per * 2 * d;
+  return (norm_groups(rows, G, NV, true) + per - 1) / per * 2 * d;
 }
 
 int launch_norm(const NormLaunch& a, hipStream_t st) {
   int G, NV;
-  plan(a.d, a.dtype, &G, &NV);
-  const int64_t groups = norm_groups(a.rows, G, a.backward);
+  plan(a.d, a.dtype, a.backward, &G, &NV);
+  const int64_t groups = norm_groups(a.rows, G, NV, a.backward);
   const bool tb = a.dtype == MOE_BF16, pb = a.param_dtype == MOE_BF16;
   if (a.rows > 0) {
     if (tb && pb) pick<bf16_t, bf16_t>(a, G, NV, groups, st);
@@ -371,10 +401,10 @@ int launch_norm(const NormLaunch& a, hipStream_t st) {
     const int n = (int)((groups + per - 1) / per);
     const dim3 grid((unsigned)((2 * a.d + 63) / 64));
     if (pb)
-      hipLaunchKernelGGL(k_norm_params<bf16_t>, grid, dim3(256), 0, st, a.partial, n, a.d, (bf16_t*)a.dweight,
+      hipLaunchKernelGGL(k_norm_params<bf16_t>, grid, dim3(1024), 0, st, a.partial, n, a.d, (bf16_t*)a.dweight,
                          (bf16_t*)a.dbias);
     else
-      hipLaunchKernelGGL(k_norm_params<float>, grid, dim3(256), 0, st, a.partial, n, a.d, (float*)a.dweight,
+      hipLaunchKernelGGL(k_norm_params<float>, grid, dim3(1024), 0, st, a.partial, n, a.d, (float*)a.dweight,
                          (float*)a.dbias);
   }
   return hipGetLastError() == hipSuccess ? 0 : -1;

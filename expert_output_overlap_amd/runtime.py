@@ -6,6 +6,7 @@ route -> layout -> expert FFN with return -> combine.  Nothing here computes any
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -182,6 +183,19 @@ def _device(device) -> torch.device:
     return torch.device(device.type, torch.cuda.current_device()) if device.type == "cuda" and device.index is None else device
 
 
+def _on_own_device(f):
+    """The method with its object's device as the current one (a launch goes to a stream of that device)."""
+
+    @functools.wraps(f)
+    def g(self, *args, **kw):
+        if torch._C._cuda_getDevice() == self.device.index:
+            return f(self, *args, **kw)
+        with torch.cuda.device(self.device):
+            return f(self, *args, **kw)
+
+    return g
+
+
 def _workspace(nbytes: int, fn: str, device):
     if nbytes < 0:
         raise B.MoeError(fn, B.MOE_EINVAL, "invalid shape")
@@ -221,6 +235,7 @@ class LayerNorm:
             if t is not None:
                 _need(t, name, (self.d,), self.param_dtype, self.device)
 
+    @_on_own_device
     def forward(self, x, weight=None, bias=None, y=None, stream=None):
         n = self._rows(x)
         y = self.y[:n] if y is None else y
@@ -229,10 +244,10 @@ class LayerNorm:
         self._params(weight=weight, bias=bias)
         s = self.shape
         s.rows, s.x_stride, s.y_stride = n, self._stride(x), self._stride(y)
-        with torch.cuda.device(self.device):
-            B.moe_layer_norm(s, x, weight, bias, y, self.mean, self.rstd, stream)
+        B.moe_layer_norm(s, x, weight, bias, y, self.mean, self.rstd, stream)
         return y
 
+    @_on_own_device
     def backward(self, dy, x, weight=None, residual=None, dx=None, stream=None):
         """dx (added to ``residual`` where given), and dweight and dbias in their buffers, for the rows x of the last
         forward call."""
@@ -249,9 +264,8 @@ class LayerNorm:
         self._params(weight=weight)
         s = self.shape
         s.rows, s.x_stride, s.y_stride, s.dx_stride = n, self._stride(x), self._stride(dy), self._stride(dx)
-        with torch.cuda.device(self.device):
-            B.moe_layer_norm_backward(s, dy, x, weight, self.mean, self.rstd, residual, dx, self.dweight, self.dbias,
-                                      self.workspace, stream)
+        B.moe_layer_norm_backward(s, dy, x, weight, self.mean, self.rstd, residual, dx, self.dweight, self.dbias,
+                                  self.workspace, stream)
         return dx
 
 
@@ -290,13 +304,14 @@ class SharedFFN:
         self.shape.tokens = n
         return n
 
+    @_on_own_device
     def forward(self, x, w_gate_up, w_down, residual=None, y=None, stream=None):
         y = self.y[: x.shape[0]] if y is None else y
         self._check(x, w_gate_up, w_down, residual=residual, y=y)
-        with torch.cuda.device(self.device):
-            B.moe_shared_ffn(self.shape, x, w_gate_up, w_down, residual, self.h, self.gu, y, self.workspace, stream)
+        B.moe_shared_ffn(self.shape, x, w_gate_up, w_down, residual, self.h, self.gu, y, self.workspace, stream)
         return y
 
+    @_on_own_device
     def backward(self, dy, x, w_gate_up, w_down, residual=None, dx=None, stream=None):
         """dx (added to ``residual`` where given), and dw_gate_up and dw_down in their buffers, for the x and the weights of
         the last forward call."""
@@ -306,8 +321,7 @@ class SharedFFN:
         self._check(x, w_gate_up, w_down, dy=dy, residual=residual, dx=dx)
         t = {"x": x, "w_gate_up": w_gate_up, "w_down": w_down, "h": self.h, "gu": self.gu, "dy": dy, "residual": residual,
              "dgu_ws": self.dgu, "dx": dx, "dw_gate_up": self.dw_gate_up, "dw_down": self.dw_down}
-        with torch.cuda.device(self.device):
-            B.moe_shared_ffn_backward(self.shape, t, self.workspace, stream)
+        B.moe_shared_ffn_backward(self.shape, t, self.workspace, stream)
         return dx
 
 
@@ -359,6 +373,7 @@ class AdamW:
         return {k: torch.zeros(k.endswith("scale") and blocks or n, dtype=torch.uint8, **z)
                 for k in ("m", "v", "m_scale", "v_scale")}
 
+    @_on_own_device
     def step(self, step, lr, grad_scale=None, stream=None):
         """step: 1, 2, ..., or an int64 tensor on the device; lr: a number, or an fp32 tensor on the device (both: what a
         captured step reads anew at each replay); grad_scale: None, or an fp32 tensor on the device."""
@@ -371,13 +386,12 @@ class AdamW:
                 setattr(cfg, "grad_scale" if field == "grad_scale" else field + "_dev", value.data_ptr())
             elif value is not None:
                 setattr(cfg, field, value)
-        with torch.cuda.device(self.device):
-            B.moe_adamw_step(self.plan, cfg, stream)
+        B.moe_adamw_step(self.plan, cfg, stream)
 
+    @_on_own_device
     def read_states(self, stream=None):
         """The 8-bit states' values into the tensors' "m_values" and "root_values", where given."""
-        with torch.cuda.device(self.device):
-            B.moe_adamw_read_states(self.plan, stream)
+        B.moe_adamw_read_states(self.plan, stream)
 
 
 class MoeBlock:
