@@ -51,7 +51,10 @@ __device__ __forceinline__ void store4(float* p, f32x4 v, int n) {
     for (int i = 0; i < n; ++i) p[i] = v[i];
 }
 __device__ __forceinline__ void store4(bf16_t* p, f32x4 v, int n) {
-  const u32x2 q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  auto two = [](float a, float b) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)a) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)b) << 16);
+  };
+  const u32x2 q = {two(v[0], v[1]), two(v[2], v[3])};
   if (n >= 4) __builtin_memcpy(p, &q, 8);
   else
     for (int i = 0; i < n; ++i) p[i] = (bf16_t)(q[i >> 1] >> (16 * (i & 1)));
@@ -81,46 +84,90 @@ __device__ __forceinline__ uint32_t e4m3_codes(f32x4 v) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], c, true);
 }
 
-// root codes: exponent and mantissa fields are those of an fp32 cut to four mantissa bits, from 2^-15
+// Root codes: exponent and mantissa fields are those of an fp32 cut to four mantissa bits, from 2^-15.  SPECIAL: code 255 is
+// told apart
+template <bool SPECIAL>
 __device__ __forceinline__ float root_value(uint32_t c) {
-  const float v = __uint_as_float(((127u - 15u) << 23) + (c << 19));
-  return c == 0 ? 0.f : c == 255 ? __uint_as_float(0x7fc00000u) : v;
+  const float v = __uint_as_float((c << 19) + ((127u - 15u) << 23));
+  return c == 0 ? 0.f : SPECIAL && c == 255 ? __uint_as_float(0x7fc00000u) : v;
 }
-__device__ __forceinline__ uint32_t root_code(float r) {  // r in units of the scale, at most 1.875 if finite
-  const uint32_t u = __float_as_uint(r);
-  const int c = (int)((u + 0x3ffffu + ((u >> 19) & 1u)) >> 19) - ((127 - 15) << 4);
-  if (!(r < INFINITY)) return 255;
-  return r > 0.f ? (uint32_t)max(c, 1) : 0u;
+__device__ __forceinline__ uint32_t root_code(float r) {  // r in units of the scale, in [0, 1.875]
+  const int u = (int)__float_as_uint(r);
+  // the nearest of four mantissa bits, ties to even, less the exponent of code 0; at least 1 where r is not 0
+  const int c = (u + ((u >> 19) & 1) + (0x3ffff - ((127 - 15) << 23))) >> 19;
+  return (uint32_t)max(c, min(u, 1));
 }
+// whether a byte of v is 255
+__device__ __forceinline__ bool any255(uint32_t v) { return ((~v - 0x01010101u) & v & 0x80808080u) != 0; }
 
 // the largest of v over the eight lanes of a block
 __device__ __forceinline__ float max8(float v) {
   auto dpp = [&](float x, auto ctrl) {
     return __builtin_bit_cast(
-        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, false));
+        float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
   };
-  v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>{}));   // lane ^ 1
-  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>{}));   // lane ^ 2
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>{}));      // lane ^ 1
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>{}));      // lane ^ 2
   return fmaxf(v, dpp(v, std::integral_constant<int, 0x141>{}));  // the other half of the eight, mirrored
 }
 
 // the scale byte for a largest magnitude: its biased exponent less `lead`, one more where its significand is over `over`
 __device__ __forceinline__ uint32_t scale_byte(float top, uint32_t over_mantissa, int lead, int least) {
-  const uint32_t u = __float_as_uint(top);
-  const int b = (int)(u >> 23) - lead + ((u & 0x7fffffu) > over_mantissa ? 1 : 0);
+  const int b = (int)((__float_as_uint(top) + (0x7fffffu - over_mantissa)) >> 23) - lead;
   return (uint32_t)max(b, least);
 }
 
-template <bool BITS8>
+// Four elements' states as codes with their block's scales.  SPECIAL: values that are not finite are told apart: they do not
+// count for the scale
+template <bool SPECIAL>
+__device__ __forceinline__ void pack(const f32x4& m, const f32x4& root, uint32_t* mc, uint32_t* vc, uint32_t* ms, uint32_t* vs) {
+  float tm = 0.f, tr = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    tm = fmaxf(tm, !SPECIAL || fabsf(m[e]) < INFINITY ? fabsf(m[e]) : 0.f);
+    tr = fmaxf(tr, !SPECIAL || root[e] < INFINITY ? root[e] : 0.f);
+  }
+  *ms = scale_byte(max8(tm), 0x600000u, 8, 1);   // 448 = 1.75 x 2^8
+  *vs = scale_byte(max8(tr), 0x700000u, 0, 16);  // 1.875
+  const float a = __uint_as_float((254u - *ms) << 23), b = __uint_as_float((254u - *vs) << 23);
+  f32x4 q;
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    q[e] = !SPECIAL || fabsf(m[e]) < INFINITY ? m[e] * a : __uint_as_float(0x7fc00000u);
+    c[e] = !SPECIAL || root[e] < INFINITY ? root_code(root[e] * b) : 255u;
+  }
+  *mc = e4m3_codes(q);
+  *vc = (c[0] | (c[1] << 8)) | ((c[2] | (c[3] << 8)) << 16);
+}
+
+// A pointer out of a descriptor, to global memory as all of them (else its accesses would be flat ones)
+template <class E>
+__device__ __forceinline__ E* global(void* p) {
+  return (E*)(__attribute__((address_space(1))) E*)p;
+}
+
+// A chunk's step.  FULL: all of its elements are the tensor's
+template <bool BITS8, bool FULL>
 __device__ __forceinline__ void step_chunk(const AdamwDesc& t, int64_t start, const Hyper& h, float gs) {
   const float lr = h.lr * t.lr_scale, decay = lr * t.weight_decay, rate = lr * h.inv_c1;
   const bool pb = t.param_dtype == MOE_BF16, gb = t.grad_dtype == MOE_BF16;
+  const int left = FULL ? ADAMW_CHUNK : (int)(t.n - start);
+  float* pf = global<float>(t.param) + start;
+  bf16_t* ph = global<bf16_t>(t.param) + start;
+  const float* gf = global<float>((void*)t.grad) + start;
+  const bf16_t* gh = global<bf16_t>((void*)t.grad) + start;
+  float *mf = global<float>(t.m) + start, *vf = global<float>(t.v) + start;
+  uint8_t *mb = global<uint8_t>(t.m) + start, *vb = global<uint8_t>(t.v) + start;
+  uint8_t *msp = global<uint8_t>(t.m_scale) + start / MOE_ADAMW_BLOCK, *vsp = global<uint8_t>(t.v_scale) + start / MOE_ADAMW_BLOCK;
   f32x4 p[PASSES], g[PASSES], m[PASSES], v[PASSES];
   uint32_t mc[PASSES], vc[PASSES], ms[PASSES], vs[PASSES];
+  auto place = [&](int k) { return (uint32_t)(k * 1024 + threadIdx.x * 4); };
+  auto count = [&](uint32_t i) { return FULL ? 4 : min(4, left - (int)i); };
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
-    const int64_t i = start + k * 1024 + threadIdx.x * 4;
-    const int n = (int)min((int64_t)4, t.n - i);
+    const uint32_t i = place(k);
+    const int n = count(i);
     if (n <= 0) {
       p[k] = g[k] = m[k] = v[k] = f32x4{0, 0, 0, 0};
       mc[k] = vc[k] = 0;
@@ -128,42 +175,45 @@ __device__ __forceinline__ void step_chunk(const AdamwDesc& t, int64_t start, co
       continue;
     }
     if (pb) {
-      const u32x2 q = load4((const bf16_t*)t.param + i, n);
+      const u32x2 q = load4(ph + i, n);
       p[k][0] = __uint_as_float(q[0]);
       p[k][1] = __uint_as_float(q[1]);
-    } else p[k] = load4((const float*)t.param + i, n);
+    } else p[k] = load4(pf + i, n);
     if (gb) {
-      const u32x2 q = load4((const bf16_t*)t.grad + i, n);
+      const u32x2 q = load4(gh + i, n);
       g[k][0] = __uint_as_float(q[0]);
       g[k][1] = __uint_as_float(q[1]);
-    } else g[k] = load4((const float*)t.grad + i, n);
+    } else g[k] = load4(gf + i, n);
     if (BITS8) {
-      mc[k] = load4((const uint8_t*)t.m + i, n);
-      vc[k] = load4((const uint8_t*)t.v + i, n);
-      ms[k] = t.m_scale[i / MOE_ADAMW_BLOCK];
-      vs[k] = t.v_scale[i / MOE_ADAMW_BLOCK];
+      mc[k] = load4((const uint8_t*)mb + i, n);
+      vc[k] = load4((const uint8_t*)vb + i, n);
+      ms[k] = msp[i / MOE_ADAMW_BLOCK];
+      vs[k] = vsp[i / MOE_ADAMW_BLOCK];
     } else {
-      m[k] = load4((const float*)t.m + i, n);
-      v[k] = load4((const float*)t.v + i, n);
+      m[k] = load4((const float*)mf + i, n);
+      v[k] = load4((const float*)vf + i, n);
     }
   }
 #pragma unroll
   for (int k = 0; k < PASSES; ++k) {
-    const int64_t i = start + k * 1024 + threadIdx.x * 4;
-    const int n = (int)min((int64_t)4, t.n - i);
+    const uint32_t i = place(k);
+    const int n = count(i);
     if (pb) p[k] = widen(u32x2{__float_as_uint(p[k][0]), __float_as_uint(p[k][1])});
     if (gb) g[k] = widen(u32x2{__float_as_uint(g[k][0]), __float_as_uint(g[k][1])});
     if (BITS8) {
       const float a = scale_of(ms[k]), b = scale_of(vs[k]);
       m[k] = e4m3_values(mc[k]);
+      const bool special = __ballot(any255(vc[k])) != 0;  // hardly ever
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        const uint32_t c = (vc[k] >> (8 * e)) & 255u;
+        const float r = (special ? root_value<true>(c) : root_value<false>(c)) * b;
         m[k][e] *= a;
-        const float r = root_value((vc[k] >> (8 * e)) & 255u) * b;
         v[k][e] = r * r;
       }
     }
     f32x4 root;
+    float all = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float q = g[k][e] * gs;
@@ -173,42 +223,26 @@ __device__ __forceinline__ void step_chunk(const AdamwDesc& t, int64_t start, co
       const float den = fmaf(root[e], h.inv_root_c2, h.eps);
       // both parts of the change before it meets p: 1 - lr weight_decay, rounded, would lose most of a small decay
       p[k][e] -= fmaf(rate * m[k][e], __builtin_amdgcn_rcpf(den), decay * p[k][e]);
+      if (BITS8) all += fabsf(m[k][e]) + root[e];
     }
-    if (BITS8) {
-      // a block's largest finite magnitudes (elements past the tensor hold 0), then scales and codes
-      float tm = 0.f, tr = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        tm = fmaxf(tm, fabsf(m[k][e]) < INFINITY ? fabsf(m[k][e]) : 0.f);
-        tr = fmaxf(tr, root[e] < INFINITY ? root[e] : 0.f);
-      }
-      ms[k] = scale_byte(max8(tm), 0x600000u, 8, 1);    // 448 = 1.75 x 2^8
-      vs[k] = scale_byte(max8(tr), 0x700000u, 0, 16);   // 1.875
-      const float a = __uint_as_float((254u - ms[k]) << 23), b = __uint_as_float((254u - vs[k]) << 23);
-      f32x4 q;
-      uint32_t rc = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        q[e] = fabsf(m[k][e]) < INFINITY ? m[k][e] * a : __uint_as_float(0x7fc00000u);
-        rc |= root_code(root[e] * b) << (8 * e);
-      }
-      mc[k] = e4m3_codes(q);
-      vc[k] = rc;
+    if (BITS8) {  // elements past the tensor hold 0
+      if (__ballot(!(all < INFINITY)) != 0) pack<true>(m[k], root, &mc[k], &vc[k], &ms[k], &vs[k]);
+      else pack<false>(m[k], root, &mc[k], &vc[k], &ms[k], &vs[k]);
     }
     if (n <= 0) continue;
-    if (pb) store4((bf16_t*)t.param + i, p[k], n);
-    else store4((float*)t.param + i, p[k], n);
-    if (t.copy) store4((bf16_t*)t.copy + i, p[k], n);
+    if (pb) store4(ph + i, p[k], n);
+    else store4(pf + i, p[k], n);
+    if (t.copy) store4(global<bf16_t>(t.copy) + start + i, p[k], n);
     if (BITS8) {
-      store4((uint8_t*)t.m + i, mc[k], n);
-      store4((uint8_t*)t.v + i, vc[k], n);
+      store4(mb + i, mc[k], n);
+      store4(vb + i, vc[k], n);
       if ((threadIdx.x & 7) == 0) {
-        t.m_scale[i / MOE_ADAMW_BLOCK] = (uint8_t)ms[k];
-        t.v_scale[i / MOE_ADAMW_BLOCK] = (uint8_t)vs[k];
+        msp[i / MOE_ADAMW_BLOCK] = (uint8_t)ms[k];
+        vsp[i / MOE_ADAMW_BLOCK] = (uint8_t)vs[k];
       }
     } else {
-      store4((float*)t.m + i, m[k], n);
-      store4((float*)t.v + i, v[k], n);
+      store4(mf + i, m[k], n);
+      store4(vf + i, v[k], n);
     }
   }
 }
@@ -232,33 +266,59 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwStep a) {
   }
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   const int64_t start = (int64_t)c.index * ADAMW_CHUNK;
-  if (t.state_bits == 8) step_chunk<true>(t, start, h, gs);
-  else step_chunk<false>(t, start, h, gs);
+  const bool full = t.n - start >= ADAMW_CHUNK;
+  if (t.state_bits == 8) {
+    if (full) step_chunk<true, true>(t, start, h, gs);
+    else step_chunk<true, false>(t, start, h, gs);
+  } else {
+    if (full) step_chunk<false, true>(t, start, h, gs);
+    else step_chunk<false, false>(t, start, h, gs);
+  }
+}
+
+template <bool FULL>
+__device__ __forceinline__ void read_chunk(const AdamwDesc& t, int64_t start) {
+  const int left = FULL ? ADAMW_CHUNK : (int)(t.n - start);
+  // m, then the root: codes and scales of the whole chunk first, then the values
+#pragma unroll
+  for (int what = 0; what < 2; ++what) {
+    void* to = what ? t.root_values : t.m_values;
+    if (!to) continue;
+    const uint8_t* code = global<uint8_t>(what ? t.v : t.m) + start;
+    const uint8_t* scale = global<uint8_t>(what ? t.v_scale : t.m_scale) + start / MOE_ADAMW_BLOCK;
+    bf16_t* out = global<bf16_t>(to) + start;
+    uint32_t c[PASSES], s[PASSES];
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const uint32_t i = (uint32_t)(k * 1024 + threadIdx.x * 4);
+      if (!FULL && (int)i >= left) continue;
+      c[k] = load4(code + i, FULL ? 4 : left - (int)i);
+      s[k] = scale[i / MOE_ADAMW_BLOCK];
+    }
+#pragma unroll
+    for (int k = 0; k < PASSES; ++k) {
+      const uint32_t i = (uint32_t)(k * 1024 + threadIdx.x * 4);
+      if (!FULL && (int)i >= left) continue;
+      f32x4 v;
+      if (what == 0) v = e4m3_values(c[k]);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = root_value<true>((c[k] >> (8 * e)) & 255u);
+      const float f = scale_of(s[k]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+      store4(out + i, v, FULL ? 4 : left - (int)i);
+    }
+  }
 }
 
 __global__ __launch_bounds__(256) void k_adamw_read(AdamwStep a) {
   const AdamwChunk c = a.chunks[blockIdx.x];
   const AdamwDesc& t = a.tensors[c.tensor];
-  if (t.state_bits != 8 || (!t.m_values && !t.root_values)) return;
-#pragma unroll
-  for (int k = 0; k < PASSES; ++k) {
-    const int64_t i = (int64_t)c.index * ADAMW_CHUNK + k * 1024 + threadIdx.x * 4;
-    const int n = (int)min((int64_t)4, t.n - i);
-    if (n <= 0) return;
-    if (t.m_values) {
-      const float s = scale_of(t.m_scale[i / MOE_ADAMW_BLOCK]);
-      f32x4 v = e4m3_values(load4((const uint8_t*)t.m + i, n));
-      for (int e = 0; e < 4; ++e) v[e] *= s;
-      store4((bf16_t*)t.m_values + i, v, n);
-    }
-    if (t.root_values) {
-      const float s = scale_of(t.v_scale[i / MOE_ADAMW_BLOCK]);
-      const uint32_t q = load4((const uint8_t*)t.v + i, n);
-      f32x4 v;
-      for (int e = 0; e < 4; ++e) v[e] = root_value((q >> (8 * e)) & 255u) * s;
-      store4((bf16_t*)t.root_values + i, v, n);
-    }
-  }
+  const int64_t start = (int64_t)c.index * ADAMW_CHUNK;
+  if (t.state_bits != 8) return;
+  if (t.n - start >= ADAMW_CHUNK) read_chunk<true>(t, start);
+  else read_chunk<false>(t, start);
 }
 
 }  // namespace
