@@ -113,12 +113,13 @@ __device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t
 }
 
 // ---- few tokens --------------------------------------------------------------------------------------------------------
-// Up to 32 tokens: the weights stream past once and bound the time.  A workgroup takes RT x 16 rows of the weights (GLU with
-// RT = 1: 8 of the gate's and the same 8 of the up projection's) as one operand of 16x16 products whose other is the tokens,
-// 16 per product; its eight waves share out the k in chunks of 128 bytes of each row and add their sums in wave order at the
-// end.  A lane holds 32 neighbouring bytes of its row per chunk; which k of a chunk meet in which product does not
-// matter as long as both operands agree, so the bytes go to the products as they were loaded: no LDS, no barrier before the
-// end.  SU chunks are in flight per wave.
+// The weights stream past once and bound the time.  A workgroup takes RT x 16 rows of the weights (GLU with RT = 1: 8 of the
+// gate's and the same 8 of the up projection's) as one operand of 16x16 products whose other is the tokens, 16 per product;
+// its eight waves share out the k in chunks of 128 bytes of each row and add their sums in wave order at the end.  Which k
+// of a chunk meet in which product does not matter as long as both operands agree.
+//
+// Rows that do not start at 16 bytes: a lane holds 32 neighbouring bytes of its row per chunk and gives them to the products
+// as they were loaded, SU chunks in flight per wave.
 template <typename T>
 struct Chunk32 {  // 32 bytes of a row: 16 bf16 or 8 fp32
   u32x4_t v[2];
@@ -151,6 +152,31 @@ __device__ __forceinline__ f32x4_t products(const Chunk32<T>& a, const Chunk32<T
     }
   }
   return c;
+}
+
+// The eight waves' sums in wave order, and the epilogue.  A product's element: row 4 (lane / 16) .. + 3 of the weights, token
+// lane % 16
+template <typename T, int EPI, int RT, int MT>
+__device__ __forceinline__ void few_finish(const Gemm& p, int n0, int tid, const f32x4_t (*part)[RT * MT][64]) {
+  const int lane = tid & 63;
+  auto sum = [&](int i, int l) {
+    f32x4_t v = part[0][i][l];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += part[k][i][l];
+    return v;
+  };
+  if (EPI == EPI_GLU) {
+    constexpr int L = RT == 1 ? 32 : 64;
+    if (tid >= MT * L) return;
+    const int m = tid / L, l = tid % L, tok = 16 * m + (l & 15), n = n0 + 4 * (l >> 4);
+    if (tok >= p.M || n >= p.N) return;
+    finish4<T, EPI>(p, tok, n, sum(m, l), RT == 1 ? sum(m, l + 32) : sum(MT + m, l));
+  } else {
+    if (tid >= RT * MT * 64) return;
+    const int i = tid >> 6, t = i / MT, m = i % MT, tok = 16 * m + (lane & 15), n = n0 + 16 * t + 4 * (lane >> 4);
+    if (tok >= p.M || n >= p.N) return;
+    finish4<T, EPI>(p, tok, n, sum(i, lane), f32x4_t{0.f, 0.f, 0.f, 0.f});
+  }
 }
 
 template <typename T, int EPI, int RT, int MT, int SU>
@@ -208,25 +234,7 @@ __global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
   __syncthreads();
-  // sums of a product's element: row 4 (lane / 16) .. + 3 of the weights, token lane % 16
-  auto sum = [&](int i, int l) {
-    f32x4_t v = part[0][i][l];
-#pragma unroll
-    for (int k = 1; k < NW; ++k) v += part[k][i][l];
-    return v;
-  };
-  if (EPI == EPI_GLU) {
-    constexpr int L = RT == 1 ? 32 : 64;
-    if (tid >= MT * L) return;
-    const int m = tid / L, l = tid % L, tok = 16 * m + (l & 15), n = n0 + 4 * (l >> 4);
-    if (tok >= p.M || n >= p.N) return;
-    finish4<T, EPI>(p, tok, n, sum(m, l), RT == 1 ? sum(m, l + 32) : sum(MT + m, l));
-  } else {
-    if (tid >= RT * MT * 64) return;
-    const int i = tid >> 6, t = i / MT, m = i % MT, tok = 16 * m + (lane & 15), n = n0 + 16 * t + 4 * (lane >> 4);
-    if (tok >= p.M || n >= p.N) return;
-    finish4<T, EPI>(p, tok, n, sum(i, lane), f32x4_t{0.f, 0.f, 0.f, 0.f});
-  }
+  few_finish<T, EPI, RT, MT>(p, n0, tid, part);
 }
 
 template <typename T, int EPI, int RT, int MT, int SU>
@@ -236,12 +244,145 @@ int few(const Gemm& p, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
-// Tokens up to which the weights stream past (gemm_few).  7168 x 2048: 24 tokens 33 us, against 40 for 65 in tiles; 48 tokens
-// 51 us (three products of tokens per weight).
-constexpr int FEW = 32;
+// Rows that start at 16 bytes: both operands through LDS.  Each wave has a ring of D slots of its own, which LDS-DMA loads of
+// 8 rows of 128 bytes fill D chunks ahead; no barrier before the end.  A load asks the L2 for whole 128-byte lines, where the
+// lanes' own 32 bytes above ask for each line in parts: 16 tokens of 4096 x 14336 take 69 us instead of 90 (64-byte rows: 90
+// too), 24 tokens 83 instead of 107; 72 us is what the weights take at 4.9 TB/s.  Few slots suffice, since more of them let
+// fewer workgroups into a CU.  16-byte piece c of row r of a slot stands at piece c ^ swz(r): a read's 16 rows hit all banks.
+template <typename T, int EPI, int RT, int MT, int D>
+__global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
+  constexpr int ES = sizeof(T), CK = 128 / ES, NW = 8, SLOT = (RT + MT) * 2048;
+  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;  // columns of C
+  extern __shared__ __align__(1024) unsigned char smem[];
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * COLS;
+  const uint32_t ldb = (uint32_t)p.ldb * ES, lda = (uint32_t)p.lda * ES;
+  auto wrow = [&](int t, int r) -> uint32_t {  // row r of weight tile t, from row n0 of the weights
+    const int c = EPI == EPI_GLU ? (RT == 1 ? r & 7 : r) : 16 * t + r;
+    const bool up = EPI == EPI_GLU && (RT == 1 ? r >= 8 : t == 1);
+    return (uint32_t)((n0 + c < p.N ? c : 0) + (up ? p.up : 0)) * ldb;
+  };
+  auto xrow = [&](int t, int r) -> uint32_t { return (uint32_t)(16 * t + r < p.M ? 16 * t + r : 0) * lda; };
+  auto swz = [](int r) { return (r & 7) ^ (r >> 3); };
+  // load i of a tile: rows 8 i + lane / 8, piece lane % 8
+  uint32_t off[RT + MT][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    const uint32_t piece = (uint32_t)((lane & 7) ^ swz(r)) << 4;
+#pragma unroll
+    for (int t = 0; t < RT + MT; ++t) off[t][i] = (t < RT ? wrow(t, r) : xrow(t - RT, r)) + piece;
+  }
+  const unsigned char* wbase = (const unsigned char*)p.b + (int64_t)n0 * ldb;
+  const unsigned char* xbase = (const unsigned char*)p.a;
+  unsigned char* ring = smem + wave * D * SLOT;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)ring;
+  const int chunks = p.K / CK, mine = chunks > wave ? (chunks - wave + NW - 1) / NW : 0;
+  auto load = [&](int j) {  // this wave's chunk j
+    const int64_t at = (int64_t)(wave + j * NW) * 128;
+    const uint32_t slot = lds0 + j % D * SLOT;
+#pragma unroll
+    for (int t = 0; t < RT + MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) dma16((t < RT ? wbase : xbase) + at, off[t][i], slot + t * 2048 + i * 1024);
+  };
+  f32x4_t acc[RT][MT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const u32x4_t (&f)[RT + MT]) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (ES == 2) {
+          acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[t]),
+                                                              __builtin_bit_cast(bf16x8_t, f[RT + m]), acc[t][m], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[t][i]), __uint_as_float(f[RT + m][i]), acc[t][m],
+                                                             0, 0, 0);
+        }
+      }
+  };
+  const int r = lane & 15, q = lane >> 4;
+  auto use = [&](int j) {
+    const unsigned char* slot = ring + j % D * SLOT + r * 128;
+    u32x4_t f[2][RT + MT];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < RT + MT; ++t) f[h][t] = *(const u32x4_t*)(slot + t * 2048 + (((4 * h + q) ^ swz(r)) << 4));
+    if (j + D < mine) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot is read: its next chunk may land
+      load(j + D);
+    }
+    multiply(f[0]);
+    multiply(f[1]);
+  };
+#pragma unroll
+  for (int j = 0; j < D; ++j)
+    if (j < mine) load(j);
+  int j = 0;
+  for (; j + D <= mine; ++j) {  // D - 1 chunks after this one are in flight
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((D - 1) * (RT + MT) * 2) : "memory");
+    use(j);
+  }
+  if (j < mine) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  for (; j < mine; ++j) use(j);
+  if (p.K % CK && chunks % NW == wave) {  // the rest of the rows, under 128 bytes in whole pieces
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = (4 * h + q) * 16;
+      u32x4_t f[RT + MT];
+#pragma unroll
+      for (int t = 0; t < RT + MT; ++t) {
+        const unsigned char* s = t < RT ? wbase + wrow(t, r) : xbase + xrow(t - RT, r);
+        f[t] = c < p.K % CK * ES ? *(const u32x4_t*)(s + (int64_t)chunks * 128 + c) : u32x4_t{0u, 0u, 0u, 0u};
+      }
+      multiply(f);
+    }
+  }
+  __syncthreads();  // every wave is done with its ring
+  f32x4_t(*part)[RT * MT][64] = (f32x4_t(*)[RT * MT][64])smem;
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
+  __syncthreads();
+  few_finish<T, EPI, RT, MT>(p, n0, tid, part);
+}
+
+template <typename T, int EPI, int RT, int MT, int D>
+int ring(const Gemm& p, hipStream_t st) {
+  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT, LDS = 8 * D * (RT + MT) * 2048;
+  const void* k = (const void*)k_gemm_ring<T, EPI, RT, MT, D>;
+  if (LDS > 65536 && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, LDS) != hipSuccess) return -1;
+  void* params[] = {(void*)&p};
+  return hipLaunchKernel(k, dim3((unsigned)((p.N + COLS - 1) / COLS)), dim3(512), params, LDS, st) == hipSuccess ? 0 : -1;
+}
+
+// Whether the weights stream past (gemm_few), or the tokens are many enough for tiles.  Measured: 4096 x 14336 with 32 tokens
+// 87 us against 91 for 40 in tiles, with 64 tokens 121 against 82 (each weight meets four products' worth of tokens); 7168 x
+// 2048 with 40 tokens 32 and 34, with 64 both 37; 2048 x 1408 with 64 tokens 11 and 21 (tiles need k-splits there).
+bool few_tokens(int64_t tokens, int d, int f, int elem) {
+  const int piece = 16 / elem;
+  return tokens <= 32 || (tokens <= 64 && d % piece == 0 && f % piece == 0 && (int64_t)d * f * elem <= 1 << 25);
+}
 
 template <typename T, int EPI>
 int gemm_few(const Gemm& p, hipStream_t st) {
+  constexpr int PER = 16 / sizeof(T);  // elements of a 16-byte piece
+  if (p.lda % PER == 0 && p.ldb % PER == 0 && p.K % PER == 0 && ((int64_t)p.up + 32) * p.ldb * (int)sizeof(T) < (1ll << 32)) {
+    if (p.M <= 16) return ring<T, EPI, 1, 1, 2>(p, st);
+    if (p.M <= 32) return ring<T, EPI, 1, 2, 1>(p, st);
+    if (p.M <= 48) return ring<T, EPI, 1, 3, 1>(p, st);
+    return ring<T, EPI, 1, 4, 1>(p, st);
+  }
   if (p.M <= 16) return few<T, EPI, 1, 1, 4>(p, st);
   return few<T, EPI, 1, 2, 2>(p, st);
 }
@@ -1035,7 +1176,7 @@ int run_f32(const SharedLaunch& s, hipStream_t st) {
   float* partial = (float*)s.workspace;
   int rc;
   if (!s.backward) {
-    if (s.tokens <= FEW) {
+    if (few_tokens(s.tokens, s.d, s.f, 4)) {
       if ((rc = gemm_few<float, EPI_GLU>(b.glu, st))) return rc;
       return gemm_few<float, EPI_STORE>(b.down, st);
     }
@@ -1052,7 +1193,7 @@ int run_bf16(const SharedLaunch& s, hipStream_t st) {
     if ((rc = clear(s.dw_gate_up, 2ll * s.f * s.d, st))) return rc;
     return clear(s.dw_down, (int64_t)s.f * s.d, st);
   }
-  if (!s.backward && s.tokens <= FEW) {
+  if (!s.backward && few_tokens(s.tokens, s.d, s.f, 2)) {
     const Block b = block_f32(s);  // the operands as they are
     if ((rc = gemm_few<bf16_t, EPI_GLU>(b.glu, st))) return rc;
     return gemm_few<bf16_t, EPI_STORE>(b.down, st);
