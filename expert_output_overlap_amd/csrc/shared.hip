@@ -790,25 +790,26 @@ constexpr int MAX_SPLITS = 16;
 // Tile and k-splits of a product, by an estimate of its time from what the tiles measured (us per k-tile of 64, operands
 // from HBM).  256 x 256: 1.5 with one workgroup on each CU.  128 x 128 in two stages: 0.85 where a CU has one workgroup, 1.05
 // for two at once; in four stages (one workgroup fills a CU's LDS): 0.62, the loads' latency hidden by their depth instead
-// of by the other workgroup.  64 x 128 in three stages: 0.53 and 0.75.  So the large tile is 1.4 times as fast per product
-// once every CU has one, and the small ones win where they would leave CUs idle: 777 tokens of the skewed workload's widths
-// take 37 us forward in 64 x 128 or deep 128 x 128 tiles, 49 in 128 x 128, 82 in 256 x 256; 2048 tokens 60, 62 and 93;
-// 16384 tokens of the DeepSeek-V3-shaped widths 1310 in 256 x 256.  Splitting k costs the fp32 sums' way to memory and
-// back and a second launch; 128 tokens of those widths take 47 us in four splits and 80 in one.
+// of by the other workgroup.  64 x 128 in three stages: 0.53 and 0.75.  256 x 128 in three: 0.85.  So the large tiles are 1.4
+// times as fast per product once every CU has one, and the small ones win where they would leave CUs idle: 777 tokens of the
+// skewed workload's widths take 36 us forward in 64 x 128 or deep 128 x 128 tiles, 49 in 128 x 128, 82 in 256 x 256; 2048
+// tokens 53, 62 and 93; 2048 tokens of the DeepSeek-V3-shaped widths 179, and 200 without the 256 x 128 tile; 16384 tokens
+// 1270 in 256 x 256.  Splitting k costs the fp32 sums' way to memory and back and a second launch; 128 tokens of those widths
+// take 44 us with splits and 80 without.
 struct Choice {
   int tile, splits;
 };
 const struct {
   int bm, bn, per_cu;
   double alone, full, fixed;  // us: a k-tile with one workgroup on the CU, with per_cu of them, and a tile's two ends
-} TILES[] = {{256, 256, 1, 1.5, 1.5, 5.0}, {128, 128, 2, 0.85, 1.05, 3.0}, {128, 128, 1, 0.62, 0.62, 3.0}, {64, 128, 2, 0.53, 0.75, 2.5}};
+} TILES[] = {{256, 256, 1, 1.5, 1.5, 5.0}, {128, 128, 2, 0.85, 1.05, 3.0}, {128, 128, 1, 0.62, 0.62, 3.0}, {64, 128, 2, 0.53, 0.75, 2.5}, {256, 128, 1, 0.85, 0.85, 3.5}};
 int64_t tiles_of(int t, int64_t M, int64_t cols) { return ((M + TILES[t].bm - 1) / TILES[t].bm) * ((cols + TILES[t].bn - 1) / TILES[t].bn); }
 double join_us(int64_t floats) { return 4.0 + 8.0 * floats / 3.5e6; }  // sums to memory and back
 
 Choice choose(int64_t M, int64_t cols, int nkt) {
   Choice best{0, 1};
   double least = 1e30;
-  for (int t = 0; t < 4; ++t) {
+  for (int t = 0; t < 5; ++t) {
     const int64_t n = tiles_of(t, M, cols);
     for (int s = 1; s <= MAX_SPLITS; ++s) {
       if (s > 1 && (nkt / s < 4 || s * M * cols > PARTIAL)) break;
@@ -869,16 +870,17 @@ int gemm_bf16(const Gemm& p, float* partial, hipStream_t st) {
   const Choice c = choose(p.M, partial_cols(p, EPI), (p.K + 63) / 64);
   if (c.tile == 0) return gemm_tiles<256, 256, 2, 4, 2, BCOL, EPI>(p, c.splits, partial, st);
   if (c.tile == 1) return gemm_tiles<128, 128, 2, 2, 2, BCOL, EPI>(p, c.splits, partial, st);
-  if (c.tile == 2) return gemm_tiles<128, 128, 2, 2, 4, BCOL, EPI>(p, c.splits, partial, st);
-  return gemm_tiles<64, 128, 2, 2, 3, BCOL, EPI>(p, c.splits, partial, st);
+  if (c.tile == 2) return gemm_tiles<128, 128, 4, 2, 4, BCOL, EPI>(p, c.splits, partial, st);
+  if (c.tile == 3) return gemm_tiles<64, 128, 2, 2, 3, BCOL, EPI>(p, c.splits, partial, st);
+  return gemm_tiles<256, 128, 4, 2, 3, BCOL, EPI>(p, c.splits, partial, st);
 }
 
 int grads_bf16(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
   int splits[3];
   const Choice c = choose_grads(p, splits);
   if (c.tile == 0) return grads_tiles<256, 256, 2, 4, 2>(p, splits, partial, st);
-  if (c.tile == 1) return grads_tiles<128, 128, 2, 2, 2>(p, splits, partial, st);
-  return grads_tiles<128, 128, 2, 2, 4>(p, splits, partial, st);
+  if (c.tile == 1) return grads_tiles<128, 128, 4, 2, 2>(p, splits, partial, st);
+  return grads_tiles<128, 128, 4, 2, 4>(p, splits, partial, st);
 }
 
 // ---- fp32 --------------------------------------------------------------------------------------------------------------
@@ -910,12 +912,17 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   // eight neighbours along memory per thread and operand: by rows, k 8 (tid % 4) .. of row tid / 4; by columns, rows
   // 4 (tid % 16) .. of k tid / 16 and tid / 16 + 16.  Outside the matrix: 0
   f32x4_t rega[2][2], regb[2][2];  // of two k-tiles: a load has two k-tiles' time to arrive
-  auto four = [&](const float* q, int c, int limit, int seg, int jump) {  // contiguous elements c .. c + 3 < limit at q
-    if (c + 4 <= limit && (c >= seg || c + 4 <= seg)) return load4(q + c + (c >= seg ? jump : 0), 4);
-    f32x4_t v = {0, 0, 0, 0};
+  // contiguous elements c .. c + 3 at q, those from limit on 0 (in: whether any are wanted): no branch, so that all of a
+  // thread's loads go out together
+  auto four = [&](const float* q, int c, int limit, int seg, int jump, bool in) {
+    f32x4_t v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < limit) v[i] = q[c + i + (c + i >= seg ? jump : 0)];
+    for (int i = 0; i < 4; ++i) {
+      const int e = min(c + i, limit - 1);
+      v[i] = q[e + (e >= seg ? jump : 0)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = in && c + i < limit ? v[i] : 0.f;
     return v;
   };
   // a k-tile that ends before the last k and does not straddle a_seg: whole fours from a lane's fixed places.  Rows past the
@@ -928,7 +935,6 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
                          : B + ((rb_row < p.N ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
   const bool wide = p.lda >= 4 && p.ldb >= 4;
   auto fetch = [&](int kt, f32x4_t* ra, f32x4_t* rb) {
-    const f32x4_t zero = {0, 0, 0, 0};
     const int k0 = kt * FK;
     if (wide && k0 + FK < p.K && (ACOL || k0 >= p.a_seg || k0 + FK <= p.a_seg)) {
       const float* qa = pa + (ACOL ? (int64_t)k0 * p.lda : k0 + (k0 >= p.a_seg ? p.a_jump : 0));
@@ -941,20 +947,11 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (ACOL) {
-        const int k = kt * FK + (tid >> 4) + 16 * h;
-        ra[h] = k < p.K ? four(A + (int64_t)k * p.lda, ca, p.M, 0x7fffffff, 0) : zero;
-      } else {
-        const int m = m0 + (tid >> 2);
-        ra[h] = m < p.M ? four(A + (int64_t)m * p.lda, kt * FK + 8 * (tid & 3) + 4 * h, p.K, p.a_seg, p.a_jump) : zero;
-      }
-      if (BCOL) {
-        const int k = kt * FK + (tid >> 4) + 16 * h;
-        rb[h] = k < p.K ? four(B + (int64_t)k * p.ldb, cb, p.N, 0x7fffffff, 0) : zero;
-      } else {
-        const int64_t at = rb_row + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0);
-        rb[h] = rb_row < p.N ? four(B + at * p.ldb, kt * FK + 8 * (tid & 3) + 4 * h, p.K, 0x7fffffff, 0) : zero;
-      }
+      const int kc = k0 + (tid >> 4) + 16 * h, kr = k0 + 8 * (tid & 3) + 4 * h, last = p.K - 1;
+      ra[h] = ACOL ? four(A + (int64_t)min(kc, last) * p.lda, ca, p.M, 0x7fffffff, 0, kc <= last)
+                   : four(A + (int64_t)min(m0 + row, p.M - 1) * p.lda, kr, p.K, p.a_seg, p.a_jump, true);
+      rb[h] = BCOL ? four(B + (int64_t)min(kc, last) * p.ldb, cb, p.N, 0x7fffffff, 0, kc <= last)
+                   : four(B + (min(rb_row, p.N - 1) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb, kr, p.K, 0x7fffffff, 0, true);
     }
   };
   auto keep = [&](int st, const f32x4_t* ra, const f32x4_t* rb) {
