@@ -4,7 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
-#include <new>
+#include <exception>
 #include <vector>
 
 #include "../../include/moe_overlap.h"
@@ -23,6 +23,23 @@ bool meet(const void* p, int64_t n, const void* q, int64_t m) {
   return p && q && n > 0 && m > 0 && (uintptr_t)p < (uintptr_t)q + (uintptr_t)m && (uintptr_t)q < (uintptr_t)p + (uintptr_t)n;
 }
 
+struct Span {
+  const void* p;
+  int64_t n;
+};
+
+// Whether an output overlaps an input or another output; same(o, i): a pair that may be the same buffer
+template <int O, int I, class F>
+bool overlaps(const Span (&out)[O], const Span (&in)[I], F same) {
+  for (int o = 0; o < O; ++o) {
+    for (int i = 0; i < I; ++i)
+      if (meet(out[o].p, out[o].n, in[i].p, in[i].n) && !(out[o].p == in[i].p && same(o, i))) return true;
+    for (int q = 0; q < o; ++q)
+      if (meet(out[o].p, out[o].n, out[q].p, out[q].n)) return true;
+  }
+  return false;
+}
+
 const char* check_norm(const moe_norm_shape* s) {
   if (!s) return "null shape";
   if (s->rows < 0 || s->rows > (1ll << 40)) return "rows must be in [0, 2^40]";
@@ -30,7 +47,8 @@ const char* check_norm(const moe_norm_shape* s) {
   if (!is_dtype(s->dtype) || !is_dtype(s->param_dtype)) return "dtype must be MOE_BF16 or MOE_F32";
   if (!(s->eps > 0.f) || !std::isfinite(s->eps)) return "eps must be positive and finite";
   for (const int64_t stride : {s->x_stride, s->y_stride, s->dx_stride})
-    if (stride != 0 && (stride < s->d || stride > (1ll << 40))) return "a row stride must be 0 or in [d, 2^40]";
+    if (stride != 0 && (stride < s->d || stride > (1ll << 46) / std::max<int64_t>(s->rows, 1)))
+      return "a row stride must be 0 or at least d, and rows x stride at most 2^46";
   return nullptr;
 }
 
@@ -53,6 +71,7 @@ const char* check_shared(const moe_shared_shape* s) {
   if (s->d < 1 || s->d > 65536) return "d must be in [1, 65536]";
   if (s->f < 1 || s->f > 65536) return "f must be in [1, 65536]";
   if (!is_dtype(s->dtype)) return "dtype must be MOE_BF16 or MOE_F32";
+  if (s->tokens * std::max(s->d, 2 * s->f) > (1ll << 34)) return "tokens x max(d, 2f) must be at most 2^34";
   return nullptr;
 }
 
@@ -66,6 +85,7 @@ const char* check_adamw(const moe_adamw_tensor* t, int32_t n) {
     if (a.n < 0 || a.n > (1ll << 40)) return "elements must be in [0, 2^40]";
     if (!is_dtype(a.param_dtype) || !is_dtype(a.grad_dtype)) return "dtype must be MOE_BF16 or MOE_F32";
     if (a.state_bits != 32 && a.state_bits != 8) return "state_bits must be 32 or 8";
+    if (a.reserved != 0) return "reserved must be 0";
     if (!std::isfinite(a.weight_decay) || !std::isfinite(a.lr_scale)) return "weight_decay and lr_scale must be finite";
     if (a.n == 0) continue;
     if (!a.param || !a.grad || !a.m || !a.v) return "null pointer";
@@ -77,7 +97,8 @@ const char* check_adamw(const moe_adamw_tensor* t, int32_t n) {
       return "a tensor must be aligned to its elements";
     chunks += (a.n + ADAMW_CHUNK - 1) / ADAMW_CHUNK;
   }
-  return chunks > 0x7fffffff ? "too many elements for one plan" : nullptr;
+  // 256 threads each, under 2^32 in a launch
+  return chunks >= 1 << 24 ? "too many elements for one plan" : nullptr;
 }
 
 int64_t adamw_chunks(const moe_adamw_tensor* t, int32_t n) {
@@ -114,8 +135,11 @@ int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* weight, c
     return moe_fail(MOE_EINVAL, "a tensor must be aligned to its elements");
   NormLaunch a = norm_of(s);
   if (s->rows > 0) {
-    const int64_t es = elem(s->dtype), nx = ((s->rows - 1) * a.x_stride + s->d) * es, ny = ((s->rows - 1) * a.y_stride + s->d) * es;
-    if (meet(x, nx, y, ny) && !(x == y && a.x_stride == a.y_stride)) return moe_fail(MOE_EINVAL, "y overlaps x");
+    const int64_t es = elem(s->dtype), r = s->rows - 1, np = s->d * elem(s->param_dtype);
+    const Span out[] = {{y, (r * a.y_stride + s->d) * es}, {mean, 4 * s->rows}, {rstd, 4 * s->rows}},
+               in[] = {{x, (r * a.x_stride + s->d) * es}, {weight, np}, {bias, np}};
+    if (overlaps(out, in, [&](int o, int i) { return o == 0 && i == 0 && a.x_stride == a.y_stride; }))
+      return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   }
   a.x = x;
   a.weight = weight;
@@ -146,11 +170,13 @@ int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void*
     if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
   }
   if (s->rows > 0) {
-    const int64_t es = elem(s->dtype), r = s->rows - 1;
-    const int64_t nx = (r * a.x_stride + s->d) * es, ny = (r * a.y_stride + s->d) * es, nd = (r * a.dx_stride + s->d) * es;
-    if (meet(x, nx, dx, nd)) return moe_fail(MOE_EINVAL, "dx overlaps x");
-    if (meet(dy, ny, dx, nd) && !(dy == dx && a.y_stride == a.dx_stride)) return moe_fail(MOE_EINVAL, "dx overlaps dy");
-    if (meet(residual, nd, dx, nd) && residual != dx) return moe_fail(MOE_EINVAL, "dx overlaps residual");
+    const int64_t es = elem(s->dtype), r = s->rows - 1, np = s->d * elem(s->param_dtype);
+    const Span out[] = {{dx, (r * a.dx_stride + s->d) * es}, {dweight, np}, {dbias, np},
+                        {params ? workspace : nullptr, moe_layer_norm_workspace_bytes(s)}},
+               in[] = {{dy, (r * a.y_stride + s->d) * es}, {residual, (r * a.dx_stride + s->d) * es},
+                       {x, (r * a.x_stride + s->d) * es}, {weight, np}, {mean, 4 * s->rows}, {rstd, 4 * s->rows}};
+    if (overlaps(out, in, [&](int o, int i) { return o == 0 && (i == 1 || (i == 0 && a.y_stride == a.dx_stride)); }))
+      return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   }
   a.backward = true;
   a.dy = dy;
@@ -185,12 +211,10 @@ int moe_shared_ffn(const moe_shared_shape* s, const void* x, const void* w_gate_
   if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
   const int64_t es = elem(s->dtype), nx = s->tokens * s->d * es, nw = (int64_t)s->d * s->f * es,
                 nh = s->tokens * shared_row(s) * es, ngu = s->tokens * 2 * shared_row(s) * 4;
-  if (meet(y, nx, x, nx) || meet(y, nx, w_gate_up, 2 * nw) || meet(y, nx, w_down, nw) || meet(y, nx, h, nh) ||
-      meet(y, nx, gu, ngu) || (residual != y && meet(y, nx, residual, nx)))
-    return moe_fail(MOE_EINVAL, "y overlaps another tensor");
-  if (meet(h, nh, x, nx) || meet(h, nh, gu, ngu) || meet(gu, ngu, x, nx) || meet(h, nh, residual, nx) ||
-      meet(gu, ngu, residual, nx))
-    return moe_fail(MOE_EINVAL, "h or gu overlaps another tensor");
+  const Span out[] = {{y, nx}, {h, nh}, {gu, ngu}, {workspace, need}},
+             in[] = {{residual, nx}, {x, nx}, {w_gate_up, 2 * nw}, {w_down, nw}};
+  if (overlaps(out, in, [](int o, int i) { return o == 0 && i == 0; }))
+    return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   SharedLaunch a{};
   a.tokens = s->tokens;
   a.d = s->d;
@@ -221,17 +245,10 @@ int moe_shared_ffn_backward(const moe_shared_shape* s, const moe_shared_bwd_args
   if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
   const int64_t es = elem(s->dtype), nx = s->tokens * s->d * es, nw = (int64_t)s->d * s->f * es,
                 nh = s->tokens * shared_row(s) * es, ngu = s->tokens * 2 * shared_row(s) * 4;
-  const struct { const void* p; int64_t n; } in[] = {{b->x, nx}, {b->w_gate_up, 2 * nw}, {b->w_down, nw}, {b->h, nh},
-                                                     {b->gu, ngu}, {b->dy, nx}, {b->residual, nx}},
-      out[] = {{b->dgu_ws, 2 * nh}, {b->dx, nx}, {b->dw_gate_up, 2 * nw}, {b->dw_down, nw}};
-  for (const auto& o : out)
-    for (const auto& i : in) {
-      const bool same = o.p == i.p && o.p == b->dx && i.p == b->residual;
-      if (!same && meet(o.p, o.n, i.p, i.n)) return moe_fail(MOE_EINVAL, "an output overlaps an input");
-    }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < i; ++j)
-      if (meet(out[i].p, out[i].n, out[j].p, out[j].n)) return moe_fail(MOE_EINVAL, "two outputs overlap");
+  const Span out[] = {{b->dx, nx}, {b->dgu_ws, 2 * nh}, {b->dw_gate_up, 2 * nw}, {b->dw_down, nw}, {workspace, need}},
+             in[] = {{b->residual, nx}, {b->x, nx}, {b->w_gate_up, 2 * nw}, {b->w_down, nw}, {b->h, nh}, {b->gu, ngu}, {b->dy, nx}};
+  if (overlaps(out, in, [](int o, int i) { return o == 0 && i == 0; }))
+    return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   SharedLaunch a{};
   a.backward = true;
   a.tokens = s->tokens;
@@ -267,11 +284,11 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
   if (n_tensors > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
   if (off(workspace, 16)) return moe_fail(MOE_EINVAL, "workspace must be 16-byte aligned");
   try {
-    struct Span {
+    struct Range {
       uintptr_t at, end;
       bool written;
     };
-    std::vector<Span> spans;
+    std::vector<Range> spans;
     int n8 = 0;
     for (int i = 0; i < n_tensors; ++i) {
       const moe_adamw_tensor& a = t[i];
@@ -287,9 +304,9 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
         if (o.p && (o.p != workspace || i == 0)) spans.push_back({(uintptr_t)o.p, (uintptr_t)o.p + (uintptr_t)o.n, true});
       spans.push_back({(uintptr_t)a.grad, (uintptr_t)a.grad + (uintptr_t)(a.n * elem(a.grad_dtype)), false});
     }
-    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+    std::sort(spans.begin(), spans.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
     uintptr_t any = 0, written = 0;  // ends of what was seen so far, and of what of it the step writes
-    for (const Span& s : spans) {
+    for (const Range& s : spans) {
       if (s.at < written || (s.written && s.at < any))
         return moe_fail(MOE_EINVAL, "a buffer that the step writes overlaps another (the same tensor twice?)");
       any = std::max(any, s.end);
@@ -312,7 +329,7 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
     plan->n_chunks = n_chunks;
     plan->n_tensors = n_tensors;
     plan->states8 = n8;
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {
     return moe_fail(MOE_EINVAL, "out of host memory");
   }
   return MOE_OK;

@@ -23,6 +23,7 @@ struct Gemm {
   int64_t lda, ldb;
   int a_seg, a_jump;
   int M, N, K;
+  int n_in;  // columns of C that B has, the others become 0 (N: a whole padded row of h, or of dg and du)
   // epilogue
   void* c;  // GLU: h; DGLU: dg | du; STORE: C
   int64_t ldc;
@@ -71,11 +72,11 @@ __device__ __forceinline__ float sigmoid(float g) {
   return sizeof(T) == 2 ? __builtin_amdgcn_rcpf(1.0f + __expf(-g)) : 1.0f / (1.0f + __expf(-g));
 }
 
-// Four neighbouring columns n .. of row m through the epilogue (sum2: GLU's up sums).  Columns past N are cut; h, gu and dgu
-// have whole fours in a row, where they become 0.
+// Four neighbouring columns n .. of row m through the epilogue (sum2: GLU's up sums).  Columns past n_in become 0 in h, gu and
+// dgu, whatever was summed or stands there, and are cut in C.
 template <typename T, int EPI>
 __device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t sum, f32x4_t sum2) {
-  const int in = p.N - n;
+  const int in = p.n_in - n;
   if (EPI == EPI_GLU) {
     f32x4_t h;
 #pragma unroll
@@ -190,7 +191,7 @@ __global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     int c = EPI == EPI_GLU ? n0 + (RT == 1 ? r & 7 : r) : n0 + 16 * t + r;
-    int64_t row = c < p.N ? c : 0;
+    int64_t row = c < p.n_in ? c : 0;
     if (EPI == EPI_GLU && (RT == 1 ? r >= 8 : t == 1)) row += p.up;
     w[t] = (const T*)p.b + row * p.ldb + q * (32 / sizeof(T));
   }
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
   auto wrow = [&](int t, int r) -> uint32_t {  // row r of weight tile t, from row n0 of the weights
     const int c = EPI == EPI_GLU ? (RT == 1 ? r & 7 : r) : 16 * t + r;
     const bool up = EPI == EPI_GLU && (RT == 1 ? r >= 8 : t == 1);
-    return (uint32_t)((n0 + c < p.N ? c : 0) + (up ? p.up : 0)) * ldb;
+    return (uint32_t)((n0 + c < p.n_in ? c : 0) + (up ? p.up : 0)) * ldb;
   };
   auto xrow = [&](int t, int r) -> uint32_t { return (uint32_t)(16 * t + r < p.M ? 16 * t + r : 0) * lda; };
   auto swz = [](int r) { return (r & 7) ^ (r >> 3); };
@@ -473,10 +474,10 @@ struct Tile {
       const int q = wave * LB + j;
       if (BCOL) {
         const int c = n0 + 8 * col_c(q, BN);
-        boff[j] = (uint32_t)col_k(q, BN) * ldb + (uint32_t)(c < p.N ? c : 0) * 2;
+        boff[j] = (uint32_t)col_k(q, BN) * ldb + (uint32_t)(c < p.n_in ? c : 0) * 2;
       } else {
         const int r = (8 * q + (lane >> 3)) & (COLS - 1);  // GLU: gate rows, then up rows, whose base lies further on
-        boff[j] = (uint32_t)(n0 + r < p.N ? r : 0) * ldb + row_k(q);
+        boff[j] = (uint32_t)(n0 + r < p.n_in ? r : 0) * ldb + row_k(q);
       }
     }
     const unsigned char* abase = (const unsigned char*)p.a + (ACOL ? (int64_t)t0 * 64 * lda : (int64_t)m0 * lda + (int64_t)t0 * 128);
@@ -931,8 +932,8 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   const float* pa = ACOL ? A + (int64_t)(tid >> 4) * p.lda + (ca < p.M ? ca : 0)
                          : A + (int64_t)(m0 + row < p.M ? m0 + row : 0) * p.lda + 8 * (tid & 3);
   const int rb_row = n0 + (row & (BN - 1));
-  const float* pb = BCOL ? B + (int64_t)(tid >> 4) * p.ldb + (cb < p.N ? cb : 0)
-                         : B + ((rb_row < p.N ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
+  const float* pb = BCOL ? B + (int64_t)(tid >> 4) * p.ldb + (cb < p.n_in ? cb : 0)
+                         : B + ((rb_row < p.n_in ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
   const bool wide = p.lda >= 4 && p.ldb >= 4;
   auto fetch = [&](int kt, f32x4_t* ra, f32x4_t* rb) {
     const int k0 = kt * FK;
@@ -950,8 +951,8 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
       const int kc = k0 + (tid >> 4) + 16 * h, kr = k0 + 8 * (tid & 3) + 4 * h, last = p.K - 1;
       ra[h] = ACOL ? four(A + (int64_t)min(kc, last) * p.lda, ca, p.M, 0x7fffffff, 0, kc <= last)
                    : four(A + (int64_t)min(m0 + row, p.M - 1) * p.lda, kr, p.K, p.a_seg, p.a_jump, true);
-      rb[h] = BCOL ? four(B + (int64_t)min(kc, last) * p.ldb, cb, p.N, 0x7fffffff, 0, kc <= last)
-                   : four(B + (min(rb_row, p.N - 1) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb, kr, p.K, 0x7fffffff, 0, true);
+      rb[h] = BCOL ? four(B + (int64_t)min(kc, last) * p.ldb, cb, p.n_in, 0x7fffffff, 0, kc <= last)
+                   : four(B + (min(rb_row, p.n_in - 1) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb, kr, p.K, 0x7fffffff, 0, true);
     }
   };
   auto keep = [&](int st, const f32x4_t* ra, const f32x4_t* rb) {
@@ -1137,8 +1138,8 @@ void pack_sizes(int64_t tokens, int d, int f, bool backward, int64_t (&n)[4]) {
 }
 
 // The call's products.  f32: on the operands as they are.  bf16: on rows that start at 16 bytes, widths D and F in whole
-// eights; the weights' rows and columns past d and f are 0, so that sums over a whole D or F need no care, and g, u and h
-// past f become 0.
+// eights; the weights' rows and columns past d and f are 0, so that sums over a whole D or F need no care.  Either way h, g,
+// u, dg and du past f are written as 0.
 struct Block {
   Gemm glu, down;                      // forward
   Gemm dglu, dx, dw_gate_up, dw_down;  // backward
@@ -1147,24 +1148,24 @@ struct Block {
 Block block_f32(const SharedLaunch& s) {
   Block b{};
   const int T = (int)s.tokens, d = s.d, f = s.f, F = s.row, none = 0x7fffffff;
-  b.glu = {s.x, s.w_gate_up, d, d, none, 0, T, f, d, s.h, F, nullptr, s.gu, 2 * F, F, f, none, none};
-  b.down = {s.h, s.w_down, F, f, none, 0, T, d, f, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
-  b.dglu = {s.dy, s.w_down, d, f, none, 0, T, f, d, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
-  b.dx = {s.dgu, s.w_gate_up, 2 * F, d, f, F - f, T, d, 2 * f, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
-  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, none, 0, 2 * F, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
-  b.dw_down = {s.dy, s.h, d, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
+  b.glu = {s.x, s.w_gate_up, d, d, none, 0, T, F, d, f, s.h, F, nullptr, s.gu, 2 * F, F, f, none, none};
+  b.down = {s.h, s.w_down, F, f, none, 0, T, d, f, d, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dglu = {s.dy, s.w_down, d, f, none, 0, T, F, d, f, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
+  b.dx = {s.dgu, s.w_gate_up, 2 * F, d, f, F - f, T, d, 2 * f, d, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dw_gate_up = {s.dgu, s.x, 2 * F, d, none, 0, 2 * F, d, T, d, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
+  b.dw_down = {s.dy, s.h, d, F, none, 0, d, f, T, f, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
   return b;
 }
 
 Block block_bf16(const SharedLaunch& s, const void* x, const void* wgu, const void* wd, const void* dy) {
   Block b{};
   const int T = (int)s.tokens, d = s.d, f = s.f, F = s.row, D = (int)up8(d), none = 0x7fffffff;
-  b.glu = {x, wgu, D, D, none, 0, T, F, D, s.h, F, nullptr, s.gu, 2 * F, F, F, none, none};
-  b.down = {s.h, wd, F, F, none, 0, T, d, F, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
-  b.dglu = {dy, wd, D, F, none, 0, T, F, D, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
-  b.dx = {s.dgu, wgu, 2 * F, D, none, 0, T, d, 2 * F, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
-  b.dw_gate_up = {s.dgu, x, 2 * F, D, none, 0, 2 * F, d, T, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
-  b.dw_down = {dy, s.h, D, F, none, 0, d, f, T, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
+  b.glu = {x, wgu, D, D, none, 0, T, F, D, f, s.h, F, nullptr, s.gu, 2 * F, F, F, none, none};
+  b.down = {s.h, wd, F, F, none, 0, T, d, F, d, s.y, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dglu = {dy, wd, D, F, none, 0, T, F, D, f, s.dgu, 2 * F, nullptr, s.gu, 2 * F, F, 0, none, none};
+  b.dx = {s.dgu, wgu, 2 * F, D, none, 0, T, d, 2 * F, d, s.dx, d, s.residual, nullptr, 0, 0, 0, none, none};
+  b.dw_gate_up = {s.dgu, x, 2 * F, D, none, 0, 2 * F, d, T, d, s.dw_gate_up, d, nullptr, nullptr, 0, 0, 0, f, F};
+  b.dw_down = {dy, s.h, D, F, none, 0, d, f, T, f, s.dw_down, f, nullptr, nullptr, 0, 0, 0, none, none};
   return b;
 }
 

@@ -360,7 +360,7 @@ int moe_combine_backward(const moe_shape* s, const moe_layout* L, const void* d_
  * Statistics and sums in fp32 (the variance from the differences to the mean), each result rounded once.  The rows'
  * sums of the weight's gradient run in a fixed order, so equal calls on equal devices give equal bits.
  * Any alignment and any row stride >= d; elements between rows are neither read nor written.  An output may not overlap
- * an input, except that y may be x and dx may be dy or residual (with the same row stride). */
+ * an input or another output, except that y may be x and dx may be dy or residual (with the same row stride). */
 typedef struct {
   int64_t rows;         /* T >= 0 (0: dweight and dbias become 0, nothing else is written) */
   int32_t d;            /* 1 .. MOE_NORM_MAX_D */
@@ -399,14 +399,14 @@ int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void*
  * results once; g and u are kept in fp32 (in bf16 they would add a third rounding of the size of the result's own to every
  * gradient).  f32: everything in fp32. */
 typedef struct {
-  int64_t tokens;  /* T in [0, 2^27] (0: the backward's weight gradients become 0, nothing else is written) */
+  int64_t tokens;  /* T in [0, 2^27], T max(d, 2f) <= 2^34 (0: the backward's weight gradients become 0, nothing else is written) */
   int32_t d;       /* 1 .. 65536 */
   int32_t f;       /* 1 .. 65536 */
   int32_t dtype;   /* moe_dtype */
 } moe_shared_shape;
 
 /* Elements in a row of h and of each half of gu and dgu_ws in the buffers below: f rounded up to a multiple of 8, so that every row starts at
- * 16 bytes; the elements past f are the library's.  -1 for an invalid shape. */
+ * 16 bytes; the elements past f are written as 0.  -1 for an invalid shape. */
 int64_t moe_shared_ffn_row(const moe_shared_shape* s);
 
 /* Bytes of the workspace of a forward (backward = 0) or backward (1) call; -1 for an invalid shape.  It holds k-split

@@ -20,7 +20,7 @@ def norm_shape(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(rows=-1), dict(d=0), dict(d=B.MOE_NORM_MAX_D + 1), dict(dtype=2), dict(param_dtype=-1),
-                                dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x_stride=63),
+                                dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(x_stride=63), dict(x_stride=1 << 46), dict(rows=1 << 30, y_stride=1 << 20),
                                 dict(y_stride=-64), dict(dx_stride=1)])
 def test_norm_shapes(kw):
     s = norm_shape(**kw)
@@ -38,6 +38,9 @@ def test_norm_arguments():
     refused(f(x=P[0] + 1), "aligned")
     refused(f(w=P[1] + 2), "aligned")
     refused(f(y=P[0] + 64), "overlaps")
+    refused(f(y=P[1]), "overlaps")
+    refused(f(m=P[3]), "overlaps")
+    refused(f(r=P[4] + 8), "overlaps")
     need = B.moe_layer_norm_workspace_bytes(s)
     assert need > 0
     b = lambda **kw: L.moe_layer_norm_backward(ctypes.byref(s), *[kw.get(k, d) for k, d in (
@@ -48,9 +51,9 @@ def test_norm_arguments():
     refused(b(n=need - 1), "too small")
     refused(b(ws=None), "too small")
     refused(b(ws=P[9] + 8), "aligned")
-    refused(b(dx=P[1]), "overlaps x")
-    refused(b(dx=P[0] + 2), "overlaps dy")
-    refused(b(dx=P[5] + 128), "overlaps residual")
+    for kw in (dict(dx=P[1]), dict(dx=P[0] + 2), dict(dx=P[5] + 128), dict(dx=P[2]), dict(dw=P[8]), dict(dw=P[2]), dict(db=P[6]),
+               dict(ws=P[0]), dict(ws=P[7])):
+        refused(b(**kw), "overlaps")
     assert L.moe_layer_norm(None, P[0], P[1], P[2], P[3], None, None, None) == B.MOE_EINVAL
 
 
@@ -64,7 +67,7 @@ def shared_shape(**kw):
 
 
 @pytest.mark.parametrize("kw", [dict(tokens=-1), dict(tokens=(1 << 27) + 1), dict(d=0), dict(d=65537), dict(f=0),
-                                dict(f=65537), dict(dtype=3)])
+                                dict(f=65537), dict(dtype=3), dict(tokens=1 << 20, f=8200)])
 def test_shared_shapes(kw):
     s = shared_shape(**kw)
     assert B.moe_shared_ffn_row(s) == -1
@@ -86,9 +89,9 @@ def test_shared_arguments():
     for k, p in (("x", P[0]), ("wgu", P[1]), ("wd", P[2]), ("res", P[3]), ("h", P[4]), ("gu", P[5]), ("y", P[6]), ("ws", P[7])):
         refused(f(**{k: p + 8}), "aligned")
     for other in (P[0], P[1], P[2], P[4], P[5], P[3] + 16):
-        refused(f(y=other), "y overlaps")
-    refused(f(h=P[0]), "h or gu overlaps")
-    refused(f(gu=P[4]), "h or gu overlaps")
+        refused(f(y=other), "overlaps")
+    for kw in (dict(h=P[0]), dict(gu=P[4]), dict(ws=P[1]), dict(ws=P[6])):
+        refused(f(**kw), "overlaps")
     s0 = shared_shape(d=100, f=36)
     need = B.moe_shared_ffn_workspace_bytes(s0, False)
     if need:
@@ -104,12 +107,12 @@ def test_shared_arguments():
             refused(b(**{k: None}), "null")
         refused(b(**{k: P[B.SHARED_BWD_FIELDS.index(k)] + 4}), "aligned")
     at = dict(zip(B.SHARED_BWD_FIELDS, P))
-    refused(b(dx=at["x"]), "output overlaps an input")
-    refused(b(dx=at["dy"]), "output overlaps an input")
-    refused(b(dgu_ws=at["h"]), "output overlaps an input")
-    refused(b(dgu_ws=at["gu"] + 16), "output overlaps an input")
-    refused(b(dw_down=at["w_down"]), "output overlaps an input")
-    refused(b(dw_down=at["dw_gate_up"]), "two outputs")
+    refused(b(dx=at["x"]), "overlaps")
+    refused(b(dx=at["dy"]), "overlaps")
+    refused(b(dgu_ws=at["h"]), "overlaps")
+    refused(b(dgu_ws=at["gu"] + 16), "overlaps")
+    refused(b(dw_down=at["w_down"]), "overlaps")
+    refused(b(dw_down=at["dw_gate_up"]), "overlaps")
     assert L.moe_shared_ffn_backward(ctypes.byref(s), None, None, 0, None) == B.MOE_EINVAL
 
 
@@ -135,7 +138,7 @@ def bind(tensors, ws=P[15], n=1 << 20):
 
 @pytest.mark.parametrize("kw,words", [
     (dict(n=-1), "elements"), (dict(param_dtype=5), "dtype"), (dict(grad_dtype=-2), "dtype"), (dict(state_bits=16), "bits"),
-    (dict(weight_decay=float("nan")), "finite"), (dict(lr_scale=float("inf")), "finite"), (dict(param=None), "null"),
+    (dict(reserved=1), "reserved"), (dict(n=1 << 37), "too many"), (dict(weight_decay=float("nan")), "finite"), (dict(lr_scale=float("inf")), "finite"), (dict(param=None), "null"),
     (dict(grad=None), "null"), (dict(m=None), "null"), (dict(state_bits=8), "scales"), (dict(m_scale=P[5]), "8-bit"),
     (dict(param=P[0] + 2), "aligned"), (dict(m=P[3] + 1), "aligned"), (dict(copy=P[1] + 1), "aligned"),
     (dict(copy=P[0]), "overlaps"), (dict(m=P[2]), "overlaps"), (dict(v=P[3] + 396), "overlaps"), (dict(grad=P[0] + 4), "overlaps"),

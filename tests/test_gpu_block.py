@@ -221,6 +221,24 @@ def test_shared_ffn_writes_only_its_outputs(T, d, f, dtype):
           ("y", "dx", "dw_gate_up", "dw_down"), (T, d, f, dtype))
 
 
+@pytest.mark.parametrize("T,d,f", [(2, 100, 36), (40, 24, 33), (70, 100, 36), (300, 65, 9), (20, 64, 4), (90, 72, 68)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_ffn_does_not_read_what_it_has_not_written(T, d, f, dtype):
+    """Buffers and workspace full of NaN before the calls: the padding of their rows reaches no result."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, dtype, seed=8)
+    op = SharedFFN(T, d, f, dtype)
+    for t in (op.y, op.h, op.gu, op.dgu, op.dx, op.dw_gate_up, op.dw_down):
+        t.fill_(float("nan"))
+    if op.workspace is not None:
+        op.workspace.fill_(255)
+    want = ref.shared_ffn(x, wgu, wd, residual=res, dy=dy)
+    got = {"y": op.forward(x, wgu, wd), "dx": op.backward(dy, x, wgu, wd, residual=res), "dw_gate_up": op.dw_gate_up,
+           "dw_down": op.dw_down}
+    check(got, want, ("y", "dx", "dw_gate_up", "dw_down"), (T, d, f, dtype))
+
+
 def test_shared_ffn_of_nothing():
     from expert_output_overlap_amd.runtime import SharedFFN
 
