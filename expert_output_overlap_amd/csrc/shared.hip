@@ -113,6 +113,14 @@ __device__ __forceinline__ void finish4(const Gemm& p, int64_t m, int n, f32x4_t
   }
 }
 
+// A product as one or several of a launch's workgroups, one per tile and k-split
+struct Part {
+  Gemm p;
+  int splits;
+  int first, blocks;  // workgroups [first, first + blocks) of the launch; first is a multiple of 8
+  float* partial;     // splits > 1: [splits][M][ld] sums
+  int64_t ld;
+};
 // ---- few tokens --------------------------------------------------------------------------------------------------------
 // The weights stream past once and bound the time.  A workgroup takes RT x 16 rows of the weights (GLU with RT = 1: 8 of the
 // gate's and the same 8 of the up projection's) as one operand of 16x16 products whose other is the tokens, 16 per product;
@@ -158,8 +166,16 @@ __device__ __forceinline__ f32x4_t products(const Chunk32<T>& a, const Chunk32<T
 // The eight waves' sums in wave order, and the epilogue.  A product's element: row 4 (lane / 16) .. + 3 of the weights, token
 // lane % 16
 template <typename T, int EPI, int RT, int MT>
-__device__ __forceinline__ void few_finish(const Gemm& p, int n0, int tid, const f32x4_t (*part)[RT * MT][64]) {
+__device__ __forceinline__ void few_finish(const Part& a, int n0, int tid, const f32x4_t (*part)[RT * MT][64]) {
+  const Gemm& p = a.p;
   const int lane = tid & 63;
+  auto out = [&](int64_t m, int n, const f32x4_t& v, const f32x4_t& w) {
+    if (a.partial) {
+      float* o = a.partial + ((int64_t)blockIdx.y * p.M + m) * a.ld + n;
+      *(f32x4_t*)o = v;
+      if (EPI == EPI_GLU) *(f32x4_t*)(o + a.ld / 2) = w;
+    } else finish4<T, EPI>(p, m, n, v, w);
+  };
   auto sum = [&](int i, int l) {
     f32x4_t v = part[0][i][l];
 #pragma unroll
@@ -171,17 +187,18 @@ __device__ __forceinline__ void few_finish(const Gemm& p, int n0, int tid, const
     if (tid >= MT * L) return;
     const int m = tid / L, l = tid % L, tok = 16 * m + (l & 15), n = n0 + 4 * (l >> 4);
     if (tok >= p.M || n >= p.N) return;
-    finish4<T, EPI>(p, tok, n, sum(m, l), RT == 1 ? sum(m, l + 32) : sum(MT + m, l));
+    out(tok, n, sum(m, l), RT == 1 ? sum(m, l + 32) : sum(MT + m, l));
   } else {
     if (tid >= RT * MT * 64) return;
     const int i = tid >> 6, t = i / MT, m = i % MT, tok = 16 * m + (lane & 15), n = n0 + 16 * t + 4 * (lane >> 4);
     if (tok >= p.M || n >= p.N) return;
-    finish4<T, EPI>(p, tok, n, sum(i, lane), f32x4_t{0.f, 0.f, 0.f, 0.f});
+    out(tok, n, sum(i, lane), f32x4_t{0.f, 0.f, 0.f, 0.f});
   }
 }
 
 template <typename T, int EPI, int RT, int MT, int SU>
-__global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
+__global__ __launch_bounds__(512) void k_gemm_few(Part a) {
+  const Gemm& p = a.p;
   constexpr int CH = 128 / sizeof(T), NW = 8;
   constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;  // columns of C
   __shared__ f32x4_t part[NW][RT * MT][64];
@@ -202,17 +219,18 @@ __global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const int whole = p.K / CH;  // chunks that are full
+  // this split's chunks that are full, [begin, whole)
+  const int all = p.K / CH, begin = (int)((int64_t)all * blockIdx.y / a.splits), whole = (int)((int64_t)all * (blockIdx.y + 1) / a.splits);
   auto chunks = [&](int c, auto count, bool cut) {  // chunks c, c + NW, ..
     constexpr int U = decltype(count)::value;
-    Chunk32<T> a[U][RT], b[U][MT];
+    Chunk32<T> cw[U][RT], cx[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = (c + u * NW) * CH, n = cut ? p.K - k - q * (int)(32 / sizeof(T)) : CH;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) a[u][t].load(w[t] + k, n);
+      for (int t = 0; t < RT; ++t) cw[u][t].load(w[t] + k, n);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) b[u][m].load(x[m] + k, n);
+      for (int m = 0; m < MT; ++m) cx[u][m].load(x[m] + k, n);
     }
     __builtin_amdgcn_sched_barrier(0);  // every load goes out before the first product waits for one
 #pragma unroll
@@ -220,29 +238,22 @@ __global__ __launch_bounds__(512) void k_gemm_few(Gemm p) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = products(a[u][t], b[u][m], acc[t][m]);
+        for (int m = 0; m < MT; ++m) acc[t][m] = products(cw[u][t], cx[u][m], acc[t][m]);
   };
-  int c = wave;
+  int c = begin + wave;
   for (; c + (SU - 1) * NW < whole; c += SU * NW) chunks(c, std::integral_constant<int, SU>{}, false);
   if (SU >= 4 && c + ((SU + 1) / 2 - 1) * NW < whole) {
     chunks(c, std::integral_constant<int, (SU + 1) / 2>{}, false);
     c += (SU + 1) / 2 * NW;
   }
   for (; c < whole; c += NW) chunks(c, std::integral_constant<int, 1>{}, false);
-  if (c == whole && p.K % CH) chunks(c, std::integral_constant<int, 1>{}, true);
+  if (c == all && p.K % CH) chunks(c, std::integral_constant<int, 1>{}, true);
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
     for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
   __syncthreads();
-  few_finish<T, EPI, RT, MT>(p, n0, tid, part);
-}
-
-template <typename T, int EPI, int RT, int MT, int SU>
-int few(const Gemm& p, hipStream_t st) {
-  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;
-  hipLaunchKernelGGL((k_gemm_few<T, EPI, RT, MT, SU>), dim3((unsigned)((p.N + COLS - 1) / COLS)), dim3(512), 0, st, p);
-  return hipGetLastError() == hipSuccess ? 0 : -1;
+  few_finish<T, EPI, RT, MT>(a, n0, tid, part);
 }
 
 // Rows that start at 16 bytes: both operands through LDS.  Each wave has a ring of D slots of its own, which LDS-DMA loads of
@@ -251,7 +262,8 @@ int few(const Gemm& p, hipStream_t st) {
 // too), 24 tokens 83 instead of 107; 72 us is what the weights take at 4.9 TB/s.  Few slots suffice, since more of them let
 // fewer workgroups into a CU.  16-byte piece c of row r of a slot stands at piece c ^ swz(r): a read's 16 rows hit all banks.
 template <typename T, int EPI, int RT, int MT, int D>
-__global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
+__global__ __launch_bounds__(512) void k_gemm_ring(Part a) {
+  const Gemm& p = a.p;
   constexpr int ES = sizeof(T), CK = 128 / ES, NW = 8, SLOT = (RT + MT) * 2048;
   constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT;  // columns of C
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -280,9 +292,11 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
   const unsigned char* xbase = (const unsigned char*)p.a;
   unsigned char* ring = smem + wave * D * SLOT;
   const uint32_t lds0 = (uint32_t)(uintptr_t)ring;
-  const int chunks = p.K / CK, mine = chunks > wave ? (chunks - wave + NW - 1) / NW : 0;
+  // this split's whole chunks, and this wave's of them
+  const int all = p.K / CK, begin = (int)((int64_t)all * blockIdx.y / a.splits);
+  const int chunks = (int)((int64_t)all * (blockIdx.y + 1) / a.splits) - begin, mine = chunks > wave ? (chunks - wave + NW - 1) / NW : 0;
   auto load = [&](int j) {  // this wave's chunk j
-    const int64_t at = (int64_t)(wave + j * NW) * 128;
+    const int64_t at = (int64_t)(begin + wave + j * NW) * 128;
     const uint32_t slot = lds0 + j % D * SLOT;
 #pragma unroll
     for (int t = 0; t < RT + MT; ++t)
@@ -335,7 +349,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
   }
   if (j < mine) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   for (; j < mine; ++j) use(j);
-  if (p.K % CK && chunks % NW == wave) {  // the rest of the rows, under 128 bytes in whole pieces
+  if (p.K % CK && blockIdx.y + 1 == gridDim.y && chunks % NW == wave) {  // the rest of the rows, under 128 bytes in whole pieces
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = (4 * h + q) * 16;
@@ -343,7 +357,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
 #pragma unroll
       for (int t = 0; t < RT + MT; ++t) {
         const unsigned char* s = t < RT ? wbase + wrow(t, r) : xbase + xrow(t - RT, r);
-        f[t] = c < p.K % CK * ES ? *(const u32x4_t*)(s + (int64_t)chunks * 128 + c) : u32x4_t{0u, 0u, 0u, 0u};
+        f[t] = c < p.K % CK * ES ? *(const u32x4_t*)(s + (int64_t)all * 128 + c) : u32x4_t{0u, 0u, 0u, 0u};
       }
       multiply(f);
     }
@@ -355,37 +369,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Gemm p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
   __syncthreads();
-  few_finish<T, EPI, RT, MT>(p, n0, tid, part);
-}
-
-template <typename T, int EPI, int RT, int MT, int D>
-int ring(const Gemm& p, hipStream_t st) {
-  constexpr int COLS = EPI == EPI_GLU ? 8 * RT : 16 * RT, LDS = 8 * D * (RT + MT) * 2048;
-  const void* k = (const void*)k_gemm_ring<T, EPI, RT, MT, D>;
-  if (LDS > 65536 && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, LDS) != hipSuccess) return -1;
-  void* params[] = {(void*)&p};
-  return hipLaunchKernel(k, dim3((unsigned)((p.N + COLS - 1) / COLS)), dim3(512), params, LDS, st) == hipSuccess ? 0 : -1;
-}
-
-// Whether the weights stream past (gemm_few), or the tokens are many enough for tiles.  Measured: 4096 x 14336 with 32 tokens
-// 87 us against 91 for 40 in tiles, with 64 tokens 121 against 82 (each weight meets four products' worth of tokens); 7168 x
-// 2048 with 40 tokens 32 and 34, with 64 both 37; 2048 x 1408 with 64 tokens 11 and 21 (tiles need k-splits there).
-bool few_tokens(int64_t tokens, int d, int f, int elem) {
-  const int piece = 16 / elem;
-  return tokens <= 32 || (tokens <= 64 && d % piece == 0 && f % piece == 0 && (int64_t)d * f * elem <= 1 << 25);
-}
-
-template <typename T, int EPI>
-int gemm_few(const Gemm& p, hipStream_t st) {
-  constexpr int PER = 16 / sizeof(T);  // elements of a 16-byte piece
-  if (p.lda % PER == 0 && p.ldb % PER == 0 && p.K % PER == 0 && ((int64_t)p.up + 32) * p.ldb * (int)sizeof(T) < (1ll << 32)) {
-    if (p.M <= 16) return ring<T, EPI, 1, 1, 2>(p, st);
-    if (p.M <= 32) return ring<T, EPI, 1, 2, 1>(p, st);
-    if (p.M <= 48) return ring<T, EPI, 1, 3, 1>(p, st);
-    return ring<T, EPI, 1, 4, 1>(p, st);
-  }
-  if (p.M <= 16) return few<T, EPI, 1, 1, 4>(p, st);
-  return few<T, EPI, 1, 2, 2>(p, st);
+  few_finish<T, EPI, RT, MT>(a, n0, tid, part);
 }
 
 // ---- bf16 tiles ------------------------------------------------------------------------------------------------------
@@ -631,14 +615,6 @@ struct Tile {
   }
 };
 
-// A product as one or several of a launch's workgroups, one per tile and k-split
-struct Part {
-  Gemm p;
-  int splits;
-  int first, blocks;  // workgroups [first, first + blocks) of the launch; first is a multiple of 8
-  float* partial;     // splits > 1: [splits][M][ld] sums
-  int64_t ld;
-};
 struct Parts {  // dx, dw_gate_up, dw_down
   Part part[3];
 };
@@ -787,6 +763,55 @@ int grads_tiles(const Gemm* const (&p)[3], const int (&splits)[3], float* partia
 // Floats that a product's k-splits may take, and how many splits
 constexpr int64_t PARTIAL = 512ll * 128 * 128;
 constexpr int MAX_SPLITS = 16;
+
+// Few tokens: k-splits up to a workgroup for each CU, of four chunks for each wave at least
+template <typename T, int EPI, int COLS>
+Part few_part(const Gemm& p, float* partial) {
+  const int64_t groups = (p.N + COLS - 1) / COLS, ld = partial_cols(p, EPI);
+  const int64_t most = std::min(std::min(256 / groups, (int64_t)MAX_SPLITS), std::min<int64_t>(p.K * (int64_t)sizeof(T) / 128 / 32, PARTIAL / (p.M * ld)));
+  const int splits = (int)std::max<int64_t>(1, most);
+  return {p, splits, 0, (int)groups, splits > 1 ? partial : nullptr, ld};
+}
+
+template <typename T, int EPI, int RT, int MT, int SU>
+int few(const Gemm& p, float* partial, hipStream_t st) {
+  const Part a = few_part<T, EPI, EPI == EPI_GLU ? 8 * RT : 16 * RT>(p, partial);
+  hipLaunchKernelGGL((k_gemm_few<T, EPI, RT, MT, SU>), dim3(a.blocks, a.splits), dim3(512), 0, st, a);
+  if (hipGetLastError() != hipSuccess) return -1;
+  return launch_finish<T, EPI>(a, st);
+}
+
+template <typename T, int EPI, int RT, int MT, int D>
+int ring(const Gemm& p, float* partial, hipStream_t st) {
+  constexpr int LDS = 8 * D * (RT + MT) * 2048;
+  const Part a = few_part<T, EPI, EPI == EPI_GLU ? 8 * RT : 16 * RT>(p, partial);
+  const void* k = (const void*)k_gemm_ring<T, EPI, RT, MT, D>;
+  if (LDS > 65536 && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, LDS) != hipSuccess) return -1;
+  void* params[] = {(void*)&a};
+  if (hipLaunchKernel(k, dim3(a.blocks, a.splits), dim3(512), params, LDS, st) != hipSuccess) return -1;
+  return launch_finish<T, EPI>(a, st);
+}
+
+// Whether the weights stream past (gemm_few), or the tokens are many enough for tiles.  Measured: 4096 x 14336 with 32 tokens
+// 87 us against 91 for 40 in tiles, with 64 tokens 121 against 82 (each weight meets four products' worth of tokens); 7168 x
+// 2048 with 40 tokens 32 and 34, with 64 both 37; 2048 x 1408 with 64 tokens 11 and 21 (tiles need k-splits there).
+bool few_tokens(int64_t tokens, int d, int f, int elem) {
+  const int piece = 16 / elem;
+  return tokens <= 32 || (tokens <= 64 && d % piece == 0 && f % piece == 0 && (int64_t)d * f * elem <= 1 << 25);
+}
+
+template <typename T, int EPI>
+int gemm_few(const Gemm& p, float* partial, hipStream_t st) {
+  constexpr int PER = 16 / sizeof(T);  // elements of a 16-byte piece
+  if (p.lda % PER == 0 && p.ldb % PER == 0 && p.K % PER == 0 && ((int64_t)p.up + 32) * p.ldb * (int)sizeof(T) < (1ll << 32)) {
+    if (p.M <= 16) return ring<T, EPI, 1, 1, 2>(p, partial, st);
+    if (p.M <= 32) return ring<T, EPI, 1, 2, 1>(p, partial, st);
+    if (p.M <= 48) return ring<T, EPI, 1, 3, 1>(p, partial, st);
+    return ring<T, EPI, 1, 4, 1>(p, partial, st);
+  }
+  if (p.M <= 16) return few<T, EPI, 1, 1, 4>(p, partial, st);
+  return few<T, EPI, 1, 2, 2>(p, partial, st);
+}
 
 // Tile and k-splits of a product, by an estimate of its time from what the tiles measured (us per k-tile of 64, operands
 // from HBM).  256 x 256: 1.5 with one workgroup on each CU.  128 x 128 in two stages: 0.85 where a CU has one workgroup, 1.05
@@ -1046,16 +1071,16 @@ __global__ __launch_bounds__(256) void k_grads_f32(Parts a) {
   else if (mine(a.part[1]) || mine(a.part[2])) f32_tile<EPI_STORE, true, true>(a.part[mine(a.part[1]) ? 1 : 2], sh);
 }
 
-// splits of a product of which a launch has `tiles` tiles in all: up to four workgroups for each CU, of 256 k at least
-int f32_splits(const Gemm& p, int epi, int64_t tiles, int64_t room) {
-  return (int)std::max<int64_t>(1, std::min(std::min(1024 / tiles, room / (p.M * partial_cols(p, epi))), std::min<int64_t>(MAX_SPLITS, p.K / 256)));
+// splits of a product of so many tiles: up to four workgroups for each CU, of 256 k at least
+int f32_splits(const Gemm& p, int epi, int64_t tiles) {
+  return (int)std::max<int64_t>(1, std::min(std::min(1024 / tiles, PARTIAL / (p.M * partial_cols(p, epi))), std::min<int64_t>(MAX_SPLITS, p.K / 256)));
 }
 
 template <int EPI, bool BCOL>
 int gemm_f32(const Gemm& p, float* partial, hipStream_t st) {
   Part a;
   if (!make_part(&a, p, EPI, 64, 64, 1, partial, 0)) return -1;
-  if (!make_part(&a, p, EPI, 64, 64, f32_splits(p, EPI, a.blocks, PARTIAL), partial, 0)) return -1;
+  if (!make_part(&a, p, EPI, 64, 64, f32_splits(p, EPI, a.blocks), partial, 0)) return -1;
   hipLaunchKernelGGL((k_gemm_f32<EPI, BCOL>), dim3((unsigned)a.blocks), dim3(256), 0, st, a);
   if (hipGetLastError() != hipSuccess) return -1;
   return launch_finish<float, EPI>(a, st);
@@ -1063,12 +1088,16 @@ int gemm_f32(const Gemm& p, float* partial, hipStream_t st) {
 
 int grads_f32(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
   Parts g;
-  int64_t blocks, room = PARTIAL;
+  int64_t blocks, room = PARTIAL, work = 0;
   int splits[3] = {1, 1, 1};
   if (!make_grads(&g, p, 64, 64, splits, partial, &blocks)) return -1;
+  for (int i = 0; i < 3; ++i) work += (int64_t)g.part[i].blocks * ((p[i]->K + FK - 1) / FK);
+  // sums no longer than what four workgroups on each CU would take of the whole, but of 256 k at least
+  const int64_t len = std::max<int64_t>(256 / FK, work / 1024);
   for (int i = 0; i < 3; ++i) {
-    if (p[i]->M > 0) splits[i] = f32_splits(*p[i], EPI_STORE, blocks, room);
-    if (splits[i] > 1) room -= splits[i] * p[i]->M * partial_cols(*p[i], EPI_STORE);
+    const int64_t floats = p[i]->M * partial_cols(*p[i], EPI_STORE);
+    if (floats > 0) splits[i] = (int)std::max<int64_t>(1, std::min(std::min<int64_t>(MAX_SPLITS, p[i]->K / FK / len), room / floats));
+    if (splits[i] > 1) room -= splits[i] * floats;
   }
   if (!make_grads(&g, p, 64, 64, splits, partial, &blocks)) return -1;
   hipLaunchKernelGGL(k_grads_f32, dim3((unsigned)blocks), dim3(256), 0, st, g);
@@ -1175,8 +1204,8 @@ int run_f32(const SharedLaunch& s, hipStream_t st) {
   int rc;
   if (!s.backward) {
     if (few_tokens(s.tokens, s.d, s.f, 4)) {
-      if ((rc = gemm_few<float, EPI_GLU>(b.glu, st))) return rc;
-      return gemm_few<float, EPI_STORE>(b.down, st);
+      if ((rc = gemm_few<float, EPI_GLU>(b.glu, partial, st))) return rc;
+      return gemm_few<float, EPI_STORE>(b.down, partial, st);
     }
     if ((rc = gemm_f32<EPI_GLU, false>(b.glu, partial, st))) return rc;
     return gemm_f32<EPI_STORE, false>(b.down, partial, st);
@@ -1193,8 +1222,8 @@ int run_bf16(const SharedLaunch& s, hipStream_t st) {
   }
   if (!s.backward && few_tokens(s.tokens, s.d, s.f, 2)) {
     const Block b = block_f32(s);  // the operands as they are
-    if ((rc = gemm_few<bf16_t, EPI_GLU>(b.glu, st))) return rc;
-    return gemm_few<bf16_t, EPI_STORE>(b.down, st);
+    if ((rc = gemm_few<bf16_t, EPI_GLU>(b.glu, (float*)s.workspace, st))) return rc;
+    return gemm_few<bf16_t, EPI_STORE>(b.down, (float*)s.workspace, st);
   }
   int64_t n[4];
   pack_sizes(s.tokens, s.d, s.f, s.backward, n);
