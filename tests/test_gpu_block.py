@@ -156,7 +156,9 @@ def test_shared_ffn(T, d, f, dtype):
 
 
 @pytest.mark.parametrize("T,d,f,dtype", [(4096, 1024, 768, "bf16"), (3, 2048, 5632, "bf16"), (40, 4096, 3000, "bf16"),
-                                         (1500, 2000, 1000, "bf16"), (600, 700, 800, "f32")])
+                                         (1500, 2000, 1000, "bf16"), (600, 700, 800, "f32"),
+                                         (2, 192, 6895, "f32"), (2, 192, 13790, "bf16"), (20, 48, 9001, "bf16"),
+                                         (50, 4096, 64, "bf16"), (60, 264, 6000, "f32"), (300, 7168, 520, "bf16")])
 def test_shared_ffn_larger(T, d, f, dtype):
     """Sizes where the products split, or fill the device several times; the same call twice gives the same bits."""
     from expert_output_overlap_amd.runtime import SharedFFN
