@@ -620,7 +620,11 @@ struct Parts {  // dx, dw_gate_up, dw_down
 };
 
 // Workgroups go round the eight XCDs, so a run of 1/8 of a product's tiles is one XCD's, whose L2 its tiles share: bands of
-// eight tile rows, walked column by column.
+// BAND tile rows, walked column by column. An XCD's 32 tiles at a time read BAND row and 32 / BAND column blocks, fewest at
+// five or six. Forward and backward, us (16384 x 7168 x 2048; 8192 x 4096 x 4096): 4 rows 1222 + 2329; 694 + 1373, 6 rows
+// 1213 + 2343; 685 + 1313, 8 rows 1268 + 2379; 705 + 1358, 16 rows 1290 + 2440 at the first.
+constexpr int BAND = 6;
+
 template <class G>
 __device__ __forceinline__ void bf16_tile(const Part& a, int bm, unsigned char* smem) {
   const Gemm& p = a.p;
@@ -633,9 +637,9 @@ __device__ __forceinline__ void bf16_tile(const Part& a, int bm, unsigned char* 
   }
   const int s = i / tiles;
   i -= s * tiles;
-  const int band = i / (8 * nt), rows = min(8, mt - band * 8), r = i - band * 8 * nt;
+  const int band = i / (BAND * nt), rows = min(BAND, mt - band * BAND), r = i - band * BAND * nt;
   const int t0 = (int)((int64_t)nkt * s / a.splits), t1 = (int)((int64_t)nkt * (s + 1) / a.splits);
-  G::run(p, smem, (band * 8 + r % rows) * bm, (r / rows) * G::COLS, t0, t1 - t0,
+  G::run(p, smem, (band * BAND + r % rows) * bm, (r / rows) * G::COLS, t0, t1 - t0,
          a.partial ? a.partial + (int64_t)s * p.M * a.ld : nullptr, a.ld);
 }
 
