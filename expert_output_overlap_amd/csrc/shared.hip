@@ -939,8 +939,10 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   const int t0 = (int)((int64_t)nkt * s / part.splits), t1 = (int)((int64_t)nkt * (s + 1) / part.splits);
   const float *A = (const float*)p.a, *B = (const float*)p.b;
 
-  // eight neighbours along memory per thread and operand: by rows, k 8 (tid % 4) .. of row tid / 4; by columns, rows
-  // 4 (tid % 16) .. of k tid / 16 and tid / 16 + 16.  Outside the matrix: 0
+  // eight elements per thread and operand: by rows, k 8 (tid % 4) .. of row tid / 4; by columns, four neighbouring rows of
+  // k kc and kc + 16, a wave's 8 x 8 lanes over 32 rows (a line) and 8 k, so that its LDS stores hit 32 banks (16 rows by 4 k hit 16: the
+  // backward at 4096 x 2048 x 2048 2124 -> 1938 us).  Outside the matrix: 0
+  const int rc = 4 * (lane & 7) + 32 * (wave & 1), kc = (lane >> 3) + 8 * (wave >> 1);
   f32x4_t rega[2][2], regb[2][2];  // of two k-tiles: a load has two k-tiles' time to arrive
   // contiguous elements c .. c + 3 at q, those from limit on 0 (in: whether any are wanted): no branch, so that all of a
   // thread's loads go out together
@@ -957,11 +959,11 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   };
   // a k-tile that ends before the last k and does not straddle a_seg: whole fours from a lane's fixed places.  Rows past the
   // matrix read its first; columns past it read the next row (the last k is not in such a k-tile); neither is stored
-  const int ca = m0 + 4 * (tid & 15), cb = n0 + 4 * (tid & 15), row = tid >> 2;
-  const float* pa = ACOL ? A + (int64_t)(tid >> 4) * p.lda + (ca < p.M ? ca : 0)
+  const int ca = m0 + rc, cb = n0 + rc, row = tid >> 2;
+  const float* pa = ACOL ? A + (int64_t)kc * p.lda + (ca < p.M ? ca : 0)
                          : A + (int64_t)(m0 + row < p.M ? m0 + row : 0) * p.lda + 8 * (tid & 3);
   const int rb_row = n0 + (row & (BN - 1));
-  const float* pb = BCOL ? B + (int64_t)(tid >> 4) * p.ldb + (cb < p.n_in ? cb : 0)
+  const float* pb = BCOL ? B + (int64_t)kc * p.ldb + (cb < p.n_in ? cb : 0)
                          : B + ((rb_row < p.n_in ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
   const bool wide = p.lda >= 4 && p.ldb >= 4;
   auto fetch = [&](int kt, f32x4_t* ra, f32x4_t* rb) {
@@ -977,10 +979,10 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int kc = k0 + (tid >> 4) + 16 * h, kr = k0 + 8 * (tid & 3) + 4 * h, last = p.K - 1;
-      ra[h] = ACOL ? four(A + (int64_t)min(kc, last) * p.lda, ca, p.M, 0x7fffffff, 0, kc <= last)
+      const int k = k0 + kc + 16 * h, kr = k0 + 8 * (tid & 3) + 4 * h, last = p.K - 1;
+      ra[h] = ACOL ? four(A + (int64_t)min(k, last) * p.lda, ca, p.M, 0x7fffffff, 0, k <= last)
                    : four(A + (int64_t)min(m0 + row, p.M - 1) * p.lda, kr, p.K, p.a_seg, p.a_jump, true);
-      rb[h] = BCOL ? four(B + (int64_t)min(kc, last) * p.ldb, cb, p.n_in, 0x7fffffff, 0, kc <= last)
+      rb[h] = BCOL ? four(B + (int64_t)min(k, last) * p.ldb, cb, p.n_in, 0x7fffffff, 0, k <= last)
                    : four(B + (min(rb_row, p.n_in - 1) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb, kr, p.K, 0x7fffffff, 0, true);
     }
   };
@@ -989,12 +991,12 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
     for (int h = 0; h < 2; ++h) {
       if (ACOL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[st][4 * (tid & 15) + i][(tid >> 4) + 16 * h] = ra[h][i];
-      } else *(f32x4_t*)&sa[st][tid >> 2][8 * (tid & 3) + 4 * h] = ra[h];
+        for (int i = 0; i < 4; ++i) sa[st][rc + i][kc + 16 * h] = ra[h][i];
+      } else *(f32x4_t*)&sa[st][row][8 * (tid & 3) + 4 * h] = ra[h];
       if (BCOL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sb[st][4 * (tid & 15) + i][(tid >> 4) + 16 * h] = rb[h][i];
-      } else *(f32x4_t*)&sb[st][tid >> 2][8 * (tid & 3) + 4 * h] = rb[h];
+        for (int i = 0; i < 4; ++i) sb[st][rc + i][kc + 16 * h] = rb[h][i];
+      } else *(f32x4_t*)&sb[st][row][8 * (tid & 3) + 4 * h] = rb[h];
     }
   };
 
@@ -1006,7 +1008,7 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
     for (int i = 0; i < 2; ++i) acc[j][i] = total[j][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int r = lane & 15, q = lane >> 4;
   const int brow[2] = {EPI == EPI_GLU ? wn * 16 : wn * 32, EPI == EPI_GLU ? 32 + wn * 16 : wn * 32 + 16};
-  auto ktile = [&](auto parity, int kt) {  // stage and registers of k-tile kt - t0 even or odd
+  auto ktile = [&](auto parity, int kt) {  // k-tile kt - t0 even or odd
     constexpr int st = decltype(parity)::value;
     __syncthreads();
     if (kt + 2 < t1) fetch(kt + 2, rega[st], regb[st]);
@@ -1061,13 +1063,15 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   }
 }
 
+// Four workgroups on a CU, at 128 registers and no spill: forward and backward at 4096 x 2048 x 2048 877 + 1751 us (117.5
+// TFLOP/s of the 153 of a large fp32 product); left to the compiler's choice of registers 925 + 1938.
 template <int EPI, bool BCOL>
-__global__ __launch_bounds__(256) void k_gemm_f32(Part a) {
+__global__ __launch_bounds__(256, 4) void k_gemm_f32(Part a) {
   __shared__ __align__(16) F32Stage sh;
   f32_tile<EPI, false, BCOL>(a, sh);
 }
 
-__global__ __launch_bounds__(256) void k_grads_f32(Parts a) {
+__global__ __launch_bounds__(256, 4) void k_grads_f32(Parts a) {
   __shared__ __align__(16) F32Stage sh;
   const int i = blockIdx.x;
   auto mine = [&](const Part& q) { return i >= q.first && i < q.first + q.blocks; };
