@@ -218,16 +218,15 @@ __device__ __forceinline__ void step_chunk(const AdamwDesc& t, int64_t start, co
     for (int e = 0; e < 4; ++e) {
       const float q = g[k][e] * gs;
       if (BITS8) {
-        // each product and sum rounded by itself, and the root correctly: what decides between two codes is then the formula's
+        // each product and sum rounded by itself, as the root is: what decides between two codes is then the formula's
         // plain fp32 evaluation, the same in any program, not what a compiler made of it
         m[k][e] = __fadd_rn(__fmul_rn(h.beta1, m[k][e]), __fmul_rn(h.one1, q));
         v[k][e] = __fadd_rn(__fmul_rn(h.beta2, v[k][e]), __fmul_rn(h.one2, __fmul_rn(q, q)));
-        root[e] = __fsqrt_rn(v[k][e]);
       } else {
         m[k][e] = fmaf(h.beta1, m[k][e], h.one1 * q);
         v[k][e] = fmaf(h.beta2, v[k][e], h.one2 * q * q);
-        root[e] = __builtin_amdgcn_sqrtf(v[k][e]);  // 1 ulp
       }
+      root[e] = __fsqrt_rn(v[k][e]);  // right for subnormals too: the root of a v of 1e-42 still divides where eps is small
       const float den = fmaf(root[e], h.inv_root_c2, h.eps);
       // both parts of the change before it meets p: 1 - lr weight_decay, rounded, would lose most of a small decay
       p[k][e] -= fmaf(rate * m[k][e], __builtin_amdgcn_rcpf(den), decay * p[k][e]);

@@ -18,24 +18,29 @@ bool is_dtype(int t) { return t == MOE_BF16 || t == MOE_F32; }
 
 bool off(const void* p, uintptr_t align) { return (uintptr_t)p % align != 0; }
 
-// Bytes [p, p + n) of two buffers in common
-bool meet(const void* p, int64_t n, const void* q, int64_t m) {
-  return p && q && n > 0 && m > 0 && (uintptr_t)p < (uintptr_t)q + (uintptr_t)m && (uintptr_t)q < (uintptr_t)p + (uintptr_t)n;
-}
-
-struct Span {
+struct Span {  // n bytes, or rows of `row` bytes every `stride` bytes in them
   const void* p;
-  int64_t n;
+  int64_t n, row = 0, stride = 0;
 };
+
+// Bytes of two buffers in common.  Rows of one stride may lie between each other's, as two slices of one wider tensor do
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
+  if (!p || !q || a.n <= 0 || b.n <= 0 || p >= q + (uintptr_t)b.n || q >= p + (uintptr_t)a.n) return false;
+  if (a.stride == 0 || a.stride != b.stride) return true;
+  const int64_t s = a.stride, to = (int64_t)((p < q ? q - p : p - q) % (uintptr_t)s);  // from the lower one's row on
+  const Span &low = p < q ? a : b, &high = p < q ? b : a;
+  return to < low.row || to + high.row > s;
+}
 
 // Whether an output overlaps an input or another output; same(o, i): a pair that may be the same buffer
 template <int O, int I, class F>
 bool overlaps(const Span (&out)[O], const Span (&in)[I], F same) {
   for (int o = 0; o < O; ++o) {
     for (int i = 0; i < I; ++i)
-      if (meet(out[o].p, out[o].n, in[i].p, in[i].n) && !(out[o].p == in[i].p && same(o, i))) return true;
+      if (meet(out[o], in[i]) && !(out[o].p == in[i].p && same(o, i))) return true;
     for (int q = 0; q < o; ++q)
-      if (meet(out[o].p, out[o].n, out[q].p, out[q].n)) return true;
+      if (meet(out[o], out[q])) return true;
   }
   return false;
 }
@@ -63,6 +68,12 @@ NormLaunch norm_of(const moe_norm_shape* s) {
   a.y_stride = s->y_stride ? s->y_stride : s->d;
   a.dx_stride = s->dx_stride ? s->dx_stride : s->d;
   return a;
+}
+
+// All rows of a matrix of the norm's, one every `stride` elements
+Span norm_rows(const moe_norm_shape* s, const void* p, int64_t stride) {
+  const int64_t es = elem(s->dtype);
+  return {p, ((s->rows - 1) * stride + s->d) * es, s->d * es, stride * es};
 }
 
 const char* check_shared(const moe_shared_shape* s) {
@@ -135,9 +146,9 @@ int moe_layer_norm(const moe_norm_shape* s, const void* x, const void* weight, c
     return moe_fail(MOE_EINVAL, "a tensor must be aligned to its elements");
   NormLaunch a = norm_of(s);
   if (s->rows > 0) {
-    const int64_t es = elem(s->dtype), r = s->rows - 1, np = s->d * elem(s->param_dtype);
-    const Span out[] = {{y, (r * a.y_stride + s->d) * es}, {mean, 4 * s->rows}, {rstd, 4 * s->rows}},
-               in[] = {{x, (r * a.x_stride + s->d) * es}, {weight, np}, {bias, np}};
+    const int64_t np = s->d * elem(s->param_dtype);
+    const Span out[] = {norm_rows(s, y, a.y_stride), {mean, 4 * s->rows}, {rstd, 4 * s->rows}},
+               in[] = {norm_rows(s, x, a.x_stride), {weight, np}, {bias, np}};
     if (overlaps(out, in, [&](int o, int i) { return o == 0 && i == 0 && a.x_stride == a.y_stride; }))
       return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   }
@@ -170,11 +181,10 @@ int moe_layer_norm_backward(const moe_norm_shape* s, const void* dy, const void*
     if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
   }
   if (s->rows > 0) {
-    const int64_t es = elem(s->dtype), r = s->rows - 1, np = s->d * elem(s->param_dtype);
-    const Span out[] = {{dx, (r * a.dx_stride + s->d) * es}, {dweight, np}, {dbias, np},
+    const int64_t np = s->d * elem(s->param_dtype);
+    const Span out[] = {norm_rows(s, dx, a.dx_stride), {dweight, np}, {dbias, np},
                         {params ? workspace : nullptr, moe_layer_norm_workspace_bytes(s)}},
-               in[] = {{dy, (r * a.y_stride + s->d) * es}, {residual, (r * a.dx_stride + s->d) * es},
-                       {x, (r * a.x_stride + s->d) * es}, {weight, np}, {mean, 4 * s->rows}, {rstd, 4 * s->rows}};
+               in[] = {norm_rows(s, dy, a.y_stride), norm_rows(s, residual, a.dx_stride), norm_rows(s, x, a.x_stride), {weight, np}, {mean, 4 * s->rows}, {rstd, 4 * s->rows}};
     if (overlaps(out, in, [&](int o, int i) { return o == 0 && (i == 1 || (i == 0 && a.y_stride == a.dx_stride)); }))
       return moe_fail(MOE_EINVAL, "an output overlaps an input or another output");
   }
@@ -288,7 +298,7 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
       uintptr_t at, end;
       bool written;
     };
-    std::vector<Range> spans;
+    std::vector<Range> spans{{(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)need, true}};
     int n8 = 0;
     for (int i = 0; i < n_tensors; ++i) {
       const moe_adamw_tensor& a = t[i];
@@ -299,9 +309,9 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
       const struct { const void* p; int64_t n; } out[] = {{a.param, a.n * elem(a.param_dtype)}, {a.copy, a.n * 2},
                                                           {a.m, a.n * ss}, {a.v, a.n * ss}, {a.m_scale, blocks},
                                                           {a.v_scale, blocks}, {a.m_values, a.n * 2},
-                                                          {a.root_values, a.n * 2}, {workspace, need}};
+                                                          {a.root_values, a.n * 2}};
       for (const auto& o : out)
-        if (o.p && (o.p != workspace || i == 0)) spans.push_back({(uintptr_t)o.p, (uintptr_t)o.p + (uintptr_t)o.n, true});
+        if (o.p) spans.push_back({(uintptr_t)o.p, (uintptr_t)o.p + (uintptr_t)o.n, true});
       spans.push_back({(uintptr_t)a.grad, (uintptr_t)a.grad + (uintptr_t)(a.n * elem(a.grad_dtype)), false});
     }
     std::sort(spans.begin(), spans.end(), [](const Range& a, const Range& b) { return a.at < b.at; });

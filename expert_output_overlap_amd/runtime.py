@@ -366,6 +366,8 @@ class AdamW:
     @staticmethod
     def states(p: torch.Tensor, bits: int = 32) -> dict:
         """The states of a tensor before its first step: zeros."""
+        if bits not in (8, 32):
+            raise ValueError("states in 8 or 32 bits, not %r" % (bits,))
         n, z = p.numel(), dict(device=p.device)
         if bits == 32:
             return {k: torch.zeros(n, **z) for k in ("m", "v")}

@@ -360,7 +360,8 @@ int moe_combine_backward(const moe_shape* s, const moe_layout* L, const void* d_
  * Statistics and sums in fp32 (the variance from the differences to the mean), each result rounded once.  The rows'
  * sums of the weight's gradient run in a fixed order, so equal calls on equal devices give equal bits.
  * Any alignment and any row stride >= d; elements between rows are neither read nor written.  An output may not overlap
- * an input or another output, except that y may be x and dx may be dy or residual (with the same row stride). */
+ * an input or another output (rows of one stride may lie between each other's: slices of one wider tensor), except that y may
+ * be x and dx may be dy or residual (with the same row stride). */
 typedef struct {
   int64_t rows;         /* T >= 0 (0: dweight and dbias become 0, nothing else is written) */
   int32_t d;            /* 1 .. MOE_NORM_MAX_D */
@@ -475,7 +476,7 @@ typedef struct {
 } moe_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0, 1), eps >= 0, all finite */
+  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0, 1), eps >= 0 (0: a v of 0 divides by it), all finite */
   int64_t step;                /* t >= 1 */
   const float* grad_scale;     /* (device) factor of every gradient, e.g. a clipping coefficient; NULL = 1 */
   const float* lr_dev;         /* (device) overrides lr, or NULL; with step_dev: for a captured call that is replayed */

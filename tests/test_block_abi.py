@@ -57,6 +57,13 @@ def test_norm_arguments():
     assert L.moe_layer_norm(None, P[0], P[1], P[2], P[3], None, None, None) == B.MOE_EINVAL
 
 
+@pytest.mark.parametrize("at", [-190, -128, -2, 2, 126, 66 + 256, 190 + 256])
+def test_norm_rows_between_rows(at):
+    """x and y in one buffer of rows of 192 elements, 64 of which each takes: refused where two rows meet."""
+    s = norm_shape(rows=16, x_stride=96, y_stride=96)
+    refused(B.lib().moe_layer_norm(ctypes.byref(s), P[0], P[1], P[2], P[0] + at, None, None, None), "overlaps")
+
+
 def test_norm_workspace_grows_with_rows_to_a_limit():
     sizes = [B.moe_layer_norm_workspace_bytes(norm_shape(rows=r, d=7168)) for r in (1, 10, 1000, 10 ** 6, 10 ** 9)]
     assert sizes == sorted(sizes) and sizes[-1] == sizes[-2] <= 64 << 20
@@ -155,6 +162,8 @@ def test_adamw_plans():
     refused(bind([t, adam(**other)], ws=None), "too small")
     refused(bind([t], ws=P[15] + 4), "aligned")
     refused(bind([t], ws=P[0]), "overlaps")
+    refused(bind([adam(n=0), adam()], ws=P[3]), "overlaps")
+    refused(bind([t, adam(**other)], ws=P[7]), "overlaps")
     two = (B.moe_adamw_tensor * 2)(t, adam(**other, n=5000))
     assert B.moe_adamw_workspace_bytes(two) == 256 + 2 * ctypes.sizeof(B.moe_adamw_tensor)
     assert B.moe_adamw_workspace_bytes((B.moe_adamw_tensor * 1)(adam(n=-1))) == -1
@@ -180,3 +189,12 @@ def test_adamw_unbound_plan():
     refused(B.lib().moe_adamw_step(None, ctypes.byref(cfg()), None), "plan")
     refused(B.lib().moe_adamw_step(ctypes.byref(B.moe_adamw_plan(None, 3, 1, 0)), ctypes.byref(cfg()), None), "plan")
     refused(B.lib().moe_adamw_read_states(None, None), "plan")
+
+
+def test_adamw_state_bits():
+    import torch
+
+    from expert_output_overlap_amd.runtime import AdamW
+
+    with pytest.raises(ValueError, match="8 or 32"):
+        AdamW.states(torch.zeros(4), 16)

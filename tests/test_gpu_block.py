@@ -90,6 +90,23 @@ def test_norm_leaves_what_is_not_its_own():
     ref.within(y[:, 17:113], *want["y"], "y")
 
 
+def test_norm_between_its_own_rows():
+    """x, y, dy and dx as slices of one wide tensor."""
+    from expert_output_overlap_amd.runtime import LayerNorm
+
+    rnd = gen(5)
+    op = LayerNorm(33, 96, "bf16", "f32")
+    wide = torch.empty(33, 4 * 96 + 1, device="cuda", dtype=torch.bfloat16).copy_(rnd(33, 4 * 96 + 1))
+    x, y, dy, dx = (wide[:, 96 * i: 96 * (i + 1)] for i in (1, 0, 3, 2))
+    x0, dy0, w, b = x.clone(), dy.clone(), 1 + rnd(96), rnd(96)
+    last = wide[:, -1].clone()
+    op.forward(x, w, b, y=y)
+    op.backward(dy, x, w, dx=dx)
+    want = ref.layer_norm(x0, w, b, 1e-5, dy0)
+    check({"y": y, "dx": dx, "dweight": op.dweight, "dbias": op.dbias}, want, ("y", "dx", "dweight", "dbias"), "slices")
+    assert torch.equal(x, x0) and torch.equal(dy, dy0) and torch.equal(wide[:, -1], last)
+
+
 def test_norm_of_nothing_and_without_parameters():
     from expert_output_overlap_amd.runtime import LayerNorm
 
@@ -413,6 +430,17 @@ def test_adamw_values_that_are_not_finite(bits):
         if bits == 8:
             assert ((b["m"][bad] & 0x7F) == 0x7F).all() and (b["v"][bad] == 255).all()
             assert torch.equal(a["m_scale"], b["m_scale"]) and torch.equal(a["v_scale"], b["v_scale"])
+
+
+def test_adamw_of_tiny_gradients():
+    """No eps, and squares among the subnormals: with m and v from one gradient the update is lr.  v = 0.05 (1e-20)^2 = 5e-42
+    holds two roundings of 2^-150 = 7e-46 at most, a relative 3e-4 of it and 1.5e-4 of its root; 2e-4 with fp32's own."""
+    from expert_output_overlap_amd.runtime import AdamW
+
+    t = {"p": torch.zeros(300, device="cuda"), "g": torch.full((300,), 1e-20, device="cuda")}
+    t.update(AdamW.states(t["p"]))
+    AdamW([t], betas=HYPER["betas"], eps=0.0).step(1, 1e-3)
+    ref.within(t["p"], torch.full((300,), -1e-3, device="cuda", dtype=torch.float64), torch.full((300,), 2e-7, device="cuda", dtype=torch.float64), "tiny")
 
 
 def test_adamw_step_from_the_device():
