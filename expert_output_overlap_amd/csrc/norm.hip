@@ -126,11 +126,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_norm(NormLaunch a) {
   const int t = threadIdx.x % G, d = a.d;
   float w[NV * C], b[NV * C];
   const PT *wp = (const PT*)a.weight, *bp = (const PT*)a.bias;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    params<PT, C>(wp, (j * G + t) * C, d, 1.f, w + j * C);
-    params<PT, C>(bp, (j * G + t) * C, d, 0.f, b + j * C);
-  }
   const int64_t step = (int64_t)gridDim.x * PER;
   int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / G;
   u32x4 next[NV];
@@ -142,7 +137,12 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_norm(NormLaunch a) {
       next[j] = c < d ? K::load(p + c, d - c) : u32x4{0, 0, 0, 0};
     }
   };
-  if (r < a.rows) fetch(r);
+  if (r < a.rows) fetch(r);  // before the parameters: a single row's sums then run while those arrive
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    params<PT, C>(wp, (j * G + t) * C, d, 1.f, w + j * C);
+    params<PT, C>(bp, (j * G + t) * C, d, 0.f, b + j * C);
+  }
   for (; r < a.rows; r += step) {
     u32x4 x[NV];
 #pragma unroll

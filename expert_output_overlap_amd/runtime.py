@@ -178,6 +178,11 @@ def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device, strided=False
         raise ValueError("%s: not contiguous" % name)
 
 
+def _first(t: torch.Tensor, n: int) -> torch.Tensor:
+    """The first n rows (a view costs a microsecond, so none of all of them)."""
+    return t if n == t.shape[0] else t[:n]
+
+
 def _device(device) -> torch.device:
     device = torch.device(device)
     return torch.device(device.type, torch.cuda.current_device()) if device.type == "cuda" and device.index is None else device
@@ -230,18 +235,18 @@ class LayerNorm:
     def _stride(self, t):
         return t.stride(0) if t.shape[0] > 1 else 0
 
-    def _params(self, **params):
-        for name, t in params.items():
-            if t is not None:
-                _need(t, name, (self.d,), self.param_dtype, self.device)
+    def _param(self, t, name):
+        if t is not None:
+            _need(t, name, (self.d,), self.param_dtype, self.device)
 
     @_on_own_device
     def forward(self, x, weight=None, bias=None, y=None, stream=None):
         n = self._rows(x)
-        y = self.y[:n] if y is None else y
+        y = _first(self.y, n) if y is None else y
         _need(x, "x", (n, self.d), self.dtype, self.device, strided=True)
         _need(y, "y", (n, self.d), self.dtype, self.device, strided=True)
-        self._params(weight=weight, bias=bias)
+        self._param(weight, "weight")
+        self._param(bias, "bias")
         s = self.shape
         s.rows, s.x_stride, s.y_stride = n, self._stride(x), self._stride(y)
         B.moe_layer_norm(s, x, weight, bias, y, self.mean, self.rstd, stream)
@@ -254,14 +259,14 @@ class LayerNorm:
         if not self.train:
             raise RuntimeError("made without train=True")
         n = self._rows(x)
-        dx = self.dx[:n] if dx is None else dx
+        dx = _first(self.dx, n) if dx is None else dx
         for name, t in (("x", x), ("dy", dy), ("dx", dx)):
             _need(t, name, (n, self.d), self.dtype, self.device, strided=True)
         if residual is not None:
             _need(residual, "residual", (n, self.d), self.dtype, self.device, strided=True)
             if self._stride(residual) != self._stride(dx):
                 raise ValueError("residual and dx: their rows must lie equally far apart")
-        self._params(weight=weight)
+        self._param(weight, "weight")
         s = self.shape
         s.rows, s.x_stride, s.y_stride, s.dx_stride = n, self._stride(x), self._stride(dy), self._stride(dx)
         B.moe_layer_norm_backward(s, dy, x, weight, self.mean, self.rstd, residual, dx, self.dweight, self.dbias,
@@ -306,7 +311,7 @@ class SharedFFN:
 
     @_on_own_device
     def forward(self, x, w_gate_up, w_down, residual=None, y=None, stream=None):
-        y = self.y[: x.shape[0]] if y is None else y
+        y = _first(self.y, x.shape[0]) if y is None else y
         self._check(x, w_gate_up, w_down, residual=residual, y=y)
         B.moe_shared_ffn(self.shape, x, w_gate_up, w_down, residual, self.h, self.gu, y, self.workspace, stream)
         return y
@@ -317,7 +322,7 @@ class SharedFFN:
         the last forward call."""
         if not self.train:
             raise RuntimeError("made without train=True")
-        dx = self.dx[: x.shape[0]] if dx is None else dx
+        dx = _first(self.dx, x.shape[0]) if dx is None else dx
         self._check(x, w_gate_up, w_down, dy=dy, residual=residual, dx=dx)
         t = {"x": x, "w_gate_up": w_gate_up, "w_down": w_down, "h": self.h, "gu": self.gu, "dy": dy, "residual": residual,
              "dgu_ws": self.dgu, "dx": dx, "dw_gate_up": self.dw_gate_up, "dw_down": self.dw_down}
