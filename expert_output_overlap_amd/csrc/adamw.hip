@@ -2,6 +2,8 @@
 //
 // Bound by HBM: every element's parameter, gradient and states are read once, the parameter, its copy and the states
 // written once (30 bytes per element with an fp32 master, gradient and states and a bf16 copy; 18 with 8-bit states).
+// 138.5 million elements: 774 us (5.37 TB/s) with 32-bit states, 461 (5.41) with 8-bit ones and 138 (6.0) for their values.
+// Through flat instead of global accesses and with every chunk checked against its tensor's end: 849, and 1113 for both.
 // The tensors are cut into chunks of ADAMW_CHUNK elements, one workgroup each; a table in the plan names each chunk's
 // tensor, so a launch of many small tensors has no search and no empty workgroups.  A thread takes four elements side by
 // side (a 16-byte access per fp32 array and wave: 1 KB), ADAMW_CHUNK / 1024 times, every load of all of them issued before

@@ -824,7 +824,7 @@ int gemm_few(const Gemm& p, float* partial, hipStream_t st) {
 // times as fast per product once every CU has one, and the small ones win where they would leave CUs idle: 777 tokens of the
 // skewed workload's widths take 36 us forward in 64 x 128 or deep 128 x 128 tiles, 49 in 128 x 128, 82 in 256 x 256; 2048
 // tokens 53, 62 and 93; 2048 tokens of the DeepSeek-V3-shaped widths 179, and 200 without the 256 x 128 tile; 16384 tokens
-// 1270 in 256 x 256.  Splitting k costs the fp32 sums' way to memory and back and a second launch; 128 tokens of those widths
+// 1213 in 256 x 256.  Splitting k costs the fp32 sums' way to memory and back and a second launch; 128 tokens of those widths
 // take 44 us with splits and 80 without.
 struct Choice {
   int tile, splits;
