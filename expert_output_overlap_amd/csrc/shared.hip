@@ -919,12 +919,18 @@ int grads_bf16(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
 // for either layout of an operand, from which a lane takes 16 bytes for four products at once (which k meet in which
 // product does not matter as long as both operands agree).  The tile is small so that four workgroups share a CU and hide
 // each other's latency.  The products take C's columns as their rows, which leaves a lane four neighbouring columns.
-constexpr int FK = 32, FLD = FK + 4;  // rows 144 bytes apart: the 16 lanes of a read phase hit 64 distinct banks
+constexpr int FK = 32;
 constexpr int FSUM = 256;             // k of a partial sum: one running sum over thousands would lose a few bits
 
 struct F32Stage {
-  float a[2][64][FLD], b[2][64][FLD];
+  float a[2][64 * FK], b[2][64 * FK];
 };
+// k of a row in a stage: its 16-byte chunks permuted by the row, so that eight neighbouring rows' same chunk, a row's eight
+// chunks and every fourth row's same k fall on all banks (rows 144 bytes apart instead, as they are: the gradients' LDS
+// busy 51% instead of 28% of their time, 1751 us instead of 1685)
+__device__ __forceinline__ int f32_at(int row, int k) {
+  return row * FK + (((k >> 2) ^ (row & 7) ^ ((row >> 3) & 7)) << 2 | (k & 3));
+}
 
 template <int EPI, bool ACOL, bool BCOL>
 __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
@@ -939,9 +945,8 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   const int t0 = (int)((int64_t)nkt * s / part.splits), t1 = (int)((int64_t)nkt * (s + 1) / part.splits);
   const float *A = (const float*)p.a, *B = (const float*)p.b;
 
-  // eight elements per thread and operand: by rows, k 8 (tid % 4) .. of row tid / 4; by columns, four neighbouring rows of
-  // k kc and kc + 16, a wave's 8 x 8 lanes over 32 rows (a line) and 8 k, so that its LDS stores hit 32 banks (16 rows by 4 k hit 16: the
-  // backward at 4096 x 2048 x 2048 2124 -> 1938 us).  Outside the matrix: 0
+  // twice four elements per thread and operand: by rows, k 4 (tid % 8) .. of rows tid / 8 and tid / 8 + 32; by columns, four
+  // neighbouring rows of k kc and kc + 16: either way eight lanes take a line.  Outside the matrix: 0
   const int rc = 4 * (lane & 7) + 32 * (wave & 1), kc = (lane >> 3) + 8 * (wave >> 1);
   f32x4_t rega[2][2], regb[2][2];  // of two k-tiles: a load has two k-tiles' time to arrive
   // contiguous elements c .. c + 3 at q, those from limit on 0 (in: whether any are wanted): no branch, so that all of a
@@ -959,31 +964,34 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   };
   // a k-tile that ends before the last k and does not straddle a_seg: whole fours from a lane's fixed places.  Rows past the
   // matrix read its first; columns past it read the next row (the last k is not in such a k-tile); neither is stored
-  const int ca = m0 + rc, cb = n0 + rc, row = tid >> 2;
+  const int ca = m0 + rc, cb = n0 + rc, row = tid >> 3, kr = 4 * (tid & 7);
   const float* pa = ACOL ? A + (int64_t)kc * p.lda + (ca < p.M ? ca : 0)
-                         : A + (int64_t)(m0 + row < p.M ? m0 + row : 0) * p.lda + 8 * (tid & 3);
-  const int rb_row = n0 + (row & (BN - 1));
+                         : A + (int64_t)(m0 + row < p.M ? m0 + row : 0) * p.lda + kr;
+  const float* pa1 = ACOL ? pa + 16 * p.lda : A + (int64_t)(m0 + row + 32 < p.M ? m0 + row + 32 : 0) * p.lda + kr;
+  // row h of B's two: GLU's second lies in the up projection
+  auto brow_of = [&](int h) -> int64_t { return n0 + row + (EPI == EPI_GLU ? 0 : 32 * h); };
+  auto up_of = [&](int h) -> int64_t { return EPI == EPI_GLU && h ? p.up : 0; };
   const float* pb = BCOL ? B + (int64_t)kc * p.ldb + (cb < p.n_in ? cb : 0)
-                         : B + ((rb_row < p.n_in ? rb_row : 0) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb + 8 * (tid & 3);
+                         : B + (brow_of(0) < p.n_in ? brow_of(0) : 0) * p.ldb + kr;
+  const float* pb1 = BCOL ? pb + 16 * p.ldb : B + ((brow_of(1) < p.n_in ? brow_of(1) : 0) + up_of(1)) * p.ldb + kr;
   const bool wide = p.lda >= 4 && p.ldb >= 4;
   auto fetch = [&](int kt, f32x4_t* ra, f32x4_t* rb) {
     const int k0 = kt * FK;
     if (wide && k0 + FK < p.K && (ACOL || k0 >= p.a_seg || k0 + FK <= p.a_seg)) {
-      const float* qa = pa + (ACOL ? (int64_t)k0 * p.lda : k0 + (k0 >= p.a_seg ? p.a_jump : 0));
-      const float* qb = pb + (BCOL ? (int64_t)k0 * p.ldb : k0);
-      ra[0] = load4(qa, 4);
-      ra[1] = load4(qa + (ACOL ? 16 * p.lda : 4), 4);
-      rb[0] = load4(qb, 4);
-      rb[1] = load4(qb + (BCOL ? 16 * p.ldb : 4), 4);
+      const int64_t oa = ACOL ? (int64_t)k0 * p.lda : k0 + (k0 >= p.a_seg ? p.a_jump : 0), ob = BCOL ? (int64_t)k0 * p.ldb : k0;
+      ra[0] = load4(pa + oa, 4);
+      ra[1] = load4(pa1 + oa, 4);
+      rb[0] = load4(pb + ob, 4);
+      rb[1] = load4(pb1 + ob, 4);
       return;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int k = k0 + kc + 16 * h, kr = k0 + 8 * (tid & 3) + 4 * h, last = p.K - 1;
+      const int k = k0 + kc + 16 * h, last = p.K - 1;
       ra[h] = ACOL ? four(A + (int64_t)min(k, last) * p.lda, ca, p.M, 0x7fffffff, 0, k <= last)
-                   : four(A + (int64_t)min(m0 + row, p.M - 1) * p.lda, kr, p.K, p.a_seg, p.a_jump, true);
+                   : four(A + (int64_t)min(m0 + row + 32 * h, p.M - 1) * p.lda, k0 + kr, p.K, p.a_seg, p.a_jump, true);
       rb[h] = BCOL ? four(B + (int64_t)min(k, last) * p.ldb, cb, p.n_in, 0x7fffffff, 0, k <= last)
-                   : four(B + (min(rb_row, p.n_in - 1) + (EPI == EPI_GLU && row >= BN ? (int64_t)p.up : 0)) * p.ldb, kr, p.K, 0x7fffffff, 0, true);
+                   : four(B + (min(brow_of(h), (int64_t)p.n_in - 1) + up_of(h)) * p.ldb, k0 + kr, p.K, 0x7fffffff, 0, true);
     }
   };
   auto keep = [&](int st, const f32x4_t* ra, const f32x4_t* rb) {
@@ -991,12 +999,12 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
     for (int h = 0; h < 2; ++h) {
       if (ACOL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[st][rc + i][kc + 16 * h] = ra[h][i];
-      } else *(f32x4_t*)&sa[st][row][8 * (tid & 3) + 4 * h] = ra[h];
+        for (int i = 0; i < 4; ++i) sa[st][f32_at(rc + i, kc + 16 * h)] = ra[h][i];
+      } else *(f32x4_t*)&sa[st][f32_at(row + 32 * h, kr)] = ra[h];
       if (BCOL) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sb[st][rc + i][kc + 16 * h] = rb[h][i];
-      } else *(f32x4_t*)&sb[st][row][8 * (tid & 3) + 4 * h] = rb[h];
+        for (int i = 0; i < 4; ++i) sb[st][f32_at(rc + i, kc + 16 * h)] = rb[h][i];
+      } else *(f32x4_t*)&sb[st][f32_at(row + 32 * h, kr)] = rb[h];
     }
   };
 
@@ -1017,8 +1025,8 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
       f32x4_t a[2], b[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        a[i] = *(const f32x4_t*)&sa[st][wm * 32 + i * 16 + r][k + 4 * q];
-        b[i] = *(const f32x4_t*)&sb[st][brow[i] + r][k + 4 * q];
+        a[i] = *(const f32x4_t*)&sa[st][f32_at(wm * 32 + i * 16 + r, k + 4 * q)];
+        b[i] = *(const f32x4_t*)&sb[st][f32_at(brow[i] + r, k + 4 * q)];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -1063,8 +1071,8 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   }
 }
 
-// Four workgroups on a CU, at 128 registers and no spill: forward and backward at 4096 x 2048 x 2048 877 + 1751 us (117.5
-// TFLOP/s of the 153 of a large fp32 product); left to the compiler's choice of registers 925 + 1938.
+// Four workgroups on a CU, at 128 registers and no spill: forward and backward at 4096 x 2048 x 2048 877-926 + 1685 us (111-117
+// and 122 TFLOP/s of the 153 of a large fp32 product); left to the compiler's choice of registers 5% and 10% longer.
 template <int EPI, bool BCOL>
 __global__ __launch_bounds__(256, 4) void k_gemm_f32(Part a) {
   __shared__ __align__(16) F32Stage sh;
