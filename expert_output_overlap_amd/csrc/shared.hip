@@ -937,7 +937,7 @@ __device__ __forceinline__ void f32_tile(const Part& part, F32Stage& sh) {
   const Gemm& p = part.p;
   auto& sa = sh.a;
   auto& sb = sh.b;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave & 1, wn = wave >> 1;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave & 1, wn = wave >> 1;
   constexpr int BN = EPI == EPI_GLU ? 32 : 64;
   const int nt = (p.N + BN - 1) / BN, tiles = (p.M + 63) / 64 * nt, nkt = (p.K + FK - 1) / FK;
   const int i0 = blockIdx.x - part.first, s = i0 / tiles, tile = i0 % tiles;
@@ -1087,9 +1087,12 @@ __global__ __launch_bounds__(256, 4) void k_grads_f32(Parts a) {
   else if (mine(a.part[1]) || mine(a.part[2])) f32_tile<EPI_STORE, true, true>(a.part[mine(a.part[1]) ? 1 : 2], sh);
 }
 
-// splits of a product of so many tiles: up to four workgroups for each CU, of 256 k at least
+// splits of a product of so many tiles: up to four workgroups for each CU, of 256 k at least, or up to one for each CU of 128
+// (500 x 500 x 500: 33 + 48 us with 256 only, 31 + 42; more workgroups than CUs of 128 k lose to the sums' way to memory and
+// back: 1000 x 300 x 900 35 us forward, 46)
 int f32_splits(const Gemm& p, int epi, int64_t tiles) {
-  return (int)std::max<int64_t>(1, std::min(std::min(1024 / tiles, PARTIAL / (p.M * partial_cols(p, epi))), std::min<int64_t>(MAX_SPLITS, p.K / 256)));
+  const int64_t s = std::max(std::min<int64_t>(1024 / tiles, p.K / 256), std::min<int64_t>(256 / tiles, p.K / 128));
+  return (int)std::max<int64_t>(1, std::min(std::min<int64_t>(s, MAX_SPLITS), PARTIAL / (p.M * partial_cols(p, epi))));
 }
 
 template <int EPI, bool BCOL>
