@@ -391,8 +391,10 @@ class AdamW:
                 if value.dtype is not dtype or value.numel() != 1 or value.device != self.device:
                     raise ValueError("%s: one %s on %s wanted" % (field, dtype, self.device))
                 setattr(cfg, "grad_scale" if field == "grad_scale" else field + "_dev", value.data_ptr())
-            elif value is not None:
+            elif field != "grad_scale":
                 setattr(cfg, field, value)
+            elif value is not None:  # its field is an address: a number there would be read through
+                raise ValueError("grad_scale: one %s on %s wanted, not %r" % (dtype, self.device, value))
         B.moe_adamw_step(self.plan, cfg, stream)
 
     @_on_own_device

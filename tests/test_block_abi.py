@@ -198,3 +198,16 @@ def test_adamw_state_bits():
 
     with pytest.raises(ValueError, match="8 or 32"):
         AdamW.states(torch.zeros(4), 16)
+
+
+@pytest.mark.parametrize("value", [0, 4, 0.5])
+def test_adamw_grad_scale_is_a_tensor(value):
+    """The factor is read on the device: a number in its place would become an address."""
+    import torch
+
+    from expert_output_overlap_amd.runtime import AdamW
+
+    op = AdamW.__new__(AdamW)
+    op.device, op.betas, op.eps, op.plan = torch.device("cuda", 0), (0.9, 0.95), 1e-8, B.moe_adamw_plan()  # no tensors
+    with pytest.raises(ValueError, match="grad_scale"):
+        AdamW.step.__wrapped__(op, 1, 1e-3, grad_scale=value)
