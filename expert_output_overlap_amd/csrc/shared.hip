@@ -1141,25 +1141,28 @@ struct PackJobs {
   int64_t pieces;
 };
 
+// Workgroups of 256 threads for n elements: the kernels below walk what is past them (a launch holds under 2^32 threads)
+unsigned blocks_for(int64_t n) { return (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 20); }
+
 __global__ __launch_bounds__(256) void k_pack(PackJobs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.pieces) return;
-  int j = 0;
-  while (j + 1 < a.n && i >= a.job[j + 1].first) ++j;
-  const PackJob& b = a.job[j];
-  const int per = b.ld / 8;
-  const int64_t r = (i - b.first) / per;
-  const int c = (int)(i - b.first - r * per) * 8, part = (int)(r / b.padded), at = (int)(r - (int64_t)part * b.padded);
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (at < b.real) {
-    const bf16_t* s = b.src + ((int64_t)part * b.real + at) * b.cols + c;
-    if (c + 8 <= b.cols) __builtin_memcpy(&v, s, 16);
-    else
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.pieces; i += (int64_t)gridDim.x * 256) {
+    int j = 0;
+    while (j + 1 < a.n && i >= a.job[j + 1].first) ++j;
+    const PackJob& b = a.job[j];
+    const int per = b.ld / 8;
+    const int64_t r = (i - b.first) / per;
+    const int c = (int)(i - b.first - r * per) * 8, part = (int)(r / b.padded), at = (int)(r - (int64_t)part * b.padded);
+    u32x4_t v = {0u, 0u, 0u, 0u};
+    if (at < b.real) {
+      const bf16_t* s = b.src + ((int64_t)part * b.real + at) * b.cols + c;
+      if (c + 8 <= b.cols) __builtin_memcpy(&v, s, 16);
+      else
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < b.cols) v[k / 2] |= (uint32_t)s[k] << (16 * (k & 1));
+        for (int k = 0; k < 8; ++k)
+          if (c + k < b.cols) v[k / 2] |= (uint32_t)s[k] << (16 * (k & 1));
+    }
+    *(u32x4_t*)(b.dst + r * b.ld + c) = v;
   }
-  *(u32x4_t*)(b.dst + r * b.ld + c) = v;
 }
 
 __global__ __launch_bounds__(256) void k_clear(bf16_t* p, int64_t n) {
@@ -1260,9 +1263,8 @@ int run_bf16(const SharedLaunch& s, hipStream_t st) {
       to += n[i];
     }
   if (jobs.n) {
-    const int64_t blocks = (jobs.pieces + 255) / 256;
-    if (blocks > 0x7fffffff) return -1;
-    hipLaunchKernelGGL(k_pack, dim3((unsigned)blocks), dim3(256), 0, st, jobs);
+    hipLaunchKernelGGL(k_pack, dim3(blocks_for(jobs.pieces)), dim3(256), 0, st, jobs);
+    if (hipGetLastError() != hipSuccess) return -1;
   }
   float* partial = (float*)to;
   const Block b = block_bf16(s, op[0], op[1], op[2], op[3]);

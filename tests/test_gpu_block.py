@@ -313,6 +313,36 @@ def test_shared_ffn_gradients_against_differences():
         assert abs((grad.double() * v.double()).sum().item() - want) <= 2.0 ** -12 * (terms + abs(want)) , k
 
 
+def test_shared_ffn_of_more_pieces_than_a_launch_has_threads():
+    """x and dy of an odd width whose packed copies are 2^32 pieces of 16 bytes, zeros but for a few rows (x serves as dy too).
+    A sum of 65535 products makes the worst-case bounds as large as the results, so these are held in the norm: at most three
+    roundings to bf16 in a row, each 2^-8 at most and of random sign."""
+    T, d, f = 262144, 65535, 8
+    shape = B.moe_shared_shape(T, d, f, B.MOE_BF16)
+    need = B.moe_shared_ffn_workspace_bytes(shape, True)
+    if torch.cuda.mem_get_info()[0] < need + 2 * (2 * T * d) + (8 << 30):
+        pytest.skip("%d GiB of device memory wanted" % ((need + 4 * T * d >> 30) + 8))
+    _, wgu, wd, _, _ = ffn_case(1, d, f, "bf16", seed=9)
+    rows = torch.tensor([0, 1, T // 2 + 1, T - 1], device="cuda")
+    some = gen(12)(4, d).bfloat16()
+    x, dx = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16), torch.empty(T, d, device="cuda", dtype=torch.bfloat16)
+    x[rows] = some
+    gu, h = torch.zeros(T, 2 * f, device="cuda"), torch.zeros(T, f, device="cuda", dtype=torch.bfloat16)
+    gu[rows] = (some.double() @ wgu.double().T).float()
+    g, u = gu[rows].double().chunk(2, 1)
+    h[rows] = (g * torch.sigmoid(g) * u).bfloat16()
+    dw_gate_up, dw_down = torch.empty_like(wgu), torch.empty_like(wd)
+    workspace = torch.empty(need, device="cuda", dtype=torch.uint8)
+    B.moe_shared_ffn_backward(shape, {"x": x, "w_gate_up": wgu, "w_down": wd, "h": h, "gu": gu, "dy": x,
+                                      "dgu_ws": torch.empty(T, 2 * f, device="cuda", dtype=torch.bfloat16), "dx": dx,
+                                      "dw_gate_up": dw_gate_up, "dw_down": dw_down}, workspace)
+    want = ref.shared_ffn(some, wgu, wd, dy=some)
+    for name, got in (("dx", dx[rows]), ("dw_gate_up", dw_gate_up), ("dw_down", dw_down)):
+        assert (got.double() - want[name][0]).norm() <= 3 * 2.0 ** -8 * want[name][0].norm(), name
+    dx[rows] = 0.0
+    assert not any(part.any() for part in dx.split(T // 16))
+
+
 # ---- AdamW -------------------------------------------------------------------------------------------------------
 
 def adam_tensors(sizes, bits, params, grads, seed=0, values=True):
