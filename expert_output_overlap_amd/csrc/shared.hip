@@ -1166,12 +1166,11 @@ __global__ __launch_bounds__(256) void k_pack(PackJobs a) {
 }
 
 __global__ __launch_bounds__(256) void k_clear(bf16_t* p, int64_t n) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
 }
 
 int clear(void* p, int64_t n, hipStream_t st) {
-  hipLaunchKernelGGL(k_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (bf16_t*)p, n);
+  hipLaunchKernelGGL(k_clear, dim3(blocks_for(n)), dim3(256), 0, st, (bf16_t*)p, n);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -313,6 +313,20 @@ def test_shared_ffn_gradients_against_differences():
         assert abs((grad.double() * v.double()).sum().item() - want) <= 2.0 ** -12 * (terms + abs(want)) , k
 
 
+def test_shared_ffn_of_nothing_with_wide_weights():
+    """2^32 elements of dw_gate_up, one more than a launch has threads: they become 0 all the same."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    d, f = 65536, 32768
+    op = SharedFFN(1, d, f)
+    wgu, wd = (torch.empty_like(t) for t in (op.dw_gate_up, op.dw_down))
+    none = torch.empty(0, d, device="cuda", dtype=torch.bfloat16)
+    op.dw_gate_up.fill_(3.0)
+    op.dw_down.fill_(3.0)
+    op.backward(none, none, wgu, wd)
+    assert not op.dw_gate_up.any() and not op.dw_down.any()
+
+
 def test_shared_ffn_of_more_pieces_than_a_launch_has_threads():
     """x and dy of an odd width whose packed copies are 2^32 pieces of 16 bytes, zeros but for a few rows (x serves as dy too).
     A sum of 65535 products makes the worst-case bounds as large as the results, so these are held in the norm: at most three
