@@ -121,6 +121,9 @@ struct Part {
   float* partial;     // splits > 1: [splits][M][ld] sums
   int64_t ld;
 };
+// fp32: k of a partial sum at most, in the tiles and with few tokens: one running sum over thousands would lose a few bits
+constexpr int FSUM = 256;
+
 // ---- few tokens --------------------------------------------------------------------------------------------------------
 // The weights stream past once and bound the time.  A workgroup takes RT x 16 rows of the weights (GLU with RT = 1: 8 of the
 // gate's and the same 8 of the up projection's) as one operand of 16x16 products whose other is the tokens, 16 per product;
@@ -145,6 +148,35 @@ struct Chunk32 {  // 32 bytes of a row: 16 bf16 or 8 fp32
         if (sizeof(T) == 4) v[i / 4][i % 4] = *(const uint32_t*)(p + i);
         else v[i / 8][i / 2 % 4] |= (uint32_t) * (const uint16_t*)(p + i) << (16 * (i & 1));
       }
+  }
+};
+// A wave's sums; fp32: fold() ends a partial sum and adds it to the whole
+template <typename T, int RT, int MT>
+struct FewSums {
+  f32x4_t acc[RT][MT], total[sizeof(T) == 4 ? RT : 1][sizeof(T) == 4 ? MT : 1];
+  __device__ __forceinline__ FewSums() {
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if constexpr (sizeof(T) == 4) total[t][m] = acc[t][m];
+      }
+  }
+  __device__ __forceinline__ void fold() {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          total[t][m] += acc[t][m];
+          acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        }
+    }
+  }
+  __device__ __forceinline__ f32x4_t of(int t, int m) const {
+    if constexpr (sizeof(T) == 4) return total[t][m] + acc[t][m];
+    else return acc[t][m];
   }
 };
 template <typename T>
@@ -214,11 +246,7 @@ __global__ __launch_bounds__(512) void k_gemm_few(Part a) {
   }
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = (const T*)p.a + (int64_t)(16 * t + r < p.M ? 16 * t + r : 0) * p.lda + q * (32 / sizeof(T));
-  f32x4_t acc[RT][MT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  FewSums<T, RT, MT> sums;
   // this split's chunks that are full, [begin, whole)
   const int all = p.K / CH, begin = (int)((int64_t)all * blockIdx.y / a.splits), whole = (int)((int64_t)all * (blockIdx.y + 1) / a.splits);
   auto chunks = [&](int c, auto count, bool cut) {  // chunks c, c + NW, ..
@@ -238,7 +266,9 @@ __global__ __launch_bounds__(512) void k_gemm_few(Part a) {
 #pragma unroll
       for (int t = 0; t < RT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[t][m] = products(cw[u][t], cx[u][m], acc[t][m]);
+        for (int m = 0; m < MT; ++m) sums.acc[t][m] = products(cw[u][t], cx[u][m], sums.acc[t][m]);
+    static_assert(SU * CH <= FSUM, "fp32 sums end with the call");
+    sums.fold();
   };
   int c = begin + wave;
   for (; c + (SU - 1) * NW < whole; c += SU * NW) chunks(c, std::integral_constant<int, SU>{}, false);
@@ -251,7 +281,7 @@ __global__ __launch_bounds__(512) void k_gemm_few(Part a) {
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
+    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = sums.of(t, m);
   __syncthreads();
   few_finish<T, EPI, RT, MT>(a, n0, tid, part);
 }
@@ -303,24 +333,20 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Part a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) dma16((t < RT ? wbase : xbase) + at, off[t][i], slot + t * 2048 + i * 1024);
   };
-  f32x4_t acc[RT][MT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[t][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  FewSums<T, RT, MT> sums;
   auto multiply = [&](const u32x4_t (&f)[RT + MT]) {
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        f32x4_t& c = sums.acc[t][m];
         if constexpr (ES == 2) {
-          acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[t]),
-                                                              __builtin_bit_cast(bf16x8_t, f[RT + m]), acc[t][m], 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[t]), __builtin_bit_cast(bf16x8_t, f[RT + m]), c,
+                                                      0, 0, 0);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[t][m] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[t][i]), __uint_as_float(f[RT + m][i]), acc[t][m],
-                                                             0, 0, 0);
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[t][i]), __uint_as_float(f[RT + m][i]), c, 0, 0, 0);
         }
       }
   };
@@ -338,6 +364,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Part a) {
     }
     multiply(f[0]);
     multiply(f[1]);
+    if (j % (FSUM / CK) == FSUM / CK - 1) sums.fold();
   };
 #pragma unroll
   for (int j = 0; j < D; ++j)
@@ -367,7 +394,7 @@ __global__ __launch_bounds__(512) void k_gemm_ring(Part a) {
 #pragma unroll
   for (int t = 0; t < RT; ++t)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = acc[t][m];
+    for (int m = 0; m < MT; ++m) part[wave][t * MT + m][lane] = sums.of(t, m);
   __syncthreads();
   few_finish<T, EPI, RT, MT>(a, n0, tid, part);
 }
@@ -920,7 +947,6 @@ int grads_bf16(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
 // product does not matter as long as both operands agree).  The tile is small so that four workgroups share a CU and hide
 // each other's latency.  The products take C's columns as their rows, which leaves a lane four neighbouring columns.
 constexpr int FK = 32;
-constexpr int FSUM = 256;             // k of a partial sum: one running sum over thousands would lose a few bits
 
 struct F32Stage {
   float a[2][64 * FK], b[2][64 * FK];

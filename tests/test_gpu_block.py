@@ -357,6 +357,33 @@ def test_shared_ffn_of_more_pieces_than_a_launch_has_threads():
     assert not any(part.any() for part in dx.split(T // 16))
 
 
+@pytest.mark.parametrize("T", [1, 20])
+@pytest.mark.parametrize("d,f", [(2080, 65536), (2080, 65535), (65536, 2080), (65535, 2080)])
+def test_shared_ffn_few_tokens_sum_in_two_levels(T, d, f):
+    """f32: sums of up to 8192 products in a wave, the first of them 1 and the others 2^-27.  A running sum loses the others (four
+    products at a time reach 2^-25, half of what it can hold): 2^-14 of the result.  Sums of 256 at a time that are added up
+    then round 256 + 32 times in a wave, then over eight waves: at most 304 x 2^-24 of the result, 2^-15.7, and silu's 2^-20."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    k = torch.arange(max(d, f), device="cuda")
+    terms = torch.where((k < 256) & (k % 32 == 0), 1.0, 2.0 ** -27)  # the first of each wave's
+    silu = torch.sigmoid(torch.tensor(1.0, dtype=torch.float64)).item()
+    wgu, wd = torch.zeros(2 * f, d, device="cuda"), torch.zeros(d, f, device="cuda")
+    if f > d:  # h = silu(1) terms, y its sum
+        x = torch.zeros(T, d, device="cuda")
+        x[:, 0] = 1.0
+        wgu[:f, 0], wgu[f:, 0] = 1.0, terms
+        wd.fill_(1.0)
+    else:  # u the terms' sum, y = h
+        x = torch.ones(T, d, device="cuda")
+        wgu[:f, 0] = 1.0
+        wgu[f:] = terms[:d]
+        wd[k[:d], k[:d] % f] = 1.0
+    want = torch.full((T, d), silu * terms[:max(d, f)].double().sum().item(), dtype=torch.float64, device="cuda")
+    y = SharedFFN(T, d, f, "f32", train=False).forward(x, wgu, wd)
+    ref.within(y, want, (304 * ref.E32 + 2.0 ** -20) * want, (T, d, f))
+
+
 # ---- AdamW -------------------------------------------------------------------------------------------------------
 
 def adam_tensors(sizes, bits, params, grads, seed=0, values=True):
