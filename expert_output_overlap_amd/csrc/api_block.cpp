@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <exception>
 #include <vector>
@@ -348,20 +349,22 @@ int moe_adamw_bind(const moe_adamw_tensor* t, int32_t n_tensors, void* workspace
 int moe_adamw_step(const moe_adamw_plan* plan, const moe_adamw_cfg* cfg, void* stream) {
   if (const char* e = check_plan(plan)) return moe_fail(MOE_EINVAL, e);
   if (!cfg) return moe_fail(MOE_EINVAL, "null cfg");
-  if (!std::isfinite(cfg->lr) || cfg->lr < 0 || !std::isfinite(cfg->eps) || cfg->eps < 0)
-    return moe_fail(MOE_EINVAL, "lr and eps must be finite and not negative");
+  // the kernel's reciprocal of a divisor below 2^-126 is not finite, and makes NaN of an update of 0
+  const float lr = (float)cfg->lr, eps = (float)cfg->eps;
+  if (!(lr >= 0) || !std::isfinite(lr) || !(cfg->eps == 0 || eps >= FLT_MIN) || !std::isfinite(eps))
+    return moe_fail(MOE_EINVAL, "lr and eps must be finite in fp32 and not negative, eps 0 or at least 2^-126");
   if (!(cfg->beta1 >= 0 && cfg->beta1 < 1) || !(cfg->beta2 >= 0 && cfg->beta2 < 1))
     return moe_fail(MOE_EINVAL, "betas must be in [0, 1)");
   if (cfg->step < 1 && !cfg->step_dev) return moe_fail(MOE_EINVAL, "step must be >= 1");
   if (off(cfg->grad_scale, 4) || off(cfg->lr_dev, 4) || off(cfg->step_dev, 8))
     return moe_fail(MOE_EINVAL, "a device number must be aligned to its size");
   AdamwStep a = adamw_of(plan);
-  a.lr = (float)cfg->lr;
+  a.lr = lr;
   a.beta1 = (float)cfg->beta1;
   a.beta2 = (float)cfg->beta2;
   a.one1 = (float)(1.0 - cfg->beta1);
   a.one2 = (float)(1.0 - cfg->beta2);
-  a.eps = (float)cfg->eps;
+  a.eps = eps;
   a.log_beta1 = std::log(cfg->beta1);
   a.log_beta2 = std::log(cfg->beta2);
   const double t = (double)std::max<int64_t>(cfg->step, 1);

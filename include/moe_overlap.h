@@ -476,7 +476,7 @@ typedef struct {
 } moe_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0, 1), eps >= 0 (0: a v of 0 divides by it), all finite */
+  double lr, beta1, beta2, eps; /* lr >= 0, betas in [0, 1), eps 0 (a v of 0 divides by it) or >= 2^-126, all finite in fp32 */
   int64_t step;                /* t >= 1 */
   const float* grad_scale;     /* (device) factor of every gradient, e.g. a clipping coefficient; NULL = 1 */
   const float* lr_dev;         /* (device) overrides lr, or NULL; with step_dev: for a captured call that is replayed */

@@ -211,3 +211,15 @@ def test_adamw_grad_scale_is_a_tensor(value):
     op.device, op.betas, op.eps, op.plan = torch.device("cuda", 0), (0.9, 0.95), 1e-8, B.moe_adamw_plan()  # no tensors
     with pytest.raises(ValueError, match="grad_scale"):
         AdamW.step.__wrapped__(op, 1, 1e-3, grad_scale=value)
+
+
+@pytest.mark.parametrize("kw", [dict(eps=1e-39), dict(eps=1e-46), dict(eps=2.0 ** -126 * 0.999), dict(eps=1e39), dict(lr=1e39)])
+def test_adamw_numbers_that_single_precision_does_not_hold(kw):
+    """eps below 2^-126 would be a divisor whose reciprocal is not finite: 0 times it, of an element without gradients, is NaN."""
+    refused(B.lib().moe_adamw_step(ctypes.byref(B.moe_adamw_plan()), ctypes.byref(cfg(**kw)), None), "lr and eps")
+
+
+def test_adamw_smallest_eps():
+    plan = B.moe_adamw_plan()  # no tensors: nothing is launched
+    for eps in (0.0, 2.0 ** -126):
+        assert B.lib().moe_adamw_step(ctypes.byref(plan), ctypes.byref(cfg(eps=eps)), None) == B.MOE_OK
