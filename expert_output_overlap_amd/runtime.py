@@ -375,7 +375,7 @@ class AdamW:
             raise ValueError("states in 8 or 32 bits, not %r" % (bits,))
         n, z = p.numel(), dict(device=p.device)
         if bits == 32:
-            return {k: torch.zeros(n, **z) for k in ("m", "v")}
+            return {k: torch.zeros(n, dtype=torch.float32, **z) for k in ("m", "v")}
         blocks = -(-n // B.MOE_ADAMW_BLOCK)
         return {k: torch.zeros(k.endswith("scale") and blocks or n, dtype=torch.uint8, **z)
                 for k in ("m", "v", "m_scale", "v_scale")}

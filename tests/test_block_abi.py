@@ -223,3 +223,17 @@ def test_adamw_smallest_eps():
     plan = B.moe_adamw_plan()  # no tensors: nothing is launched
     for eps in (0.0, 2.0 ** -126):
         assert B.lib().moe_adamw_step(ctypes.byref(plan), ctypes.byref(cfg(eps=eps)), None) == B.MOE_OK
+
+
+def test_adamw_states_are_single_precision_whatever_the_default():
+    import torch
+
+    from expert_output_overlap_amd.runtime import AdamW
+
+    was = torch.get_default_dtype()
+    try:
+        for dtype in (torch.bfloat16, torch.float64):
+            torch.set_default_dtype(dtype)
+            assert {t.dtype for t in AdamW.states(torch.zeros(40, dtype=torch.bfloat16)).values()} == {torch.float32}
+    finally:
+        torch.set_default_dtype(was)
