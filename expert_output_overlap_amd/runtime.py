@@ -414,11 +414,14 @@ class MoeBlock:
         self.path, self.train = path, train
         self.norm_op = LayerNorm(path.T, path.d, path.dtype, "f32", eps, train, path.device)
         self.shared = SharedFFN(path.T, path.d, shared_f, path.dtype, train, path.device)
+        self.device = self.norm_op.device
 
+    @_on_own_device
     def norm(self, x, w, stream=None):
         self.n = self.norm_op.forward(x, w["norm_weight"], w["norm_bias"], stream=stream)
         return self.n
 
+    @_on_own_device
     def experts(self, logits, w, stream=None):
         p, out = self.path, self.path.out[: self.path.T]
         p.route(logits, stream)
@@ -427,6 +430,7 @@ class MoeBlock:
         p.combine(stream=stream)
         return self.shared.forward(self.n, w["shared_gate_up"], w["shared_down"], residual=out, y=out, stream=stream)
 
+    @_on_own_device
     def experts_backward(self, d_out, w, stream=None):
         p = self.path
         p.backward(d_out, w["w_gate_up"], w["w_down"], gu=p.gu_buffer(), stream=stream)
@@ -434,6 +438,7 @@ class MoeBlock:
         dn = p.bwd_buffers()["dx"][: p.T]
         return self.shared.backward(d_out, self.n, w["shared_gate_up"], w["shared_down"], residual=dn, dx=dn, stream=stream)
 
+    @_on_own_device
     def norm_backward(self, dn, x, w, residual=None, stream=None):
         """dx; residual: the gradient that reaches x past the block."""
         return self.norm_op.backward(dn, x, w["norm_weight"], residual=residual, stream=stream)

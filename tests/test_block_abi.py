@@ -237,3 +237,41 @@ def test_adamw_states_are_single_precision_whatever_the_default():
             assert {t.dtype for t in AdamW.states(torch.zeros(40, dtype=torch.bfloat16)).values()} == {torch.float32}
     finally:
         torch.set_default_dtype(was)
+
+
+def test_block_works_on_its_paths_device(monkeypatch):
+    """Every call of a block runs with its path's device as the current one, the path's own calls among them: they take the
+    current device's stream."""
+    import contextlib
+
+    import torch
+
+    from expert_output_overlap_amd.runtime import MoeBlock
+
+    current, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d.index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+
+    class Op:  # notes the device that is current at each of its calls
+        T, out, n = 2, torch.zeros(2, 3), None
+
+        def __getattr__(self, name):
+            return lambda *a, **kw: seen.append((name, current[0])) or {"dx": torch.zeros(2, 3)}
+
+    block = MoeBlock.__new__(MoeBlock)
+    block.path = block.norm_op = block.shared = Op()
+    block.device, block.train = torch.device("cuda", 1), True
+    w = dict.fromkeys(("norm_weight", "norm_bias", "w_gate_up", "w_down", "shared_gate_up", "shared_down"))
+    block.norm(None, w)
+    block.experts(None, w)
+    block.experts_backward(None, w)
+    block.norm_backward(None, None, w)
+    assert {d for _, d in seen} == {1} and {"route", "layout", "ffn", "combine", "backward", "combine_backward"} <= {n for n, _ in seen}
+    assert current == [0]
