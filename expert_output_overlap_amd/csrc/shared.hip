@@ -1307,9 +1307,10 @@ int64_t shared_workspace_bytes(int64_t tokens, int d, int f, int dtype, bool bac
   if (tokens == 0) return 0;
   int64_t n[4] = {0, 0, 0, 0};
   if (dtype == MOE_BF16) pack_sizes(tokens, d, f, backward, n);
-  // the k-splits' sums: at most PARTIAL floats, and MAX_SPLITS times the largest product
-  const int64_t out = backward ? std::max(std::max(tokens * up8(d), tokens * up8(f)), 2 * up8(f) * up8(d))
-                               : std::max(tokens * up8(d), tokens * 2 * up8(f));
+  // the k-splits' sums: at most PARTIAL floats, and MAX_SPLITS times a launch's products (the three gradients are one launch,
+  // their sums one after another)
+  const int64_t D = up8(d), F = up8(f);
+  const int64_t out = backward ? std::max(tokens * F, tokens * D + 2 * F * D + D * F) : std::max(tokens * D, tokens * 2 * F);
   return 2 * (n[0] + n[1] + n[2] + n[3]) + 4 * std::min<int64_t>(PARTIAL, MAX_SPLITS * out);
 }
 

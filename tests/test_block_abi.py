@@ -275,3 +275,12 @@ def test_block_works_on_its_paths_device(monkeypatch):
     block.norm_backward(None, None, w)
     assert {d for _, d in seen} == {1} and {"route", "layout", "ffn", "combine", "backward", "combine_backward"} <= {n for n, _ in seen}
     assert current == [0]
+
+
+@pytest.mark.parametrize("T,d,f,dtype", [(40, 64, 72, B.MOE_F32), (100, 40, 48, B.MOE_BF16), (33, 100, 36, B.MOE_BF16), (1, 1, 1, B.MOE_F32),
+                                         (7, 300, 8, B.MOE_F32), (4096, 7168, 2048, B.MOE_BF16)])
+def test_shared_backward_workspace_holds_every_sum(T, d, f, dtype):
+    """Sixteen k-splits of all three gradients at once (they lie one after another) and of dH, up to 2^23 sums."""
+    d8, f8 = -(-d // 8) * 8, -(-f // 8) * 8
+    sums = 16 * max(T * f8, T * d8 + 2 * f8 * d8 + d8 * f8)
+    assert B.moe_shared_ffn_workspace_bytes(shared_shape(tokens=T, d=d, f=f, dtype=dtype), True) >= 4 * min(1 << 23, sums)
