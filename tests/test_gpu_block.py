@@ -313,6 +313,54 @@ def test_shared_ffn_gradients_against_differences():
         assert abs((grad.double() * v.double()).sum().item() - want) <= 2.0 ** -12 * (terms + abs(want)) , k
 
 
+# Sizes that take every tile of the bf16 products, whole and in k-splits, with rows, columns and k that no tile divides; widths
+# of whole eights (operands as they are) and others (packed).  tests/test_block_tiles.py holds them to that.
+TILE_SIZES = [(13165, 34, 528), (16633, 40, 136), (8503, 199, 144), (3061, 2021, 32), (35, 707, 39), (11205, 1834, 37),
+              (17029, 391, 34), (17273, 136, 41), (8203, 136, 212), (3327, 40, 1800), (35, 37, 738), (16655, 132, 148),
+              (5521, 129, 2480), (65, 3739, 5512), (259, 2506, 777), (139, 3512, 2937), (443, 7425, 218), (129, 2576, 1144),
+              (39, 6559, 133), (35, 797, 1256), (39, 32, 368), (1055, 64, 3816), (665, 5136, 392), (14219, 72, 600),
+              (2049, 2056, 1416), (4920, 3304, 8), (10834, 12, 1889), (16487, 4398, 71), (137, 11126, 6352), (130, 6147, 11321)]
+
+
+@pytest.mark.parametrize("T,d,f", TILE_SIZES)
+def test_shared_ffn_tiles(T, d, f):
+    """Every tile against the formulas: outputs and workspace inside larger buffers and full of NaN before the calls, y and dx over
+    their residuals; the same bits at a second call."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, res, dy = ffn_case(T, d, f, "bf16", seed=13)
+    op, wide = SharedFFN(T, d, f), []
+
+    def inside(t, fill=float("nan")):
+        at = torch.full((t.numel() + 8192,), 7, dtype=t.dtype, device="cuda")
+        at[4096: 4096 + t.numel()] = fill
+        wide.append((at, 4096, t.numel()))
+        return at[4096: 4096 + t.numel()].view(t.shape)
+
+    op.dw_gate_up, op.dw_down, op.h, op.gu, op.dgu = (inside(t) for t in (op.dw_gate_up, op.dw_down, op.h, op.gu, op.dgu))
+    y, dx = inside(op.y), inside(op.dx)
+    op.workspace = inside(op.workspace, 255)
+    wante, want, first = ref.shared_ffn(x, wgu, wd, residual=res), ref.shared_ffn(x, wgu, wd, residual=res, dy=dy), None
+    for _ in range(2):
+        y.copy_(res)
+        dx.copy_(res)
+        op.forward(x, wgu, wd, residual=y, y=y)
+        op.backward(dy, x, wgu, wd, residual=dx, dx=dx)
+        got = {"dx": dx, "dw_gate_up": op.dw_gate_up, "dw_down": op.dw_down, "y": y}
+        if first is None:
+            check(got, {**want, "y": wante["y"]}, got, (T, d, f))
+            for name, v in got.items():  # sums of thousands: the worst case's bound is wide, the norm's is not (4 roundings in a row)
+                exact = wante["y"][0] if name == "y" else want[name][0]
+                assert (v.double() - exact).norm() <= 4 * 2.0 ** -8 * exact.norm(), (name, T, d, f)
+            first = {k: v.clone() for k, v in got.items()}
+        assert all(torch.equal(first[k], got[k]) for k in first)
+    for at, a, n in wide:
+        assert (at[:a] == 7).all() and (at[a + n:] == 7).all()
+    for t in (op.h, op.gu[:, : op.gu.shape[1] // 2], op.gu[:, op.gu.shape[1] // 2:], op.dgu[:, : op.dgu.shape[1] // 2],
+              op.dgu[:, op.dgu.shape[1] // 2:]):
+        assert (t[:, f:] == 0).all()
+
+
 def test_shared_ffn_of_nothing_with_wide_weights():
     """2^32 elements of dw_gate_up, one more than a launch has threads: they become 0 all the same."""
     from expert_output_overlap_amd.runtime import SharedFFN
