@@ -57,6 +57,18 @@ def test_norm(rows, d, dtype, params):
     check(got, want, ("y", "dx", "dweight", "dbias"), (rows, d, dtype, params))
 
 
+@pytest.mark.parametrize("rows,d", [(1100, 16384), (1031, 8200), (1500, 12001)])
+@pytest.mark.parametrize("dtype,params", [("bf16", "f32"), ("f32", "f32")])
+def test_norm_of_many_wide_rows(rows, d, dtype, params):
+    """Rows of more than 8192 elements, several for each group of threads, and again into the same buffers."""
+    op, (x, w, b, dy, res), got, want = norm_case(rows, d, dtype, params, pad=1, seed=3)
+    check(got, want, ("y", "dx", "dweight", "dbias"), (rows, d, dtype, params))
+    first = {k: v.clone() for k, v in got.items()}
+    op.forward(x, w, b)
+    op.backward(dy, x, w, residual=res)
+    assert all(torch.equal(first[k], got[k]) for k in first)
+
+
 def test_norm_is_the_same_each_time_and_in_place():
     op, (x, w, b, dy, res), got, _ = norm_case(1500, 1536, "bf16", "f32", residual=True)
     first = {k: v.clone() for k, v in got.items()}
@@ -288,6 +300,26 @@ def test_shared_ffn_bad_tokens_stay_in_their_rows(T, dtype):
         z = op.forward(x, wgu, wd, residual=res)
         keep = torch.arange(T, device="cuda") != T // 2
         assert torch.equal(z[keep], y[keep]) and torch.isnan(z[T // 2]).all()
+
+
+@pytest.mark.parametrize("T,d,f", [(5, 100, 36), (40, 64, 41), (70, 100, 36), (300, 65, 9), (300, 72, 41), (40, 128, 1001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_shared_ffn_padding_of_bad_tokens(T, d, f, dtype, bad):
+    """h, g | u and dg | du past f are 0 in every row, that of a token that is not finite too."""
+    from expert_output_overlap_amd.runtime import SharedFFN
+
+    x, wgu, wd, _, dy = ffn_case(T, d, f, dtype, seed=14)
+    x[T // 2, d // 3] = dy[T // 3, d // 2] = bad
+    op = SharedFFN(T, d, f, dtype)
+    for t in (op.h, op.gu, op.dgu):
+        t.fill_(7.0)
+    op.forward(x, wgu, wd)
+    op.backward(dy, x, wgu, wd)
+    F = op.h.shape[1]
+    for t in (op.h, op.gu[:, :F], op.gu[:, F:], op.dgu[:, :F], op.dgu[:, F:]):
+        assert (t[:, f:] == 0).all()
+    assert not torch.isfinite(op.h[T // 2, :f]).all() and not torch.isfinite(op.dgu[T // 3, :f]).all()
 
 
 def test_shared_ffn_gradients_against_differences():
