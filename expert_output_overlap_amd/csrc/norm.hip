@@ -1,7 +1,8 @@
 // Layer norm, forward and backward (formulas in include/moe_overlap.h).
 //
 // Both are bound by HBM: forward 2, backward 3 (4 with a residual) row transfers per row.  A row is held in registers
-// by a group of G threads, NV 16-byte chunks each, so it is read once and its variance is the mean of squared
+// by a group of G threads, NV 16-byte chunks each (of the backward's rows of more than 8192 elements some in scratch: plan()),
+// so it is read once and its variance is the mean of squared
 // differences to the mean (no difference of large sums).  Groups walk the rows with a stride; the next row's loads go out
 // before the current row's sums, which hides their latency behind the reductions, and the parameters stay in registers
 // for all of a group's rows (as fp32 they are four times the bytes of a bf16 row: re-reading them through the L2 for every
@@ -360,6 +361,8 @@ void pick(const NormLaunch& a, int G, int NV, int64_t groups, hipStream_t st) {
 // element besides the row: 16384 bf16 rows of 7168 take 263 us by 256 threads of four chunks, 221 by 512 of two and 194 (4.85
 // TB/s) by 1024 of one.  In the forward the fewer waves of a smaller group's sums are worth more: 103 us (4.6 TB/s) by 256
 // threads of four, 110 by 512 of two, 160 by 1024 of one.
+// More than 8192 elements in the backward: four chunks (bf16) or eight (fp32) in each of 512 threads, of whose values the compiler
+// keeps 43-45 or 176-179 registers' worth in scratch; 8192 rows of 16384 take 385 us (2.1 TB/s) and 968 (1.7), of 8192 119 and 156.
 void plan(int d, int dtype, bool backward, int* G, int* NV) {
   const int chunks = (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16;
   *G = chunks <= 128 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? (backward ? 1024 : 256) : 512;
@@ -367,8 +370,9 @@ void plan(int d, int dtype, bool backward, int* G, int* NV) {
   *NV = per <= 2 ? per : per <= 4 ? 4 : 8;
 }
 
-// Groups of a launch on 256 CUs: about as many as their registers leave room for at once, so that a group's parameters are
-// read once for many rows and its sums written once.
+// Groups of a launch on 256 CUs: few, so that a group's parameters are read once for many rows and its sums written once, but
+// enough to keep every CU in waves to the end.  In the backward that is up to twice what registers leave room for at once (104 of them
+// for a 7168-wide bf16 row: one group of 1024 threads on a CU), in the forward with four chunks too.
 int64_t norm_groups(int64_t rows, int G, int NV, bool backward) {
   const int waves = backward ? (NV == 1 ? 32 : NV == 2 ? 16 : 8) : (NV <= 2 ? 64 : 24);  // of a CU
   const int64_t most = 256ll * waves * 64 / G;

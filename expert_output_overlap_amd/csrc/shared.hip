@@ -1075,7 +1075,7 @@ int grads_f32(const Gemm* const (&p)[3], float* partial, hipStream_t st) {
 
 // bf16 operands whose rows do not start at 16 bytes, copied to rows that do: one launch for all of a call's.  Row r of a
 // copy, in parts of `padded` rows, is row (r / padded) * real + r % padded of the operand, or 0 where r % padded >= real;
-// columns past the operand's are 0.
+// columns past the operand's are 0.  777 tokens of 2046 x 1406 forward: 13.6 of 45 us; 2048 in training 14.1 + 17.6 of 172.
 struct PackJob {
   const bf16_t* src;
   bf16_t* dst;
