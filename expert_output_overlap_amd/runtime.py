@@ -407,8 +407,8 @@ class MoeBlock:
     """A pre-norm MoE block of one rank: n = norm(x); out = combine(routed experts(n)) + shared expert(n), and its backward.
     The router's product is the caller's: ``norm`` gives the rows its logits come from, ``experts`` takes the logits;
     ``experts_backward`` gives the gradient of n (and path.bwd_buffers()["dw_route"] that of the routing weights), to which
-    the caller adds the router's part before ``norm_backward``.  w: norm_weight, norm_bias, w_gate_up, w_down (the routed
-    experts' [E_l, ...]), shared_gate_up, shared_down."""
+    the caller adds the router's part before ``norm_backward``.  Every call takes all of the path's T rows; logits are fp32
+    [T, G].  w: norm_weight, norm_bias, w_gate_up, w_down (the routed experts' [E_l, ...]), shared_gate_up, shared_down."""
 
     def __init__(self, path: MoePath, shared_f: int, eps=1e-5, train=True):
         self.path, self.train = path, train
@@ -416,14 +416,23 @@ class MoeBlock:
         self.shared = SharedFFN(path.T, path.d, shared_f, path.dtype, train, path.device)
         self.device = self.norm_op.device
 
+    def _experts_weights(self, w):
+        """The routed path takes addresses: what it reads has to be there."""
+        p = self.path
+        _need(w["w_gate_up"], "w_gate_up", (p.E_l, 2 * p.f, p.d), p.tdtype, self.device)
+        _need(w["w_down"], "w_down", (p.E_l, p.d, p.f), p.tdtype, self.device)
+
     @_on_own_device
     def norm(self, x, w, stream=None):
+        _need(x, "x", (self.path.T, self.path.d), self.path.tdtype, self.device, strided=True)
         self.n = self.norm_op.forward(x, w["norm_weight"], w["norm_bias"], stream=stream)
         return self.n
 
     @_on_own_device
     def experts(self, logits, w, stream=None):
         p, out = self.path, self.path.out[: self.path.T]
+        _need(logits, "logits", (p.T, p.G), torch.float32, self.device)
+        self._experts_weights(w)
         p.route(logits, stream)
         p.layout(self.n, stream=stream)
         p.ffn(w["w_gate_up"], w["w_down"], gu_out=p.gu_buffer() if self.train else None, stream=stream)
@@ -432,7 +441,11 @@ class MoeBlock:
 
     @_on_own_device
     def experts_backward(self, d_out, w, stream=None):
+        if not self.train:
+            raise RuntimeError("made without train=True")
         p = self.path
+        _need(d_out, "d_out", (p.T, p.d), p.tdtype, self.device)
+        self._experts_weights(w)
         p.backward(d_out, w["w_gate_up"], w["w_down"], gu=p.gu_buffer(), stream=stream)
         p.combine_backward(d_out, stream=stream)
         dn = p.bwd_buffers()["dx"][: p.T]

@@ -246,6 +246,7 @@ def test_block_works_on_its_paths_device(monkeypatch):
 
     import torch
 
+    from expert_output_overlap_amd import runtime
     from expert_output_overlap_amd.runtime import MoeBlock
 
     current, seen = [0], []
@@ -258,9 +259,10 @@ def test_block_works_on_its_paths_device(monkeypatch):
 
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
     monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(runtime, "_need", lambda *a, **kw: None)  # no tensors here
 
     class Op:  # notes the device that is current at each of its calls
-        T, out, n = 2, torch.zeros(2, 3), None
+        T, G, E_l, d, f, tdtype, out, n = 2, 4, 4, 3, 5, torch.float32, torch.zeros(2, 3), None
 
         def __getattr__(self, name):
             return lambda *a, **kw: seen.append((name, current[0])) or {"dx": torch.zeros(2, 3)}
@@ -284,3 +286,45 @@ def test_shared_backward_workspace_holds_every_sum(T, d, f, dtype):
     d8, f8 = -(-d // 8) * 8, -(-f // 8) * 8
     sums = 16 * max(T * f8, T * d8 + 2 * f8 * d8 + d8 * f8)
     assert B.moe_shared_ffn_workspace_bytes(shared_shape(tokens=T, d=d, f=f, dtype=dtype), True) >= 4 * min(1 << 23, sums)
+
+
+def test_block_checks_before_it_launches():
+    """A batch of fewer rows than the path's, or other tensors than the path's shape: refused before the routed path, whose calls go by
+    addresses alone, reads past them."""
+    import torch
+
+    from expert_output_overlap_amd.runtime import MoeBlock
+
+    T, G, E, d, f = 6, 4, 2, 8, 16
+
+    class Op:
+        def __getattr__(self, name):
+            raise AssertionError("called " + name)
+
+    class Path(Op):
+        pass
+
+    p = Path()
+    p.T, p.G, p.E_l, p.d, p.f, p.tdtype, p.out = T, G, E, d, f, torch.bfloat16, torch.zeros(T, d)
+    block = MoeBlock.__new__(MoeBlock)
+    block.path, block.norm_op, block.shared, block.device, block.train = p, Op(), Op(), torch.device("cpu"), True
+    block.n = torch.zeros(T, d, dtype=torch.bfloat16)
+    z = lambda *n, dtype=torch.bfloat16: torch.zeros(*n, dtype=dtype)
+    w = {"norm_weight": None, "norm_bias": None, "w_gate_up": z(E, 2 * f, d), "w_down": z(E, d, f), "shared_gate_up": None, "shared_down": None}
+    norm, experts, back = (getattr(MoeBlock, k).__wrapped__ for k in ("norm", "experts", "experts_backward"))
+    for x in (z(T - 1, d), z(T, d, dtype=torch.float32)):
+        with pytest.raises(ValueError, match="x:"):
+            norm(block, x, w)
+    for logits in (z(T - 1, G, dtype=torch.float32), z(T, G), z(T, G + 1, dtype=torch.float32), z(G, T, dtype=torch.float32).T):
+        with pytest.raises(ValueError, match="logits"):
+            experts(block, logits, w)
+    for call, first in ((experts, z(T, G, dtype=torch.float32)), (back, z(T, d))):
+        for k, bad in (("w_gate_up", z(E, f, d)), ("w_down", z(E, d, f, dtype=torch.float32))):
+            with pytest.raises(ValueError, match=k):
+                call(block, first, {**w, k: bad})
+    for d_out in (z(T - 1, d), z(T, d, dtype=torch.float32), z(T, 2 * d)[:, :d]):
+        with pytest.raises(ValueError, match="d_out"):
+            back(block, d_out, w)
+    block.train = False
+    with pytest.raises(RuntimeError, match="train"):
+        back(block, z(T, d), w)

@@ -752,3 +752,33 @@ def test_block_together():
             else:
                 w[name].copy_(t)
     assert block.path.status() == B.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_block_without_training(dtype):
+    """A block made for serving: its output against float64 (roundings as in test_block_together; fp32: 2^-24 each, sums of 128 and
+    192 products: 2^-16 of the norm), no gradients, and an output that its calls give again."""
+    from expert_output_overlap_amd.runtime import MoeBlock, MoePath
+
+    R, T_o, G, k, d, f, fs, M = 2, 40, 4, 2, 128, 128, 192, 16
+    T, D, dt, rnd = R * T_o, torch.float64, DT[dtype], gen(15)
+    w = {"norm_weight": 1 + 0.1 * rnd(d), "norm_bias": 0.1 * rnd(d), "w_gate_up": (rnd(G, 2 * f, d) / d ** 0.5).to(dt),
+         "w_down": (rnd(G, d, f) / d ** 0.5).to(dt), "shared_gate_up": (rnd(2 * fs, d) / d ** 0.5).to(dt),
+         "shared_down": (rnd(d, fs) / d ** 0.5).to(dt)}
+    block, x = MoeBlock(MoePath(R, T_o, G, G, k, d, f, M, dtype=dtype), fs, train=False), rnd(T, d).to(dt)
+    router = rnd(G, d) / d ** 0.5
+    out = block.experts(block.norm(x, w).float() @ router.T, w).clone()
+    idx, wt = block.path.topk_idx.long(), block.path.topk_w.to(D)
+    n = torch.nn.functional.layer_norm(x.to(D), (d,), w["norm_weight"].to(D), w["norm_bias"].to(D))
+
+    def mlp(gu, down):
+        g, u = (n @ gu.to(D).T).chunk(2, 1)
+        return (torch.nn.functional.silu(g) * u) @ down.to(D).T
+
+    want = mlp(w["shared_gate_up"], w["shared_down"])
+    for e in range(G):
+        want = want + (wt * (idx == e)).sum(1, keepdim=True) * mlp(w["w_gate_up"][e], w["w_down"][e])
+    assert (out.to(D) - want).norm() <= (8 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -16) * want.norm()
+    assert torch.equal(block.experts(block.norm(x, w).float() @ router.T, w), out) and block.path.status() == B.MOE_OK
+    with pytest.raises(RuntimeError, match="train"):
+        block.experts_backward(out, w)
