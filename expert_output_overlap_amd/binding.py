@@ -28,9 +28,13 @@ EXPORTS = ["moe_last_error", "moe_version", "moe_route", "moe_layout_capacity_ro
            "moe_expert_ffn_backward", "moe_combine_backward",
            "moe_layer_norm", "moe_layer_norm_workspace_bytes", "moe_layer_norm_backward", "moe_shared_ffn_row",
            "moe_shared_ffn_workspace_bytes", "moe_shared_ffn", "moe_shared_ffn_backward", "moe_adamw_workspace_bytes",
-           "moe_adamw_bind", "moe_adamw_step", "moe_adamw_read_states"]
+           "moe_adamw_bind", "moe_adamw_step", "moe_adamw_read_states", "moe_residual_norm",
+           "moe_residual_norm_workspace_bytes", "moe_residual_norm_backward", "moe_router_loss_workspace_bytes",
+           "moe_router_loss", "moe_router_backward", "moe_grad_workspace_bytes", "moe_grad_bind", "moe_grad_norm",
+           "moe_grad_clip"]
 MOE_ADAMW_BLOCK = 32
 MOE_NORM_MAX_D = 16384
+MOE_NORM_NONE, MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1, 2
 
 
 class moe_shape(ctypes.Structure):
@@ -101,6 +105,46 @@ class moe_adamw_plan(ctypes.Structure):
                 ("states8", ctypes.c_int32)]
 
 
+class moe_residual_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("d", "dtype", "param_dtype", "post", "pre")] + [
+        ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
+
+
+RESIDUAL_PARAMS = ["post_weight", "post_bias", "gate", "pre_weight", "pre_bias", "row_gate"]
+
+
+class moe_residual_norm_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in RESIDUAL_PARAMS]
+
+
+class moe_residual_norm_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "h", "s", "n", "stats")] + [
+        (n + "_stride", ctypes.c_int64) for n in "xhsn"]
+
+
+RESIDUAL_BWD_POINTERS = ["ds", "dn", "x", "h", "stats", "dx", "dh"] + ["d_" + n for n in RESIDUAL_PARAMS]
+
+
+class moe_residual_norm_bwd_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in RESIDUAL_BWD_POINTERS] + [
+        (n + "_stride", ctypes.c_int64) for n in ("ds", "dn", "x", "h", "dx", "dh")]
+
+
+class moe_router_shape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("experts", "top_k", "sequences", "dtype")] + [
+        ("balance", ctypes.c_float), ("z", ctypes.c_float)]
+
+
+class moe_grad_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("grad_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class moe_grad_plan(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_chunks", ctypes.c_int64), ("n_tensors", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, code: int, msg: str):
         super().__init__("%s failed (%d): %s" % (fn, code, msg))
@@ -142,6 +186,12 @@ def lib():
             "moe_shared_ffn": ([vp] * 9 + [i64, vp], i32), "moe_shared_ffn_backward": ([vp, vp, vp, i64, vp], i32),
             "moe_adamw_workspace_bytes": ([vp, i32], i64), "moe_adamw_bind": ([vp, i32, vp, i64, vp, vp], i32),
             "moe_adamw_step": ([vp, vp, vp], i32), "moe_adamw_read_states": ([vp, vp], i32),
+            "moe_residual_norm": ([vp] * 4, i32), "moe_residual_norm_workspace_bytes": ([vp], i64),
+            "moe_residual_norm_backward": ([vp] * 4 + [i64, vp], i32),
+            "moe_router_loss_workspace_bytes": ([vp], i64), "moe_router_loss": ([vp] * 8 + [i64, vp], i32),
+            "moe_router_backward": ([vp] * 10, i32),
+            "moe_grad_workspace_bytes": ([vp, i32], i64), "moe_grad_bind": ([vp, i32, vp, i64, vp, vp], i32),
+            "moe_grad_norm": ([vp, ctypes.c_double, ctypes.c_double, vp, vp, vp], i32), "moe_grad_clip": ([vp] * 3, i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -350,3 +400,55 @@ def moe_adamw_step(plan: moe_adamw_plan, cfg: moe_adamw_cfg, stream=None) -> int
 
 def moe_adamw_read_states(plan: moe_adamw_plan, stream=None) -> int:
     return _check("moe_adamw_read_states", lib().moe_adamw_read_states(ctypes.byref(plan), _stream(stream)))
+
+
+def moe_residual_norm(shape: moe_residual_norm_shape, params: moe_residual_norm_params, args: moe_residual_norm_args,
+                      stream=None) -> int:
+    return _check("moe_residual_norm", lib().moe_residual_norm(ctypes.byref(shape), ctypes.byref(params), ctypes.byref(args),
+                                                               _stream(stream)))
+
+
+def moe_residual_norm_workspace_bytes(shape: moe_residual_norm_shape) -> int:
+    return lib().moe_residual_norm_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_residual_norm_backward(shape: moe_residual_norm_shape, params: moe_residual_norm_params,
+                               args: moe_residual_norm_bwd_args, workspace, stream=None) -> int:
+    return _check("moe_residual_norm_backward", lib().moe_residual_norm_backward(
+        ctypes.byref(shape), ctypes.byref(params), ctypes.byref(args), _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def moe_router_loss_workspace_bytes(shape: moe_router_shape) -> int:
+    return lib().moe_router_loss_workspace_bytes(ctypes.byref(shape))
+
+
+def moe_router_loss(shape: moe_router_shape, logits, topk_idx, spans, counts, means, losses, workspace, stream=None) -> int:
+    return _check("moe_router_loss", lib().moe_router_loss(
+        ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(spans), _ptr(counts), _ptr(means), _ptr(losses),
+        _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def moe_router_backward(shape: moe_router_shape, logits, topk_idx, spans, counts, means, d_loss, d_weights, dlogits,
+                        stream=None) -> int:
+    return _check("moe_router_backward", lib().moe_router_backward(
+        ctypes.byref(shape), _ptr(logits), _ptr(topk_idx), _ptr(spans), _ptr(counts), _ptr(means), _ptr(d_loss),
+        _ptr(d_weights), _ptr(dlogits), _stream(stream)))
+
+
+def moe_grad_workspace_bytes(tensors) -> int:
+    """tensors: a ctypes array of moe_grad_tensor."""
+    return lib().moe_grad_workspace_bytes(tensors, len(tensors))
+
+
+def moe_grad_bind(tensors, workspace, plan: moe_grad_plan, stream=None) -> int:
+    return _check("moe_grad_bind", lib().moe_grad_bind(tensors, len(tensors), _ptr(workspace), _bytes(workspace),
+                                                       ctypes.byref(plan), _stream(stream)))
+
+
+def moe_grad_norm(plan: moe_grad_plan, max_norm: float, factor: float, norm, scale, stream=None) -> int:
+    return _check("moe_grad_norm", lib().moe_grad_norm(ctypes.byref(plan), max_norm, factor, _ptr(norm), _ptr(scale),
+                                                       _stream(stream)))
+
+
+def moe_grad_clip(plan: moe_grad_plan, scale, stream=None) -> int:
+    return _check("moe_grad_clip", lib().moe_grad_clip(ctypes.byref(plan), _ptr(scale), _stream(stream)))

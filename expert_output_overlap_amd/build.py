@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_overlap.so")
 SOURCES = ["api.cpp", "route.hip", "layout.hip", "ffn.hip", "bwd.hip", "combine.hip", "api_block.cpp", "norm.hip",
-           "shared.hip", "adamw.hip"]
+           "shared.hip", "adamw.hip", "api_train.cpp", "residual.hip", "router_loss.hip", "grad_norm.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # packed fp32 vector ops stay off in every GPU code object

@@ -169,6 +169,58 @@ struct AdamwStep {
 };
 int launch_adamw(const AdamwStep& a, int64_t n_chunks, bool read, hipStream_t st);
 
+// The norms around a block (residual.hip); strides in elements, all given.
+struct ResidualLaunch {
+  int64_t rows, x_stride, h_stride, s_stride, n_stride, ds_stride, dn_stride, dx_stride, dh_stride;
+  int d, dtype, param_dtype, post, pre;
+  bool backward;
+  float eps, rho;
+  moe_residual_norm_params p;
+  const void *x, *h, *ds, *dn;
+  void *s, *n, *dx, *dh;
+  float* stats;  // [rows][4]: mean and rstd of h, then of s
+  void *d_post_weight, *d_post_bias, *d_gate, *d_pre_weight, *d_pre_bias;
+  float* d_row_gate;
+  float* partial;  // backward: the workgroups' sums, or null where no [d] gradient is wanted
+};
+int64_t residual_partial_floats(int64_t rows, int d, int dtype);
+int launch_residual(const ResidualLaunch& a, hipStream_t st);
+
+// The router's losses and their gradient (router_loss.hip).
+struct RouterLaunch {
+  int64_t tokens;
+  int experts, top_k, sequences, dtype;
+  float balance, z;
+  const float* logits;
+  const int32_t *topk_idx, *spans;
+  int32_t *counts, *means;
+  float* losses;
+  const float *d_loss, *d_weights;
+  void* dlogits;
+  void* workspace;
+};
+int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences);
+int launch_router_loss(const RouterLaunch& a, hipStream_t st);
+int launch_router_backward(const RouterLaunch& a, hipStream_t st);
+
+// The gradient norm (grad_norm.hip): the plan's device table is the chunks, then the workgroups' partial sums.
+#define GRAD_CHUNK 8192  // elements of one chunk
+struct GradChunk {
+  const void* grad;
+  void* out;  // null: in place
+  int32_t n, grad_bf16, out_bf16, reserved;
+};
+struct GradLaunch {
+  const GradChunk* chunks;
+  int64_t n_chunks;
+  double* partial;
+  double max_norm, factor;
+  float *norm, *scale;
+};
+int64_t grad_partial_doubles(int64_t n_chunks);
+int launch_grad_norm(const GradLaunch& a, hipStream_t st);
+int launch_grad_clip(const GradLaunch& a, hipStream_t st);
+
 // The shared expert's block (shared.hip); row: elements in a row of h and in each half of gu and dgu.
 struct SharedLaunch {
   int64_t tokens;

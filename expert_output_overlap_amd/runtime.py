@@ -403,18 +403,218 @@ class AdamW:
         B.moe_adamw_read_states(self.plan, stream)
 
 
+NORM_KINDS = {"none": B.MOE_NORM_NONE, "layer": B.MOE_NORM_LAYER, "rms": B.MOE_NORM_RMS}
+
+
+class ResidualNorm:
+    """What joins a block's output to the residual stream and makes the next block's input (moe_residual_norm,
+    moe_residual_norm_backward), over up to ``rows`` rows of ``d`` elements, with the buffers of its results:
+    z = N1(h), s = residual_scale x + row_gate (gate z), n = N2(s), N1 = ``post`` and N2 = ``pre`` each "none", "layer" or "rms".
+    w: a dict of the parameters that there are, [d] each, of "post_weight", "post_bias", "gate", "pre_weight" and "pre_bias"
+    (others in it are not looked at); row_gate: fp32 [rows].  Rows may lie apart (a slice of a wider tensor).  A call's results stay until the
+    next call of the same kind; ``grads`` holds the parameters' gradients, and "row_gate" the row gate's."""
+
+    NAMES = B.RESIDUAL_PARAMS[:5]
+
+    def __init__(self, rows, d, dtype="bf16", param_dtype="f32", post="rms", pre="rms", residual_scale=1.0, eps=1e-5, train=True,
+                 device="cuda"):
+        self.device = _device(device)
+        self.rows, self.d, self.train = rows, d, train
+        self.dtype, self.param_dtype = TORCH_DTYPES[dtype], TORCH_DTYPES[param_dtype]
+        self.post, self.pre = post, pre
+        self.shape = B.moe_residual_norm_shape(rows, d, MOE_DTYPES[dtype], MOE_DTYPES[param_dtype], NORM_KINDS[post],
+                                               NORM_KINDS[pre], eps, residual_scale)
+        ws = _workspace(B.moe_residual_norm_workspace_bytes(self.shape), "moe_residual_norm_workspace_bytes", self.device)
+        z = dict(dtype=self.dtype, device=self.device)
+        self.s, self.n = torch.empty(rows, d, **z), torch.empty(rows, d, **z) if pre != "none" else None
+        self.stats = None
+        if train:
+            self.workspace = ws
+            self.stats = torch.empty(rows, 4, dtype=torch.float32, device=self.device)
+            self.dx, self.dh = torch.empty(rows, d, **z), torch.empty(rows, d, **z)
+            self.grads = {name: torch.empty(d, dtype=self.param_dtype, device=self.device) for name in self.NAMES
+                          if not (name.startswith("post") and post == "none" or name.startswith("pre") and pre == "none")}
+            self.grads["row_gate"] = torch.empty(rows, dtype=torch.float32, device=self.device)
+
+    def _rows(self, n, matrices):
+        """Checks the matrices and gives their addresses and strides, as the argument structures take them."""
+        got = {}
+        for name, t in matrices.items():
+            if t is None:
+                continue
+            _need(t, name, (n, self.d), self.dtype, self.device, strided=True)
+            got[name] = t.data_ptr()
+            if n > 1:
+                got[name + "_stride"] = t.stride(0)
+        return got
+
+    def _params(self, n, w, row_gate):
+        p = B.moe_residual_norm_params()
+        for name in self.NAMES:
+            t = w.get(name)
+            if t is not None:
+                _need(t, name, (self.d,), self.param_dtype, self.device)
+                setattr(p, name, t.data_ptr())
+        if row_gate is not None:
+            _need(row_gate, "row_gate", (n,), torch.float32, self.device)
+            p.row_gate = row_gate.data_ptr()
+        return p
+
+    def _count(self, x):
+        n = x.shape[0]
+        if n > self.rows:
+            raise ValueError("%d rows, made for up to %d" % (n, self.rows))
+        self.shape.rows = n
+        return n
+
+    @_on_own_device
+    def forward(self, x, h, w, row_gate=None, s=None, n=None, stream=None):
+        """(s, n), or (s, None) without a norm in front of the next block."""
+        T = self._count(x)
+        s = _first(self.s, T) if s is None else s
+        n = _first(self.n, T) if n is None and self.n is not None else n
+        a = B.moe_residual_norm_args(**self._rows(T, {"x": x, "h": h, "s": s, "n": n}),
+                                     stats=self.stats.data_ptr() if self.train and T else None)
+        B.moe_residual_norm(self.shape, self._params(T, w, row_gate), a, stream)
+        return s, n
+
+    @_on_own_device
+    def backward(self, ds, dn, x, h, w, row_gate=None, dx=None, dh=None, stream=None):
+        """(dx, dh), and the gradients of the parameters in w and of row_gate in ``grads``, for the x and h of the last forward call.
+        ds: the gradient that reaches s past the next block, or None; dn: that of n (None without a norm there)."""
+        if not self.train:
+            raise RuntimeError("made without train=True")
+        T = self._count(x)
+        dx = _first(self.dx, T) if dx is None else dx
+        dh = _first(self.dh, T) if dh is None else dh
+        b = B.moe_residual_norm_bwd_args(**self._rows(T, {"ds": ds, "dn": dn, "x": x, "h": h, "dx": dx, "dh": dh}),
+                                         stats=self.stats.data_ptr())
+        for name in self.NAMES:
+            if w.get(name) is not None and name in self.grads:
+                setattr(b, "d_" + name, self.grads[name].data_ptr())
+        if row_gate is not None:
+            b.d_row_gate = self.grads["row_gate"].data_ptr()
+        B.moe_residual_norm_backward(self.shape, self._params(T, w, row_gate), b, self.workspace, stream)
+        return dx, dh
+
+
+class RouterLoss:
+    """The router's balance loss and z loss over up to ``tokens`` rows of logits, with per-expert counts and the logits' gradient
+    (moe_router_loss, moe_router_backward): loss = balance B + z Z.  dtype: of the gradient.  spans: int32 [sequences, 2] on the
+    device, each sequence's first row and the row after its last, in ascending order (rows of none are padding), or None: equal
+    parts of the rows.  A call's results stay until the next call of the same kind: ``losses`` {loss, B, Z}, ``counts``
+    [sequences, experts], ``means`` {sequences with rows, their rows} and ``dlogits``."""
+
+    def __init__(self, tokens, experts, k, sequences=1, balance=0.01, z=0.0, dtype="f32", train=True, device="cuda"):
+        self.device = _device(device)
+        self.tokens, self.experts, self.k, self.sequences, self.train = tokens, experts, k, sequences, train
+        self.dtype = TORCH_DTYPES[dtype]
+        self.shape = B.moe_router_shape(tokens, experts, k, sequences, MOE_DTYPES[dtype], balance, z)
+        self.workspace = _workspace(B.moe_router_loss_workspace_bytes(self.shape), "moe_router_loss_workspace_bytes", self.device)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        self.counts, self.means = torch.empty(sequences, experts, **i32), torch.empty(2, **i32)
+        self.losses = torch.empty(3, dtype=torch.float32, device=self.device)
+        if train:
+            self.dlogits = torch.empty(tokens, experts, dtype=self.dtype, device=self.device)
+
+    def _check(self, logits, topk_idx, spans):
+        T = logits.shape[0]
+        if T > self.tokens:
+            raise ValueError("%d tokens, made for up to %d" % (T, self.tokens))
+        _need(logits, "logits", (T, self.experts), torch.float32, self.device)
+        _need(topk_idx, "topk_idx", (T, self.k), torch.int32, self.device)
+        if spans is not None:
+            _need(spans, "spans", (self.sequences, 2), torch.int32, self.device)
+        self.shape.tokens = T
+        return T
+
+    @_on_own_device
+    def forward(self, logits, topk_idx, spans=None, stream=None):
+        """losses, and the counts in their buffer."""
+        self._check(logits, topk_idx, spans)
+        B.moe_router_loss(self.shape, logits, topk_idx, spans, self.counts, self.means, self.losses, self.workspace, stream)
+        return self.losses
+
+    @_on_own_device
+    def backward(self, logits, topk_idx, d_weights=None, d_loss=None, spans=None, dlogits=None, stream=None):
+        """dlogits, for the logits, ids and spans of the last forward call.  d_weights: fp32 [tokens, k], the routing weights' gradient;
+        d_loss: fp32 [1] on the device, None = 1."""
+        if not self.train:
+            raise RuntimeError("made without train=True")
+        T = self._check(logits, topk_idx, spans)
+        dlogits = _first(self.dlogits, T) if dlogits is None else dlogits
+        _need(dlogits, "dlogits", (T, self.experts), self.dtype, self.device)
+        if d_weights is not None:
+            _need(d_weights, "d_weights", (T, self.k), torch.float32, self.device)
+        if d_loss is not None:
+            _need(d_loss, "d_loss", (1,), torch.float32, self.device)
+        B.moe_router_backward(self.shape, logits, topk_idx, spans, self.counts, self.means, d_loss, d_weights, dlogits, stream)
+        return dlogits
+
+
+class GradNorm:
+    """The norm of many gradients and their clipping (moe_grad_*).  tensors: dicts of device tensors, "g" (bf16 or fp32) and
+    optionally "out" (bf16 or fp32, as many elements), where ``clip`` writes instead of into g itself.  The tensors' addresses are
+    bound: their contents may change between calls, not they themselves.  ``total`` and ``scale`` (fp32 [1]) stay until the next
+    call; ``scale`` is what AdamW.step takes as grad_scale."""
+
+    def __init__(self, tensors, device=None, stream=None):
+        self.tensors = [dict(t) for t in tensors]
+        self.device = self.tensors[0]["g"].device if self.tensors else _device("cuda" if device is None else device)
+        table = (B.moe_grad_tensor * len(self.tensors))()
+        for i, (q, t) in enumerate(zip(table, self.tensors)):
+            g, out = t["g"], t.get("out")
+            for key, x in (("g", g), ("out", out)):
+                if x is not None and (x.dtype not in MOE_DTYPES or x.numel() != g.numel() or not x.is_contiguous() or
+                                      x.device != self.device):
+                    raise ValueError("tensor %d, %s: %d %s on %s, wanted %d contiguous bf16 or fp32 on %s" % (
+                        i, key, x.numel(), x.dtype, x.device, g.numel(), self.device))
+            q.grad, q.n, q.grad_dtype = g.data_ptr(), g.numel(), MOE_DTYPES[g.dtype]
+            if out is not None:
+                q.out, q.out_dtype = out.data_ptr(), MOE_DTYPES[out.dtype]
+        self.workspace = _workspace(B.moe_grad_workspace_bytes(table), "moe_grad_workspace_bytes", self.device)
+        self.plan = B.moe_grad_plan()
+        self.total, self.scale = (torch.empty(1, dtype=torch.float32, device=self.device) for _ in range(2))
+        with torch.cuda.device(self.device):
+            B.moe_grad_bind(table, self.workspace, self.plan, stream)
+
+    @_on_own_device
+    def norm(self, max_norm=float("inf"), factor=1.0, stream=None):
+        """total = factor times the norm of all gradients, scale = factor min(1, max_norm / (total + 1e-6))."""
+        B.moe_grad_norm(self.plan, max_norm, factor, self.total, self.scale, stream)
+        return self.total
+
+    @_on_own_device
+    def clip(self, max_norm=float("inf"), factor=1.0, stream=None):
+        """``norm``, and the gradients times ``scale`` into their "out" (in place without one)."""
+        B.moe_grad_norm(self.plan, max_norm, factor, self.total, self.scale, stream)
+        B.moe_grad_clip(self.plan, self.scale, stream)
+        return self.total
+
+
 class MoeBlock:
     """A pre-norm MoE block of one rank: n = norm(x); out = combine(routed experts(n)) + shared expert(n), and its backward.
     The router's product is the caller's: ``norm`` gives the rows its logits come from, ``experts`` takes the logits;
     ``experts_backward`` gives the gradient of n (and path.bwd_buffers()["dw_route"] that of the routing weights), to which
     the caller adds the router's part before ``norm_backward``.  Every call takes all of the path's T rows; logits are fp32
-    [T, G].  w: norm_weight, norm_bias, w_gate_up, w_down (the routed experts' [E_l, ...]), shared_gate_up, shared_down."""
+    [T, G].  w: norm_weight, norm_bias, w_gate_up, w_down (the routed experts' [E_l, ...]), shared_gate_up, shared_down.
 
-    def __init__(self, path: MoePath, shared_f: int, eps=1e-5, train=True):
+    losses: None, or RouterLoss's numbers as a dict (balance, z, dtype, and sequences, else the path's R owners): ``router_loss`` after
+    ``experts``, and ``router_backward``, which takes dw_route, after ``experts_backward``; the logits' gradient is the router's part.
+    join: None, or ResidualNorm's post, pre and residual_scale as a dict: ``join`` makes the residual stream and the next block's
+    input n of x and the block's output, with the parameters in w by ResidualNorm's names; a block takes such an input as its
+    attribute ``n``, in the place of ``norm``."""
+
+    def __init__(self, path: MoePath, shared_f: int, eps=1e-5, train=True, losses=None, join=None):
         self.path, self.train = path, train
         self.norm_op = LayerNorm(path.T, path.d, path.dtype, "f32", eps, train, path.device)
         self.shared = SharedFFN(path.T, path.d, shared_f, path.dtype, train, path.device)
         self.device = self.norm_op.device
+        self.losses_op = self.join_op = None
+        if losses is not None:
+            self.losses_op = RouterLoss(path.T, path.G, path.k, **{"sequences": path.R, **losses}, train=train, device=path.device)
+        if join is not None:
+            self.join_op = ResidualNorm(path.T, path.d, path.dtype, "f32", **join, eps=eps, train=train, device=path.device)
 
     def _experts_weights(self, w):
         """The routed path takes addresses: what it reads has to be there."""
@@ -450,6 +650,22 @@ class MoeBlock:
         p.combine_backward(d_out, stream=stream)
         dn = p.bwd_buffers()["dx"][: p.T]
         return self.shared.backward(d_out, self.n, w["shared_gate_up"], w["shared_down"], residual=dn, dx=dn, stream=stream)
+
+    def router_loss(self, logits, spans=None, stream=None):
+        """{loss, B, Z} of the logits that ``experts`` took (and ``losses_op.counts``)."""
+        return self.losses_op.forward(logits, self.path.topk_idx[: self.path.T], spans, stream)
+
+    def router_backward(self, logits, d_loss=None, spans=None, stream=None):
+        """The logits' gradient: of the losses, and of the routing weights through the experts' outputs."""
+        T = self.path.T
+        return self.losses_op.backward(logits, self.path.topk_idx[:T], self.path.bwd_buffers()["dw_route"][:T], d_loss, spans,
+                                       stream=stream)
+
+    def join(self, x, out, w, row_gate=None, stream=None):
+        return self.join_op.forward(x, out, w, row_gate, stream=stream)
+
+    def join_backward(self, ds, dn, x, out, w, row_gate=None, stream=None):
+        return self.join_op.backward(ds, dn, x, out, w, row_gate, stream=stream)
 
     @_on_own_device
     def norm_backward(self, dn, x, w, residual=None, stream=None):

@@ -507,6 +507,162 @@ int moe_adamw_step(const moe_adamw_plan* plan, const moe_adamw_cfg* cfg, void* s
  * holds each value exactly. */
 int moe_adamw_read_states(const moe_adamw_plan* plan, void* stream);
 
+/* ---- the norms around a block --------------------------------------------------------------------
+ * What joins a block's output h to the residual stream x and makes the next block's input of it, per row t of d elements:
+ *   z = N1(h),   s = residual_scale x + c_t (gate z),   n = N2(s)
+ * with N1 and N2 each none (N(v) = v), layer norm or RMS norm:
+ *   layer: N(v) = (v - mean(v)) rstd weight + bias, rstd = 1 / sqrt(mean((v - mean(v))^2) + eps)
+ *   rms:   N(v) = v rstd weight + bias,             rstd = 1 / sqrt(mean(v^2) + eps)
+ * gate has a number for each column, c one for each row.  Backward, from ds and dn, with v^ a norm's normalised input, and
+ * N'(a) = rstd (a - v^ mean(a v^)) [layer: - rstd mean(a)] [none: a]:
+ *   D = ds + N2'(dn pre_weight),  dx = residual_scale D,  dh = N1'(c gate D post_weight),
+ *   with U1 = sum over rows of c D h^ and U0 = sum of c D:
+ *   d_post_weight = gate U1,  d_post_bias = gate U0,  d_gate = post_weight U1 + post_bias U0,
+ *   d_pre_weight = sum of dn s^,  d_pre_bias = sum of dn,  d_row_gate[t] = sum over the row of D gate z.
+ * Everything in fp32; n comes from the unrounded s (also in the backward, which makes s anew from x and h: as exact, and no more
+ * to read), each result is rounded once.  Sums run in a fixed order: equal calls on equal devices give equal bits.
+ * Any alignment to the elements and any row stride >= d; elements between rows are neither read nor written. */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_LAYER = 1, MOE_NORM_RMS = 2 } moe_norm_kind;
+
+typedef struct {
+  int64_t rows;          /* T >= 0 (0: the parameters' gradients become 0, nothing else is written) */
+  int32_t d;             /* 1 .. MOE_NORM_MAX_D */
+  int32_t dtype;         /* moe_dtype of x, h, s, n and their gradients */
+  int32_t param_dtype;   /* moe_dtype of the weights, biases, gate and their gradients */
+  int32_t post;          /* moe_norm_kind of N1 */
+  int32_t pre;           /* moe_norm_kind of N2 */
+  float eps;             /* > 0, finite */
+  float residual_scale;  /* finite */
+} moe_residual_norm_shape;
+
+/* The parameters, all (device) [d], NULL = 1 (weights, gate) and 0 (biases); NULL where their norm is MOE_NORM_NONE. */
+typedef struct {
+  const void* post_weight;
+  const void* post_bias;
+  const void* gate;
+  const void* pre_weight;
+  const void* pre_bias;
+  const float* row_gate; /* (device) fp32 [rows], NULL = 1 */
+} moe_residual_norm_params;
+
+typedef struct {
+  const void* x;   /* (device) [rows, d] the residual stream */
+  const void* h;   /* (device) [rows, d] the block's output */
+  void* s;         /* (device) [rows, d] the new residual stream */
+  void* n;         /* (device) [rows, d] the next block's input; NULL with pre == MOE_NORM_NONE, and only then */
+  float* stats;    /* (device) fp32 [rows][4], 16-byte aligned, what the backward call takes, or NULL */
+  int64_t x_stride, h_stride, s_stride, n_stride; /* elements from a row to the next; 0 = d */
+} moe_residual_norm_args;
+
+/* s and n may be x or h (with the same row stride) where stats is NULL; no other overlap of an output. */
+int moe_residual_norm(const moe_residual_norm_shape* s, const moe_residual_norm_params* p, const moe_residual_norm_args* a,
+                      void* stream);
+
+typedef struct {
+  const void* ds;       /* (device) [rows, d] the gradient that reaches s past the next block; NULL = 0 */
+  const void* dn;       /* (device) [rows, d]; NULL with pre == MOE_NORM_NONE, and only then */
+  const void* x;        /* (device) [rows, d], h, stats: as the forward read and wrote them */
+  const void* h;
+  const float* stats;
+  void* dx;             /* (device) [rows, d], may be ds or dn (with the same row stride) */
+  void* dh;             /* (device) [rows, d], may be ds or dn (with the same row stride) */
+  void* d_post_weight;  /* (device) [d], written; each of the parameters' gradients may be NULL */
+  void* d_post_bias;
+  void* d_gate;
+  void* d_pre_weight;
+  void* d_pre_bias;
+  float* d_row_gate;    /* (device) fp32 [rows], written, or NULL */
+  int64_t ds_stride, dn_stride, x_stride, h_stride, dx_stride, dh_stride; /* 0 = d */
+} moe_residual_norm_bwd_args;
+
+/* Bytes of the backward call's workspace (the workgroups' partial sums of the parameters' gradients); -1 for an invalid shape.
+ * It needs no initial contents; calls that may run at the same time need one each. */
+int64_t moe_residual_norm_workspace_bytes(const moe_residual_norm_shape* s);
+
+/* workspace (device), 16-byte aligned, >= moe_residual_norm_workspace_bytes (may be NULL if no gradient of a [d] parameter is
+ * wanted).  One of ds and dn is needed. */
+int moe_residual_norm_backward(const moe_residual_norm_shape* s, const moe_residual_norm_params* p,
+                               const moe_residual_norm_bwd_args* b, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- the router's losses -------------------------------------------------------------------------
+ * What keeps the experts' loads even, from the logits that moe_route takes and the experts that it chose.  Rows belong to
+ * sequences; a row of no sequence is padding: it counts nowhere and its gradient is 0.  With p = softmax of a row's G logits,
+ * lse its log of the sum of exp, counts[s][g] how often sequence s's rows chose expert g, f[s][g] = G counts[s][g] / sum over g of
+ * counts[s][g] (0 where that is 0), N_s the sequence's rows, S' the sequences with rows and N all their rows:
+ *   B = 1/S' sum over s of 1/N_s sum over its rows of sum over g of f[s][g] p_g        (1 where all experts are chosen evenly)
+ *   Z = 1/N sum over rows of lse^2,     loss = balance B + z Z
+ * The gradient of the logits, with counts as constants, from dL = d_loss and the routing weights' gradient dw (a chosen expert's
+ * weight is its p, as moe_route gives it and moe_combine_backward differentiates it):
+ *   e_g = dL balance f[s][g] / (S' N_s) + sum over slots j with expert g of dw[t][j],
+ *   dlogits_g = p_g (e_g - sum over h of p_h e_h) + dL z 2 lse p_g / N.
+ * Everything in fp32, the sums over rows in 64 bits, in a fixed order: equal calls give equal bits.  An expert with a logit of -inf is not
+ * there for its row (p = 0); a row without any expert (all -inf) adds 0 to both losses and its gradient is 0, but it is one of
+ * its sequence's rows and its choices count.  A NaN or +inf makes its row's gradient and the losses NaN.  An id outside [0, G)
+ * counts nowhere, its slot's gradient goes nowhere. */
+typedef struct {
+  int64_t tokens;     /* T >= 0, T top_k < 2^31 */
+  int32_t experts;    /* G, 1 .. 1024 */
+  int32_t top_k;      /* 1 .. min(G, 16) */
+  int32_t sequences;  /* S >= 1, S G < 2^31 */
+  int32_t dtype;      /* moe_dtype of dlogits */
+  float balance, z;   /* the losses' coefficients, finite */
+} moe_router_shape;
+
+/* Bytes of the workspace of moe_router_loss; -1 for an invalid shape.  It needs no initial contents; calls that may run at the
+ * same time need one each. */
+int64_t moe_router_loss_workspace_bytes(const moe_router_shape* s);
+
+/* logits (device) fp32 [T, G]; topk_idx (device) int32 [T, k]; spans (device) int32 [S][2], each sequence's first row and the row
+ * after its last, first <= last <= the next one's first, all in [0, T] (what is outside is cut off), or NULL: S equal parts of the
+ * rows (T a multiple of S).  counts (device) int32 [S, G], means (device) int32 [2] = {S', N} and losses (device) fp32 [3] = {loss, B, Z} are written.
+ * workspace (device), 16-byte aligned, >= moe_router_loss_workspace_bytes. */
+int moe_router_loss(const moe_router_shape* s, const float* logits, const int32_t* topk_idx, const int32_t* spans,
+                    int32_t* counts, int32_t* means, float* losses, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* logits, topk_idx, spans, counts, means: the forward's; d_loss (device) fp32 [1] or NULL = 1; d_weights (device) fp32 [T, k] or
+ * NULL = 0; dlogits (device) [T, G] in s->dtype, written. */
+int moe_router_backward(const moe_router_shape* s, const float* logits, const int32_t* topk_idx, const int32_t* spans,
+                        const int32_t* counts, const int32_t* means, const float* d_loss, const float* d_weights,
+                        void* dlogits, void* stream);
+
+/* ---- gradient norm and clipping ------------------------------------------------------------------
+ * Over many tensors at once:
+ *   norm = factor sqrt(sum of g^2 over all elements of all tensors),
+ *   scale = factor min(1, max_norm / (norm + 1e-6)),     out = g scale (moe_grad_clip).
+ * scale is what moe_adamw_cfg.grad_scale takes.  Squares and sums in 64 bits, in a fixed order: no gradient is too large or too small for its
+ * square, and equal calls give equal bits.  A NaN or infinity among the gradients makes the norm one too, and scale NaN or 0;
+ * with an infinite max_norm scale = factor whatever the norm is. */
+typedef struct {
+  void* grad;         /* (device) [n] */
+  void* out;          /* (device) [n] where moe_grad_clip writes, or NULL: in place */
+  int64_t n;          /* elements, >= 0 */
+  int32_t grad_dtype; /* moe_dtype */
+  int32_t out_dtype;  /* moe_dtype of out */
+} moe_grad_tensor;
+
+/* A bound list of tensors: host values, and the descriptors in the caller's workspace. */
+typedef struct {
+  void* table;       /* (device) */
+  int64_t n_chunks;
+  int32_t n_tensors;
+  int32_t reserved;
+} moe_grad_plan;
+
+/* Bytes of the workspace that moe_grad_bind fills (the descriptors, and the calls' partial sums); -1 for invalid tensors. */
+int64_t moe_grad_workspace_bytes(const moe_grad_tensor* t, int32_t n_tensors);
+
+/* Check the tensors, write their descriptors into `workspace` (device, 16-byte aligned, kept as long as the plan) and fill
+ * *plan.  Waits for the copy on `stream`; not for a stream under capture.  MOE_EINVAL where a gradient or an output overlaps another
+ * (the same tensor twice).  Calls of one plan that may run at the same time need a plan each. */
+int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes, moe_grad_plan* plan,
+                  void* stream);
+
+/* norm, scale (device) fp32 [1], written; max_norm > 0 (or infinite), factor > 0, both representable in fp32. */
+int moe_grad_norm(const moe_grad_plan* plan, double max_norm, double factor, float* norm, float* scale, void* stream);
+
+/* out = g times *scale (device), each rounded once; in place nothing is touched where *scale is 1. */
+int moe_grad_clip(const moe_grad_plan* plan, const float* scale, void* stream);
+
 /* While enabled (nonzero), every moe_expert_ffn_overlap and moe_expert_ffn_backward call of this process times
  * each of its launches with a pair of HIP events that the launch itself records (hipExtLaunchKernel: the kernel's start and end, no marker
  * in the caller's stream).  Disabled by default.  Returns MOE_OK. */
