@@ -1,4 +1,8 @@
 // The norms around a block with its gate and the residual's scale, forward and backward (formulas in include/moe_overlap.h).
+//
+// Both are bound by HBM: forward 4 row transfers per row, backward 6.  A row is held in registers by a group of G threads, NV
+// 16-byte chunks each, and is read once; a norm's variance is the mean of squared differences to the mean.  The gate and N1's
+// parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).
 #include <algorithm>
 #include <type_traits>
 
@@ -8,217 +12,360 @@
 
 namespace {
 
-// A row's statistics over the G threads that hold it, NV chunks each in v (elements past the row are 0).  turn picks the one of
-// red's two halves that the last sum did not use
-template <int G, int NV, int C>
-__device__ __forceinline__ void row_stats(const float (&v)[NV * C], int kind, int t, int d, float eps, float (*red)[2 * (G / 64)],
-                                          int& turn, float* mean_out, float* rstd_out) {
-  float mean = 0.f, off = 0.f;
+using std::integral_constant;
+
+// C parameters from index i on, `empty` where there are none
+template <int C>
+__device__ __forceinline__ void param_chunk(const void* p, bool bf16, int i, int d, float empty, float* out) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < C; ++e) out[e] = empty;
+  } else if (bf16) params<bf16_t, C>((const bf16_t*)p, i, d, empty, out);
+  else params<float, C>((const float*)p, i, d, empty, out);
+}
+
+// A and B (0 without biases)
+template <int C>
+__device__ __forceinline__ void post_chunk(const ResidualLaunch& a, bool bf16, int i, float* A, float* B) {
+  float g[C];
+  param_chunk<C>(a.p.post_weight, bf16, i, a.d, 1.f, A);
+  param_chunk<C>(a.p.post_bias, bf16, i, a.d, 0.f, B);
+  if (!a.p.gate) return;
+  param_chunk<C>(a.p.gate, bf16, i, a.d, 1.f, g);
+#pragma unroll
+  for (int e = 0; e < C; ++e) {
+    A[e] *= g[e];
+    B[e] *= g[e];
+  }
+}
+
+// A row's statistics over the G threads that hold it; at(e): its element e of NV chunks of C, 0 past the row.  turn picks the one
+// of red's two halves that the last sum did not use
+template <int G, int NV, int C, class At>
+__device__ __forceinline__ void row_stats(At at, int kind, int t, int d, float eps, float (*red)[2 * (G / 64)], int& turn,
+                                          float* mean_out, float* rstd_out) {
   if (kind == MOE_NORM_NONE) {
     *mean_out = 0.f;
     *rstd_out = 1.f;
     return;
   }
+  float mean = 0.f, off = 0.f;
   if (kind == MOE_NORM_LAYER) {
     float s[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < NV * C; ++e) s[0] += v[e];
-    group_sum<G>(s, red[turn]);
+    for (int e = 0; e < NV * C; ++e) s[0] += at(e);
+    group_total<G>(s, red[turn]);
     turn ^= 1;
     mean = s[0] / d;
-  }
-  float q[2] = {0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const float e = v[j * C + i] - mean;
-      if ((j * G + t) * C + i < d) {
-        q[0] = fmaf(e, e, q[0]);
-        q[1] += e;
-      }
-    }
-  group_sum<G>(q, red[turn]);
-  turn ^= 1;
-  if (kind == MOE_NORM_LAYER) {  // the differences' own sum corrects the mean's rounding
-    off = q[1] / d;
-    mean += off;
-  }
-  *mean_out = mean;
-  *rstd_out = 1.0f / sqrtf(fmaxf(q[0] / d - off * off, 0.f) + eps);
-}
-
-template <typename T, int G, int NV>
-__device__ __forceinline__ void load_row(const void* base, int64_t row, int64_t stride, int t, int d, float* out) {
-  using K = Chunk<T>;
-  constexpr int C = K::C;
-  const T* p = (const T*)base + row * stride;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + t) * C;
-    const u32x4 v = c < d ? K::load(p + c, d - c) : u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < C; ++i) out[j * C + i] = K::at(v, i);
-  }
-}
-
-template <typename T, int G, int NV>
-__device__ __forceinline__ void store_row(void* base, int64_t row, int64_t stride, int t, int d, const float* v) {
-  using K = Chunk<T>;
-  constexpr int C = K::C;
-  T* p = (T*)base + row * stride;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int c = (j * G + t) * C;
-    if (c < d) K::store(p + c, K::pack(v + j * C), d - c);
-  }
-}
-
-template <typename PT, int C, int G, int NV>
-__device__ __forceinline__ void load_params(const void* p, int t, int d, float empty, float* out) {
-#pragma unroll
-  for (int j = 0; j < NV; ++j) params<PT, C>((const PT*)p, (j * G + t) * C, d, empty, out + j * C);
-}
-
-template <typename T, typename PT, int G, int NV>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_residual(ResidualLaunch a) {
-  constexpr int C = Chunk<T>::C, PER = G < 256 ? 256 / G : 1, E = NV * C;
-  __shared__ float red[2][2 * (G / 64)];
-  const int t = threadIdx.x % G, d = a.d;
-  int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * PER) {
-    float h[E], s[E], p[E], q[E];
-    load_row<T, G, NV>(a.h, r, a.h_stride, t, d, h);
-    load_row<T, G, NV>(a.x, r, a.x_stride, t, d, s);
-    float m1, r1, m2, r2;
-    row_stats<G, NV, C>(h, a.post, t, d, a.eps, red, turn, &m1, &r1);
-    const float c = a.p.row_gate ? a.p.row_gate[r] : 1.f;
-    load_params<PT, C, G, NV>(a.p.post_weight, t, d, 1.f, p);
-    load_params<PT, C, G, NV>(a.p.post_bias, t, d, 0.f, q);
-#pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = fmaf((h[e] - m1) * r1, p[e], q[e]);
-    load_params<PT, C, G, NV>(a.p.gate, t, d, 1.f, p);
+    float q[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int e = j * C + i;
-        s[e] = (j * G + t) * C + i < d ? fmaf(a.rho, s[e], c * (p[e] * h[e])) : 0.f;
+        const float e = at(j * C + i) - mean;
+        if ((j * G + t) * C + i < d) {
+          q[0] = fmaf(e, e, q[0]);
+          q[1] += e;
+        }
       }
-    store_row<T, G, NV>(a.s, r, a.s_stride, t, d, s);
-    row_stats<G, NV, C>(s, a.pre, t, d, a.eps, red, turn, &m2, &r2);
-    if (a.pre != MOE_NORM_NONE) {
-      load_params<PT, C, G, NV>(a.p.pre_weight, t, d, 1.f, p);
-      load_params<PT, C, G, NV>(a.p.pre_bias, t, d, 0.f, q);
+    group_total<G>(q, red[turn]);
+    turn ^= 1;
+    off = q[1] / d;  // the differences' own sum corrects the mean's rounding
+    mean += off;
+    *rstd_out = 1.0f / sqrtf(fmaxf(q[0] / d - off * off, 0.f) + eps);
+  } else {
+    float q[1] = {0.f};
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[e] = fmaf((s[e] - m2) * r2, p[e], q[e]);
-      store_row<T, G, NV>(a.n, r, a.n_stride, t, d, s);
+    for (int e = 0; e < NV * C; ++e) q[0] = fmaf(at(e), at(e), q[0]);
+    group_total<G>(q, red[turn]);
+    turn ^= 1;
+    *rstd_out = 1.0f / sqrtf(q[0] / d + eps);
+  }
+  *mean_out = mean;
+}
+
+// Rows by chunks: a row's address is the wave's, a chunk's 32-bit offset the lane's.  TAIL: the row's last chunk may hold fewer
+// than C elements (its code for single elements costs registers: 40 to 60 of the backward's)
+template <typename T, bool TAIL>
+struct Rows {
+  using K = Chunk<T>;
+  static __device__ __forceinline__ u32x4 load(const T* row, uint32_t c, int d) {
+    const T* p = (const T*)((const char*)row + c * (uint32_t)sizeof(T));
+    if ((int)c >= d) return u32x4{0, 0, 0, 0};
+    return TAIL ? K::load(p, d - (int)c) : load16(p);
+  }
+  static __device__ __forceinline__ void store(T* row, uint32_t c, int d, const float* f) {
+    T* p = (T*)((char*)row + c * (uint32_t)sizeof(T));
+    if ((int)c >= d) return;
+    if (TAIL) K::store(p, pack(f), d - (int)c);
+    else store16(p, pack(f));
+  }
+  // one conversion instruction for two bf16 (nearest, ties to even)
+  static __device__ __forceinline__ u32x4 pack(const float* f) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (sizeof(T) == 4) v[i] = __float_as_uint(f[i]);
+      else v[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * i]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * i + 1]) << 16);
+    }
+    return v;
+  }
+  template <int G, int NV>
+  static __device__ __forceinline__ void load_all(const void* base, int64_t row, int64_t stride, int t, int d, u32x4* v) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) v[j] = load((const T*)base + row * stride, (uint32_t)(j * G + t) * K::C, d);
+  }
+};
+
+// Makes the compiler forget what it knows of a chunk: it then unpacks it again where it is used next, instead of keeping twice the
+// registers as fp32 from its first use on
+__device__ __forceinline__ void forget(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+// The wave's number in the workgroup, as a number of the wave's
+__device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Forward.  SHARED: the parameters in LDS, once for all rows of the workgroup's eight waves, which hold a row each (G = 64: no
+// barrier); else read for each row, as where there are few rows or wide ones.
+template <typename T, int G, int NV, bool SHARED, bool TAIL>
+__global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a) {
+  using K = Chunk<T>;
+  using R = Rows<T, TAIL>;
+  constexpr int C = K::C, PER = SHARED ? 512 / G : 1, E = NV * C;
+  extern __shared__ float shared[];  // SHARED: A, pre_weight, then B and pre_bias where there is a bias; by four columns, then lanes
+  __shared__ float red[2][2 * (G / 64)];
+  const int t = threadIdx.x % G, d = a.d;
+  const bool pb = a.param_dtype == MOE_BF16, bias = a.p.post_bias || a.p.pre_bias;
+  if (SHARED) {
+    for (int c = threadIdx.x; c < NV * 64; c += 512) {
+      float v[4][C];
+      post_chunk<C>(a, pb, c * C, v[0], v[2]);
+      param_chunk<C>(a.p.pre_weight, pb, c * C, d, 1.f, v[1]);
+      param_chunk<C>(a.p.pre_bias, pb, c * C, d, 0.f, v[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < 2 || bias)
+#pragma unroll
+          for (int q = 0; q < C / 4; ++q)
+            *(float4*)(shared + k * E * 64 + ((c / 64 * (C / 4) + q) * 64 + c % 64) * 4) =
+                float4{v[k][4 * q], v[k][4 * q + 1], v[k][4 * q + 2], v[k][4 * q + 3]};
+    }
+    __syncthreads();
+  }
+  // chunk j of weight (0: A, 1: pre_weight) and of its bias
+  auto weights = [&](int which, int j, float* w, float* b) {
+    if (SHARED) {
+#pragma unroll
+      for (int q = 0; q < C / 4; ++q) {
+        const int at = ((j * (C / 4) + q) * 64 + t) * 4;
+        *(float4*)(w + 4 * q) = *(const float4*)(shared + which * E * 64 + at);
+        if (bias) *(float4*)(b + 4 * q) = *(const float4*)(shared + (2 + which) * E * 64 + at);
+        else *(float4*)(b + 4 * q) = float4{0, 0, 0, 0};
+      }
+    } else if (which == 0) post_chunk<C>(a, pb, (j * G + t) * C, w, b);
+    else {
+      param_chunk<C>(a.p.pre_weight, pb, (j * G + t) * C, d, 1.f, w);
+      param_chunk<C>(a.p.pre_bias, pb, (j * G + t) * C, d, 0.f, b);
+    }
+  };
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * PER + (SHARED ? wave_of() : 0); r < a.rows; r += (int64_t)gridDim.x * PER) {
+    u32x4 h[NV], x[NV];
+    R::template load_all<G, NV>(a.h, r, a.h_stride, t, d, h);
+    R::template load_all<G, NV>(a.x, r, a.x_stride, t, d, x);
+    const float c = a.p.row_gate ? a.p.row_gate[r] : 1.f;
+    float m1, r1, m2, r2, s[E];
+    row_stats<G, NV, C>([&](int e) { return K::at(h[e / C], e % C); }, a.post, t, d, a.eps, red, turn, &m1, &r1);
+    T* to = (T*)a.s + r * a.s_stride;
+    const float o1 = -m1 * r1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) forget(h[j]);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float w[C], b[C];
+      if (NV > 4) __builtin_amdgcn_sched_barrier(0);
+      weights(0, j, w, b);
+      const int at = (j * G + t) * C;
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        const float z = fmaf(fmaf(K::at(h[j], i), r1, o1), w[i], b[i]);
+        s[j * C + i] = at + (TAIL ? i : 0) < d ? fmaf(a.rho, K::at(x[j], i), c * z) : 0.f;
+      }
+      R::store(to, at, d, s + j * C);
+    }
+    row_stats<G, NV, C>([&](int e) { return s[e]; }, a.pre, t, d, a.eps, red, turn, &m2, &r2);
+    if (a.pre != MOE_NORM_NONE) {
+      to = (T*)a.n + r * a.n_stride;
+      const float o2 = -m2 * r2;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float w[C], b[C];
+        if (NV > 4) __builtin_amdgcn_sched_barrier(0);
+        weights(1, j, w, b);
+        const int at = (j * G + t) * C;
+#pragma unroll
+        for (int i = 0; i < C; ++i) w[i] = fmaf(fmaf(s[j * C + i], r2, o2), w[i], b[i]);
+        R::store(to, at, d, w);
+      }
     }
     if (t == 0 && a.stats) *(float4*)(a.stats + 4 * r) = float4{m1, r1, m2, r2};
   }
 }
 
-// dx and dh of a group's rows, and its sums of c D h^, c D, dn s^ and dn, which stay in registers over all of its rows and go to
-// the workspace at the end: partial [workgroup][4][d].
-template <typename T, typename PT, int G, int NV>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void k_residual_bwd(ResidualLaunch a) {
-  constexpr int C = Chunk<T>::C, PER = G < 256 ? 256 / G : 1, E = NV * C;
+// dx and dh of a group's rows, and its sums of c D h^ and dn s^ (BIAS: also of c D and dn), which stay in registers over all of its
+// rows and go to the workspace at the end: partial [workgroup][2 or 4][d].
+template <typename T, int G, int NV, bool BIAS, bool TAIL>
+__global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaunch a) {
+  using K = Chunk<T>;
+  using R = Rows<T, TAIL>;
+  constexpr int C = K::C, PER = G == 64 ? 4 : 1, E = NV * C, SUMS = BIAS ? 4 : 2;
   __shared__ float red[2][3 * (G / 64)];
-  __shared__ float join[PER > 1 ? (PER - 1) * 4 * E * G : 1];
+  __shared__ float join[PER > 1 ? (PER - 1) * SUMS * E * G : 1];
   const int t = threadIdx.x % G, d = a.d;
-  float acc[4][E];
+  const bool pb = a.param_dtype == MOE_BF16, pre = a.pre != MOE_NORM_NONE;
+  float acc[SUMS][E], A[E], B[E], W[E];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < SUMS; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    post_chunk<C>(a, pb, (j * G + t) * C, A + j * C, B + j * C);
+    param_chunk<C>(a.p.pre_weight, pb, (j * G + t) * C, d, 1.f, W + j * C);
+  }
+  const int64_t step = (int64_t)gridDim.x * PER;
+  int64_t r = (int64_t)blockIdx.x * PER + (PER > 1 ? wave_of() : 0);
+  u32x4 nh[NV], nx[NV], ns[NV], nn[NV];
+  float4 nst = {0, 0, 0, 0};
+  float nc = 1.f;
+  auto fetch = [&](int64_t row) {
+    R::template load_all<G, NV>(a.h, row, a.h_stride, t, d, nh);
+    R::template load_all<G, NV>(a.x, row, a.x_stride, t, d, nx);
+    if (a.ds) R::template load_all<G, NV>(a.ds, row, a.ds_stride, t, d, ns);
+    if (pre) R::template load_all<G, NV>(a.dn, row, a.dn_stride, t, d, nn);
+    nst = *(const float4*)(a.stats + 4 * row);
+    if (a.p.row_gate) nc = a.p.row_gate[row];
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j) ns[j] = nn[j] = u32x4{0, 0, 0, 0};
+  if (r < a.rows) fetch(r);
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / G; r < a.rows; r += (int64_t)gridDim.x * PER) {
-    const float4 st = *(const float4*)(a.stats + 4 * r);
-    const float c = a.p.row_gate ? a.p.row_gate[r] : 1.f;
-    float h[E], s[E], D[E], p[E], q[E], z[E];
-    load_row<T, G, NV>(a.h, r, a.h_stride, t, d, h);
-    load_row<T, G, NV>(a.x, r, a.x_stride, t, d, s);
-    if (a.ds) load_row<T, G, NV>(a.ds, r, a.ds_stride, t, d, D);
-    else
+  for (; r < a.rows; r += step) {
+    u32x4 h[NV], x[NV], g[NV], q[NV];
 #pragma unroll
-      for (int e = 0; e < E; ++e) D[e] = 0.f;
-    load_params<PT, C, G, NV>(a.p.post_weight, t, d, 1.f, p);
-    load_params<PT, C, G, NV>(a.p.post_bias, t, d, 0.f, q);
-    float g[E];
-    load_params<PT, C, G, NV>(a.p.gate, t, d, 1.f, g);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      h[e] = (h[e] - st.x) * st.y;
-      z[e] = g[e] * fmaf(h[e], p[e], q[e]);
-      s[e] = fmaf(a.rho, s[e], c * z[e]);
+    for (int j = 0; j < NV; ++j) {
+      h[j] = nh[j];
+      x[j] = nx[j];
+      g[j] = ns[j];
+      q[j] = nn[j];
     }
-    if (a.pre != MOE_NORM_NONE) {
-      float dn[E], w[E], v[2] = {0.f, 0.f};
-      load_row<T, G, NV>(a.dn, r, a.dn_stride, t, d, dn);
-      load_params<PT, C, G, NV>(a.p.pre_weight, t, d, 1.f, w);
+    const float4 st = nst;
+    const float c = nc, r1 = st.y, o1 = -st.x * r1, r2 = st.w, o2 = -st.z * r2;
+    if (r + step < a.rows) fetch(r + step);
+    auto n1 = [&](int j, int i) { return fmaf(K::at(h[j], i), r1, o1); };
+    auto z = [&](int j, int i, float n) { return BIAS ? fmaf(n, A[j * C + i], B[j * C + i]) : n * A[j * C + i]; };
+    auto n2 = [&](int j, int i, float n) { return fmaf(fmaf(a.rho, K::at(x[j], i), c * z(j, i, n)), r2, o2); };
+    float ma = 0.f, mn = 0.f;
+    if (pre) {
+      float v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        s[e] = (s[e] - st.z) * st.w;
-        acc[2][e] = fmaf(dn[e], s[e], acc[2][e]);
-        acc[3][e] += dn[e];
-        dn[e] *= w[e];
-        v[0] += dn[e];
-        v[1] = fmaf(dn[e], s[e], v[1]);
-      }
-      group_sum<G>(v, red[turn]);
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const int e = j * C + i;
+          const float n = n2(j, i, n1(j, i)), y = K::at(q[j], i), w = y * W[e];
+          acc[1][e] = fmaf(y, n, acc[1][e]);
+          if (BIAS) acc[SUMS - 1][e] += y;
+          v[0] += w;
+          v[1] = fmaf(w, n, v[1]);
+        }
+      group_total<G>(v, red[turn]);
       turn ^= 1;
-      const float ma = a.pre == MOE_NORM_LAYER ? v[0] / d : 0.f, mn = v[1] / d;
-#pragma unroll
-      for (int e = 0; e < E; ++e) D[e] += st.w * (dn[e] - ma - s[e] * mn);
+      if (a.pre == MOE_NORM_LAYER) ma = v[0] / d;
+      mn = v[1] / d;
     }
-    float o[E], v[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      forget(h[j]);
+      forget(x[j]);
+      forget(q[j]);
+    }
+    float D[E], v[3] = {0.f, 0.f, 0.f};
+    if (pre) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          const int e = j * C + i;
+          D[e] = fmaf(r2, fmaf(-n2(j, i, n1(j, i)), mn, fmaf(K::at(q[j], i), W[e], -ma)), K::at(g[j], i));
+        }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) D[e] = K::at(g[e / C], e % C);
+    }
+    T* to = (T*)a.dx + r * a.dx_stride;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * G + t) * C;
+      float o[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) {
         const int e = j * C + i;
-        if ((j * G + t) * C + i >= d) D[e] = 0.f;
-        o[e] = a.rho * D[e];
-        v[2] = fmaf(D[e], z[e], v[2]);
-        D[e] *= c;
-        acc[0][e] = fmaf(D[e], h[e], acc[0][e]);
-        acc[1][e] += D[e];
-        D[e] *= g[e] * p[e];
-        v[0] += D[e];
-        v[1] = fmaf(D[e], h[e], v[1]);
+        const float n = n1(j, i);
+        float y = at + (TAIL ? i : 0) < d ? D[e] : 0.f;
+        o[i] = a.rho * y;
+        v[2] = fmaf(y, z(j, i, n), v[2]);
+        y *= c;
+        acc[0][e] = fmaf(y, n, acc[0][e]);
+        if (BIAS) acc[SUMS / 2][e] += y;
+        y *= A[e];
+        v[0] += y;
+        v[1] = fmaf(y, n, v[1]);
+        D[e] = y;
       }
-    store_row<T, G, NV>(a.dx, r, a.dx_stride, t, d, o);
-    group_sum<G>(v, red[turn]);
-    turn ^= 1;
-    const float ma = a.post == MOE_NORM_LAYER ? v[0] / d : 0.f, mn = a.post == MOE_NORM_NONE ? 0.f : v[1] / d;
+      R::store(to, at, d, o);
+    }
+    if (a.post != MOE_NORM_NONE || a.d_row_gate) {
+      group_total<G>(v, red[turn]);
+      turn ^= 1;
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = st.y * (D[e] - ma - h[e] * mn);
-    store_row<T, G, NV>(a.dh, r, a.dh_stride, t, d, o);
+    for (int j = 0; j < NV; ++j) forget(h[j]);
+    ma = a.post == MOE_NORM_LAYER ? v[0] / d : 0.f;
+    mn = a.post == MOE_NORM_NONE ? 0.f : v[1] / d;
+    to = (T*)a.dh + r * a.dh_stride;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * G + t) * C;
+      float o[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] = r1 * fmaf(-n1(j, i), mn, D[j * C + i] - ma);
+      R::store(to, at, d, o);
+    }
     if (t == 0 && a.d_row_gate) a.d_row_gate[r] = v[2];
   }
   if (!a.partial) return;
   if (PER > 1) {  // the workgroup's groups, one after another
     const int w = threadIdx.x / G;
     if (w > 0) {
-      float* to = join + (w - 1) * 4 * E * G;
+      float* to = join + (w - 1) * SUMS * E * G;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < SUMS; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) to[(k * E + e) * G + t] = acc[k][e];
     }
     __syncthreads();
     if (w > 0) return;
     for (int u = 0; u < PER - 1; ++u) {
-      const float* from = join + u * 4 * E * G;
+      const float* from = join + u * SUMS * E * G;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < SUMS; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[k][e] += from[(k * E + e) * G + t];
     }
   }
-  float* out = a.partial + (int64_t)blockIdx.x * 4 * d;
+  float* out = a.partial + (int64_t)blockIdx.x * SUMS * d;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < SUMS; ++k)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -228,17 +375,18 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void k_residual_bwd(ResidualLaun
       }
 }
 
-// The parameters' gradients from the workgroups' partial sums: 64 columns per workgroup, its 16 waves take every 16th partial row,
-// and their sums are added in wave order.
+// The parameters' gradients from the workgroups' partial sums, rows of `sums` sums: 64 columns per workgroup, its 16 waves take every
+// 16th partial row, and their sums are added in wave order.
 template <typename PT>
-__global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int n) {
+__global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int n, int sums) {
   __shared__ float red[15][4][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, d = a.d;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   if (c < d)
     for (int k = wave; k < n; k += 16)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) s[u] += a.partial[((int64_t)k * 4 + u) * d + c];
+      for (int u = 0; u < 4; ++u)
+        if (u < sums) s[u] += a.partial[((int64_t)k * sums + u) * d + c];
   if (wave > 0)
 #pragma unroll
     for (int u = 0; u < 4; ++u) red[wave - 1][u][lane] = s[u];
@@ -256,77 +404,117 @@ __global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int 
     if (sizeof(PT) == 4) ((float*)p)[c] = v;
     else ((bf16_t*)p)[c] = f32_to_bf16(v);
   };
+  // {c D h^, dn s^}, or {c D h^, dn s^, c D, dn}
   const float gate = param(a.p.gate, 1.f);
   put(a.d_post_weight, gate * s[0]);
-  put(a.d_post_bias, gate * s[1]);
-  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), s[0], param(a.p.post_bias, 0.f) * s[1]));
-  put(a.d_pre_weight, s[2]);
+  put(a.d_pre_weight, s[1]);
+  put(a.d_post_bias, gate * s[2]);
   put(a.d_pre_bias, s[3]);
+  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), s[0], param(a.p.post_bias, 0.f) * s[2]));
 }
 
-template <bool BWD, typename T, typename PT, int G, int NV>
-void go(const ResidualLaunch& a, int64_t groups, hipStream_t st) {
-  constexpr int PER = G < 256 ? 256 / G : 1;
-  const dim3 grid((unsigned)((groups + PER - 1) / PER)), block(G < 256 ? 256 : G);
-  if constexpr (!BWD) hipLaunchKernelGGL((k_residual<T, PT, G, NV>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_residual_bwd<T, PT, G, NV>), grid, block, 0, st, a);
+int chunks_of(int d, int dtype) { return (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16; }
+
+// chunks in each of G threads, rounded up to a power of two
+int per_thread(int chunks, int G) {
+  int nv = 1;
+  while (nv * G < chunks) nv *= 2;
+  return nv;
 }
 
-template <typename T, typename PT>
-void pick(const ResidualLaunch& a, int G, int NV, int64_t groups, hipStream_t st) {
-  auto both = [&](auto g, auto nv) {
-    if (a.backward) go<true, T, PT, decltype(g)::value, decltype(nv)::value>(a, groups, st);
-    else go<false, T, PT, decltype(g)::value, decltype(nv)::value>(a, groups, st);
+template <typename T, int G, int NV, bool SHARED, bool TAIL>
+void forward(const ResidualLaunch& a, hipStream_t st) {
+  constexpr int PER = SHARED ? 512 / G : 1;
+  const int64_t groups = (a.rows + PER - 1) / PER, most = SHARED ? 512 : 256 * 2048 / G;
+  const int lds = SHARED ? (a.p.post_bias || a.p.pre_bias ? 4 : 2) * NV * Chunk<T>::C * 64 * 4 : 0;
+  if (lds > 65536)
+    (void)hipFuncSetAttribute((const void*)k_residual<T, G, NV, SHARED, TAIL>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  hipLaunchKernelGGL((k_residual<T, G, NV, SHARED, TAIL>), dim3((unsigned)std::min(groups, most)), dim3(SHARED ? 512 : G), lds, st, a);
+}
+
+template <typename T, bool TAIL>
+void forward(const ResidualLaunch& a, hipStream_t st) {
+  const int chunks = chunks_of(a.d, a.dtype);
+  auto with = [&](auto g, auto shared, int nv) {
+    constexpr int G = decltype(g)::value;
+    constexpr bool S = decltype(shared)::value;
+    if (nv == 1) forward<T, G, 1, S, TAIL>(a, st);
+    else if (nv == 2) forward<T, G, 2, S, TAIL>(a, st);
+    else if (nv == 4) forward<T, G, 4, S, TAIL>(a, st);
+    else if constexpr (G < 1024) {
+      if (nv == 8) forward<T, G, 8, S, TAIL>(a, st);
+      else forward<T, G, 16, S, TAIL>(a, st);
+    }
   };
-  using std::integral_constant;
-  if (G == 64 && NV == 1) both(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  else if (G == 64) both(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  else if (G == 256 && NV == 1) both(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  else if (G == 256 && NV == 2) both(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  else if (G == 256) go<false, T, PT, 256, 4>(a, groups, st);
-  else if (G == 1024) go<true, T, PT, 1024, 1>(a, groups, st);
-  else if (NV == 4) both(integral_constant<int, 512>{}, integral_constant<int, 4>{});
-  else if constexpr (sizeof(T) == 4) both(integral_constant<int, 512>{}, integral_constant<int, 8>{});
+  if (a.rows >= 2048 && chunks <= 1024) with(integral_constant<int, 64>{}, std::true_type{}, per_thread(chunks, 64));
+  else if (a.rows >= 512 || chunks <= 256) with(integral_constant<int, 256>{}, std::false_type{}, per_thread(chunks, 256));
+  else with(integral_constant<int, 1024>{}, std::false_type{}, per_thread(chunks, 1024));
 }
 
-void plan(int d, int dtype, bool backward, int* G, int* NV) {
-  const int chunks = (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16;
-  *G = chunks <= 128 ? 64 : chunks <= 512 ? 256 : chunks <= 1024 ? (backward ? 1024 : 256) : 512;
-  const int per = (chunks + *G - 1) / *G;
-  *NV = per <= 2 ? per : per <= 4 ? 4 : 8;
+// Eight elements in each thread of the backward's groups (16 where a row is wider than 8192)
+void backward_plan(int d, int dtype, int* G, int* NV) {
+  const int c = dtype == MOE_BF16 ? 8 : 4;
+  *G = 64;
+  while (*G < 1024 && *G * 8 < d) *G *= 2;
+  *NV = (*G * 8 < d ? 16 : 8) / c;
 }
 
-int64_t groups_of(int64_t rows, int G, int NV, bool backward) {
-  const int64_t most = 256ll * 16 * 64 / G;
-  return std::min(backward ? std::max(rows / 4, std::min<int64_t>(rows, 256)) : rows, most);
+int64_t backward_groups(int64_t rows, int G) { return std::min<int64_t>(std::max<int64_t>(rows / 4, std::min<int64_t>(rows, 256)), 256 * 1024 / G); }
+
+template <typename T, bool TAIL>
+void backward(const ResidualLaunch& a, bool bias, int64_t groups, hipStream_t st) {
+  int G, NV;
+  backward_plan(a.d, a.dtype, &G, &NV);
+  constexpr int V8 = 8 / Chunk<T>::C;
+  auto go = [&](auto g, auto nv) {
+    constexpr int GG = decltype(g)::value, N = decltype(nv)::value, PER = GG == 64 ? 4 : 1;
+    const dim3 grid((unsigned)((groups + PER - 1) / PER)), block(GG * PER);
+    if (bias) hipLaunchKernelGGL((k_residual_bwd<T, GG, N, true, TAIL>), grid, block, 0, st, a);
+    else hipLaunchKernelGGL((k_residual_bwd<T, GG, N, false, TAIL>), grid, block, 0, st, a);
+  };
+  if (G == 64) go(integral_constant<int, 64>{}, integral_constant<int, V8>{});
+  else if (G == 128) go(integral_constant<int, 128>{}, integral_constant<int, V8>{});
+  else if (G == 256) go(integral_constant<int, 256>{}, integral_constant<int, V8>{});
+  else if (G == 512) go(integral_constant<int, 512>{}, integral_constant<int, V8>{});
+  else if (NV == V8) go(integral_constant<int, 1024>{}, integral_constant<int, V8>{});
+  else go(integral_constant<int, 1024>{}, integral_constant<int, 2 * V8>{});
 }
 
 }  // namespace
 
 int64_t residual_partial_floats(int64_t rows, int d, int dtype) {
   int G, NV;
-  plan(d, dtype, true, &G, &NV);
-  const int64_t per = G < 256 ? 256 / G : 1;
-  return (groups_of(rows, G, NV, true) + per - 1) / per * 4 * d;
+  backward_plan(d, dtype, &G, &NV);
+  const int64_t per = G == 64 ? 4 : 1;
+  return (backward_groups(rows, G) + per - 1) / per * 4 * d;
 }
 
 int launch_residual(const ResidualLaunch& a, hipStream_t st) {
-  int G, NV;
-  plan(a.d, a.dtype, a.backward, &G, &NV);
-  const int64_t groups = groups_of(a.rows, G, NV, a.backward);
-  const bool tb = a.dtype == MOE_BF16, pb = a.param_dtype == MOE_BF16;
-  if (a.rows > 0) {
-    if (tb && pb) pick<bf16_t, bf16_t>(a, G, NV, groups, st);
-    else if (tb) pick<bf16_t, float>(a, G, NV, groups, st);
-    else if (pb) pick<float, bf16_t>(a, G, NV, groups, st);
-    else pick<float, float>(a, G, NV, groups, st);
+  const bool tb = a.dtype == MOE_BF16, tail = a.d % (tb ? 8 : 4) != 0;
+  if (!a.backward) {
+    if (a.rows == 0) return 0;
+    if (tb && tail) forward<bf16_t, true>(a, st);
+    else if (tb) forward<bf16_t, false>(a, st);
+    else if (tail) forward<float, true>(a, st);
+    else forward<float, false>(a, st);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
   }
-  if (a.backward && (a.d_post_weight || a.d_post_bias || a.d_gate || a.d_pre_weight || a.d_pre_bias)) {
-    const int64_t per = G < 256 ? 256 / G : 1;
+  int G, NV;
+  backward_plan(a.d, a.dtype, &G, &NV);
+  const int64_t groups = backward_groups(a.rows, G), per = G == 64 ? 4 : 1;
+  // sums of c D and dn too, for the biases' gradients and post_bias's part of the gate's
+  const bool bias = a.p.post_bias || a.d_post_bias || a.d_pre_bias;
+  if (a.rows > 0) {
+    if (tb && tail) backward<bf16_t, true>(a, bias, groups, st);
+    else if (tb) backward<bf16_t, false>(a, bias, groups, st);
+    else if (tail) backward<float, true>(a, bias, groups, st);
+    else backward<float, false>(a, bias, groups, st);
+  }
+  if (a.d_post_weight || a.d_post_bias || a.d_gate || a.d_pre_weight || a.d_pre_bias) {
     const int n = (int)((groups + per - 1) / per);
     const dim3 grid((unsigned)((a.d + 63) / 64));
-    if (pb) hipLaunchKernelGGL(k_residual_params<bf16_t>, grid, dim3(1024), 0, st, a, n);
-    else hipLaunchKernelGGL(k_residual_params<float>, grid, dim3(1024), 0, st, a, n);
+    if (a.param_dtype == MOE_BF16) hipLaunchKernelGGL(k_residual_params<bf16_t>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
+    else hipLaunchKernelGGL(k_residual_params<float>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
   }
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

@@ -111,4 +111,32 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* buf) {
   }
 }
 
+// As group_sum for N <= 4, with fewer registers: the waves' sums meet in lanes of one wave, 16 to a value, instead of one register
+// each (48 for the three values of 16 waves).  The results are the wave's numbers.
+template <int G, int N>
+__device__ __forceinline__ void group_total(float (&v)[N], float* buf) {
+  static_assert(N <= 4 && G <= 1024, "16 lanes to a value");
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = lanes_sum(v[n]);
+  if (G > 64) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane >> 4, w = lane & 15;
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) buf[wave * N + k] = v[k];
+    }
+    __syncthreads();
+    float s = n < N && w < G / 64 ? buf[w * N + n] : 0.f;
+    auto add = [&](auto ctrl) {
+      s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    add(std::integral_constant<int, 0x111>{});  // row_shr 1, 2, 4, 8
+    add(std::integral_constant<int, 0x112>{});
+    add(std::integral_constant<int, 0x114>{});
+    add(std::integral_constant<int, 0x118>{});
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      v[k] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 16 * k + 15));
+  }
+}
+
 }  // namespace
