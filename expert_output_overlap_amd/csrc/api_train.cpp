@@ -112,7 +112,7 @@ int64_t grad_chunks(const moe_grad_tensor* t, int32_t n) {
 int64_t table_bytes(int64_t n_chunks) { return n_chunks * (int64_t)sizeof(GradChunk); }
 
 const char* check_grad_plan(const moe_grad_plan* p) {
-  if (!p || p->n_chunks < 0 || p->n_chunks >= 1 << 24 || (p->n_chunks > 0 && !p->table)) return "plan not bound";
+  if (!p || p->n_chunks < 0 || p->n_chunks >= 1 << 24 || !p->table) return "plan not bound";
   return nullptr;
 }
 
@@ -120,7 +120,8 @@ GradLaunch grad_of(const moe_grad_plan* p) {
   GradLaunch a{};
   a.chunks = (const GradChunk*)p->table;
   a.n_chunks = p->n_chunks;
-  a.partial = (double*)((char*)p->table + table_bytes(p->n_chunks));
+  a.counters = (uint32_t*)((char*)p->table + table_bytes(p->n_chunks));
+  a.partial = (double*)(a.counters + grad_counter_words(p->n_chunks));
   return a;
 }
 
@@ -288,7 +289,7 @@ int moe_router_backward(const moe_router_shape* s, const float* logits, const in
 int64_t moe_grad_workspace_bytes(const moe_grad_tensor* t, int32_t n_tensors) {
   if (check_grads(t, n_tensors)) return -1;
   const int64_t n = grad_chunks(t, n_tensors);
-  return table_bytes(n) + 8 * grad_partial_doubles(n);
+  return table_bytes(n) + 4 * grad_counter_words(n) + 8 * grad_partial_doubles(n);
 }
 
 int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes, moe_grad_plan* plan,
@@ -296,14 +297,14 @@ int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, 
   if (const char* e = check_grads(t, n_tensors)) return moe_fail(MOE_EINVAL, e);
   if (!plan) return moe_fail(MOE_EINVAL, "null plan");
   const int64_t n_chunks = grad_chunks(t, n_tensors), need = moe_grad_workspace_bytes(t, n_tensors);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return moe_fail(MOE_EINVAL, "workspace too small");
+  if (!workspace || workspace_bytes < need) return moe_fail(MOE_EINVAL, "workspace too small");
   if (off(workspace, 16)) return moe_fail(MOE_EINVAL, "workspace must be 16-byte aligned");
   try {
     struct Range {
       uintptr_t at, end;
     };
     std::vector<Range> spans;
-    if (need > 0) spans.push_back({(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)need});
+    spans.push_back({(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)need});
     for (int i = 0; i < n_tensors; ++i) {
       if (t[i].n == 0) continue;
       const uintptr_t g = (uintptr_t)t[i].grad, o = (uintptr_t)t[i].out;
@@ -314,23 +315,23 @@ int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, 
     for (size_t i = 1; i < spans.size(); ++i)
       if (spans[i].at < spans[i - 1].end)
         return moe_fail(MOE_EINVAL, "a gradient or an output overlaps another (the same tensor twice?)");
-    if (n_chunks > 0) {
-      hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-      if (hipStreamIsCapturing((hipStream_t)stream, &cap) != hipSuccess) return moe_fail(MOE_EHIP, "stream query failed");
-      if (cap != hipStreamCaptureStatusNone) return moe_fail(MOE_EINVAL, "a plan cannot be bound under capture");
-      std::vector<GradChunk> table;
-      table.reserve((size_t)n_chunks);
-      for (int i = 0; i < n_tensors; ++i)
-        for (int64_t at = 0; at < t[i].n; at += GRAD_CHUNK)
-          table.push_back({(const char*)t[i].grad + at * elem(t[i].grad_dtype),
-                           t[i].out ? (char*)t[i].out + at * elem(t[i].out_dtype) : nullptr,
-                           (int32_t)std::min<int64_t>(GRAD_CHUNK, t[i].n - at), t[i].grad_dtype == MOE_BF16,
-                           t[i].out && t[i].out_dtype == MOE_BF16, 0});
-      if (hipMemcpyAsync(workspace, table.data(), (size_t)table_bytes(n_chunks), hipMemcpyHostToDevice, (hipStream_t)stream) !=
-              hipSuccess ||
-          hipStreamSynchronize((hipStream_t)stream) != hipSuccess)
-        return moe_fail(MOE_EHIP, "plan copy failed");
-    }
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing((hipStream_t)stream, &cap) != hipSuccess) return moe_fail(MOE_EHIP, "stream query failed");
+    if (cap != hipStreamCaptureStatusNone) return moe_fail(MOE_EINVAL, "a plan cannot be bound under capture");
+    const size_t head = (size_t)(table_bytes(n_chunks) + 4 * grad_counter_words(n_chunks));  // the records, and zeros
+    std::vector<GradChunk> table;
+    table.reserve(head / sizeof(GradChunk) + 1);
+    for (int i = 0; i < n_tensors; ++i)
+      for (int64_t at = 0; at < t[i].n; at += GRAD_CHUNK)
+        table.push_back({(const char*)t[i].grad + at * elem(t[i].grad_dtype),
+                         t[i].out ? (char*)t[i].out + at * elem(t[i].out_dtype) : nullptr,
+                         (int32_t)std::min<int64_t>(GRAD_CHUNK, t[i].n - at), t[i].grad_dtype == MOE_BF16,
+                         t[i].out && t[i].out_dtype == MOE_BF16, 0});
+    table.resize(head / sizeof(GradChunk) + 1, GradChunk{});
+    if (hipMemcpyAsync(workspace, table.data(), head, hipMemcpyHostToDevice, (hipStream_t)stream) !=
+            hipSuccess ||
+        hipStreamSynchronize((hipStream_t)stream) != hipSuccess)
+      return moe_fail(MOE_EHIP, "plan copy failed");
     plan->table = workspace;
     plan->n_chunks = n_chunks;
     plan->n_tensors = n_tensors;

@@ -1,15 +1,43 @@
 // The global norm of many gradients, and clipping (formulas in include/moe_overlap.h).
+//
+// Both are bound by HBM.  The tensors are cut into chunks of GRAD_CHUNK elements, each a record of the plan's table with its own
+// address, so that a launch of many small tensors has no search; a workgroup takes every grid-th chunk.  A square and its sum are
+// one fp64 instruction each on this chip at the fp32 rate: they hide behind the loads and need no care for the gradients' range.
 #include <algorithm>
 
 #include "common.h"
+#include "join.h"
 #include "launch.h"
+#include "row_util.h"
 
 namespace {
 
 constexpr int MAX_BLOCKS = 2048;
 
-__device__ __forceinline__ float value(const void* p, bool bf16, int64_t i) {
-  return bf16 ? bf16_to_f32(((const bf16_t*)p)[i]) : ((const float*)p)[i];
+// Sum of squares of a thread's part of a chunk
+template <typename T>
+__device__ __forceinline__ void squares(const GradChunk& k, double (&s)[2]) {
+  using K = Chunk<T>;
+  constexpr int C = K::C, STEPS = GRAD_CHUNK / C / 256;
+  const T* g = (const T*)(__attribute__((address_space(1))) const T*)k.grad;
+  u32x4 v[STEPS];
+  if (k.n == GRAD_CHUNK) {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) v[j] = load16(g + (j * 256 + threadIdx.x) * C);
+  } else {
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+      const int at = (j * 256 + (int)threadIdx.x) * C;
+      v[j] = at < k.n ? K::load(g + at, k.n - at) : u32x4{0, 0, 0, 0};
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const double d = K::at(v[j], i);
+      s[i & 1] = fma(d, d, s[i & 1]);
+    }
 }
 
 // The workgroup's sum in every thread, waves in order
@@ -17,58 +45,96 @@ __device__ __forceinline__ double block_sum(double v) {
   __shared__ double red[4];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  __syncthreads();
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
   return red[0] + red[1] + red[2] + red[3];
 }
 
-__global__ __launch_bounds__(256) void k_grad_sum(GradLaunch a) {
-  double s = 0;
+__global__ __launch_bounds__(256) void k_grad_norm(GradLaunch a) {
+  __shared__ int flag;
+  double s[2] = {0, 0};
   for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
     const GradChunk k = a.chunks[c];
-    for (int i = threadIdx.x; i < k.n; i += 256) {
-      const double g = value(k.grad, k.grad_bf16, i);
-      s = fma(g, g, s);
-    }
+    if (k.grad_bf16) squares<bf16_t>(k, s);
+    else squares<float>(k, s);
   }
-  s = block_sum(s);
-  if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
-}
-
-__global__ __launch_bounds__(256) void k_grad_finish(GradLaunch a, int n) {
-  double s = 0;
-  for (int i = threadIdx.x; i < n; i += 256) s += a.partial[i];
-  s = block_sum(s);
+  double all = block_sum(s[0] + s[1]);
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) hand_out(&a.partial[blockIdx.x], all);
+    if (!last_of(a.counters, blockIdx.x, gridDim.x, &flag)) return;
+    all = 0;
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += 256) all += take(&a.partial[i]);
+    all = block_sum(all);
+  }
   if (threadIdx.x > 0) return;
-  const double norm = a.factor * sqrt(s), ratio = a.max_norm / (norm + 1e-6);
+  const double norm = a.factor * sqrt(all), ratio = a.max_norm / (norm + 1e-6);
   *a.norm = (float)norm;
   // not fmin: a NaN stays one
   *a.scale = (float)(a.factor * (isinf(a.max_norm) || ratio >= 1 ? 1.0 : ratio));
 }
 
-__global__ __launch_bounds__(256) void k_grad_clip(GradLaunch a) {
-  const float f = *a.scale;
-  const GradChunk k = a.chunks[blockIdx.x];
-  if (!k.out && f == 1.f) return;
-  void* out = k.out ? k.out : (void*)k.grad;
-  const bool to_bf16 = k.out ? k.out_bf16 : k.grad_bf16;
-  for (int i = threadIdx.x; i < k.n; i += 256) {
-    const float v = value(k.grad, k.grad_bf16, i) * f;
-    if (to_bf16) ((bf16_t*)out)[i] = f32_to_bf16(v);
-    else ((float*)out)[i] = v;
+template <typename T, typename O>
+__device__ __forceinline__ void scaled(const GradChunk& k, void* to, float f) {
+  using K = Chunk<T>;
+  constexpr int C = K::C, STEPS = GRAD_CHUNK / C / 256;
+  const T* g = (const T*)(__attribute__((address_space(1))) const T*)k.grad;
+  O* out = (O*)(__attribute__((address_space(1))) O*)to;
+  u32x4 v[STEPS];
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int at = (j * 256 + (int)threadIdx.x) * C;
+    v[j] = k.n == GRAD_CHUNK ? load16(g + at) : at < k.n ? K::load(g + at, k.n - at) : u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int at = (j * 256 + (int)threadIdx.x) * C, n = k.n - at;
+    float w[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) w[i] = K::at(v[j], i) * f;
+    if (n <= 0) continue;
+    if (n < C) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < n) {
+          if constexpr (sizeof(O) == 4) out[at + i] = w[i];
+          else out[at + i] = f32_to_bf16(w[i]);
+        }
+    } else if constexpr (sizeof(O) == 4) __builtin_memcpy(out + at, w, 4 * C);
+    else {
+      uint32_t q[C / 2];
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i + 1]) << 16);
+      __builtin_memcpy(out + at, q, 2 * C);
+    }
   }
 }
 
-int sum_blocks(int64_t n_chunks) { return (int)std::min<int64_t>(n_chunks, MAX_BLOCKS); }
+// The chunks backwards: the last ones that k_grad_norm read are still in the last-level cache
+__global__ __launch_bounds__(256) void k_grad_clip(GradLaunch a) {
+  const float f = *a.scale;
+  const GradChunk k = a.chunks[a.n_chunks - 1 - blockIdx.x];
+  if (!k.out && f == 1.f) return;
+  void* out = k.out ? k.out : (void*)k.grad;
+  const bool to_bf16 = k.out ? k.out_bf16 : k.grad_bf16;
+  if (k.grad_bf16) {
+    if (to_bf16) scaled<bf16_t, bf16_t>(k, out, f);
+    else scaled<bf16_t, float>(k, out, f);
+  } else {
+    if (to_bf16) scaled<float, bf16_t>(k, out, f);
+    else scaled<float, float>(k, out, f);
+  }
+}
+
+int sum_blocks(int64_t n_chunks) { return (int)std::max<int64_t>(1, std::min<int64_t>(n_chunks, MAX_BLOCKS)); }
 
 }  // namespace
 
+int64_t grad_counter_words(int64_t n_chunks) { return join_words(sum_blocks(n_chunks)); }
 int64_t grad_partial_doubles(int64_t n_chunks) { return sum_blocks(n_chunks); }
 
 int launch_grad_norm(const GradLaunch& a, hipStream_t st) {
-  const int n = sum_blocks(a.n_chunks);
-  if (n > 0) hipLaunchKernelGGL(k_grad_sum, dim3(n), dim3(256), 0, st, a);
-  hipLaunchKernelGGL(k_grad_finish, dim3(1), dim3(256), 0, st, a, n);
+  hipLaunchKernelGGL(k_grad_norm, dim3(sum_blocks(a.n_chunks)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -203,7 +203,8 @@ int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int seque
 int launch_router_loss(const RouterLaunch& a, hipStream_t st);
 int launch_router_backward(const RouterLaunch& a, hipStream_t st);
 
-// The gradient norm (grad_norm.hip): the plan's device table is the chunks, then the workgroups' partial sums.
+// The gradient norm (grad_norm.hip): the plan's device table is the chunks, then counters of finished workgroups (zero between
+// calls) and their partial sums.
 #define GRAD_CHUNK 8192  // elements of one chunk
 struct GradChunk {
   const void* grad;
@@ -213,10 +214,12 @@ struct GradChunk {
 struct GradLaunch {
   const GradChunk* chunks;
   int64_t n_chunks;
+  uint32_t* counters;
   double* partial;
   double max_norm, factor;
   float *norm, *scale;
 };
+int64_t grad_counter_words(int64_t n_chunks);
 int64_t grad_partial_doubles(int64_t n_chunks);
 int launch_grad_norm(const GradLaunch& a, hipStream_t st);
 int launch_grad_clip(const GradLaunch& a, hipStream_t st);

@@ -1,13 +1,22 @@
 // The router's losses, per-expert counts and the gradient of the logits (formulas in include/moe_overlap.h).
+//
+// Bytes bound both at many tokens (logits read once in each, their gradient written), launches and latency at few.  A row is held by
+// L lanes, NV float4 each (L = 16 up to 256 experts: four rows in a wave share its instructions), so its sums are four DPP steps.
+// Forward: one launch.  With P[g] the sum of a sequence's p_g, its part of B is sum over g of f_g P_g, so counts and P can be taken
+// in one pass, before f is known.  Each sequence is cut into parts, a workgroup to a part; the last workgroup of a sequence joins its
+// parts, the last of all the sequences (join.h).
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
+#include "join.h"
 #include "launch.h"
+#include "row_util.h"
 
 namespace {
 
-constexpr int MAX_PER_LANE = 16;  // G <= 1024
-constexpr int MAX_BLOCKS = 1024;
+constexpr int BLOCK = 512, WAVES = BLOCK / 64;
+using std::integral_constant;
 
 // A sequence's rows [first, last), cut to [0, T)
 __device__ __forceinline__ void span_of(const RouterLaunch& a, int s, int* first, int* last) {
@@ -22,208 +31,464 @@ __device__ __forceinline__ void span_of(const RouterLaunch& a, int s, int* first
   *last = min(max(a.spans[2 * (int64_t)s + 1], *first), T);
 }
 
-// The sequence of row t, or -1: the last one that begins at or before it, if it has not ended
-__device__ __forceinline__ int sequence_of(const RouterLaunch& a, int t) {
-  if (!a.spans) return t / ((int)a.tokens / a.sequences);
-  int lo = 0, hi = a.sequences;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (a.spans[2 * (int64_t)mid] <= t) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo > 0 && t < a.spans[2 * (int64_t)(lo - 1) + 1] ? lo - 1 : -1;
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
 
-__device__ __forceinline__ double wave_sum_d(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+// op over the L lanes of a row, in each of them: lane ^ 1, lane ^ 2, then the halves mirrored; beyond 16 lanes by shuffles
+template <int L, class Op>
+__device__ __forceinline__ float over_row(float v, Op op) {
+  v = op(v, dpp<0xB1>(v));
+  v = op(v, dpp<0x4E>(v));
+  if (L >= 16) {
+    v = op(v, dpp<0x141>(v));
+    v = op(v, dpp<0x140>(v));
+  }
+  if (L == 64) {
+    v = op(v, __shfl_xor(v, 16, 64));
+    v = op(v, __shfl_xor(v, 32, 64));
+  }
   return v;
 }
-
-// counts = 0, and (the first workgroup) the sequences with rows and their rows
-__global__ __launch_bounds__(256) void k_router_init(RouterLaunch a) {
-  const int64_t n = (int64_t)a.sequences * a.experts;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) a.counts[i] = 0;
-  if (blockIdx.x > 0) return;
-  __shared__ int red[2][4];
-  int live = 0, rows = 0;
-  for (int s = threadIdx.x; s < a.sequences; s += 256) {
-    int first, last;
-    span_of(a, s, &first, &last);
-    live += last > first;
-    rows += last - first;
-  }
-  live = wave_sum(live);
-  rows = wave_sum(rows);
-  if ((threadIdx.x & 63) == 0) {
-    red[0][threadIdx.x >> 6] = live;
-    red[1][threadIdx.x >> 6] = rows;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) a.means[threadIdx.x] = red[threadIdx.x][0] + red[threadIdx.x][1] + red[threadIdx.x][2] + red[threadIdx.x][3];
+template <int L>
+__device__ __forceinline__ float sum_row(float v) {
+  return over_row<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float max_row(float v) {
+  return over_row<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-__global__ __launch_bounds__(256) void k_router_count(RouterLaunch a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.tokens * a.top_k) return;
-  const int s = sequence_of(a, (int)(i / a.top_k)), id = a.topk_idx[i];
-  if (s >= 0 && id >= 0 && id < a.experts) atomicAdd(&a.counts[(int64_t)s * a.experts + id], 1);
+// Four columns from c on of a row of G, `empty` past it
+__device__ __forceinline__ void load_cols(const float* row, int c, int G, float empty, float* v) {
+  const int n = G - c;
+  const u32x4 q = n > 0 ? Chunk<float>::load(row + c, n) : u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < n ? __uint_as_float(q[i]) : empty;
 }
 
-// A row's probabilities by one wave, logits lane + 64 i in lane: e = exp(l - top), their sum (0: no expert; NaN for a NaN or +inf)
-__device__ __forceinline__ void softmax_row(const RouterLaunch& a, int t, float* e, float* den, float* top) {
-  const int lane = lane_id(), G = a.experts;
-  const float* l = a.logits + (int64_t)t * G;
-  float mx = -INFINITY;
+// A row's e = exp(l - top), their sum (0: no expert, NaN: a NaN or +inf among them) and top; l in e at the call
+template <int L, int E>
+__device__ __forceinline__ void softmax_row(float (&e)[E], float* den, float* top) {
+  float mx = e[0];
 #pragma unroll
-  for (int i = 0; i < MAX_PER_LANE; ++i) {
-    e[i] = lane + 64 * i < G ? l[lane + 64 * i] : -INFINITY;
-    mx = fmaxf(mx, e[i]);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  for (int i = 1; i < E; ++i) mx = fmaxf(mx, e[i]);
+  mx = max_row<L>(mx);
   if (mx == -INFINITY) mx = 0.f;
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < MAX_PER_LANE; ++i) {
-    e[i] = expf(e[i] - mx);
+  for (int i = 0; i < E; ++i) {
+    e[i] = __expf(e[i] - mx);
     sum += e[i];
   }
-  *den = wave_sum_f(sum);
+  *den = sum_row<L>(sum);
   *top = mx;
 }
 
-// f of sequence s
-__device__ __forceinline__ void load_f(const RouterLaunch& a, int s, float* f) {
-  const int lane = lane_id(), G = a.experts;
-  const int32_t* c = a.counts + (int64_t)s * G;
-  float sum = 0.f;
-  int n[MAX_PER_LANE], total = 0;
+// The workgroup's sums of N values in every thread; waves in order
+template <int N>
+__device__ __forceinline__ void block_sums(double (&v)[N], double* red) {
 #pragma unroll
-  for (int i = 0; i < MAX_PER_LANE; ++i) {
-    n[i] = lane + 64 * i < G ? c[lane + 64 * i] : 0;
-    total += n[i];
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor(v[n], o, 64);
+  __syncthreads();  // red may hold the sums before
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int n = 0; n < N; ++n) red[(threadIdx.x >> 6) * N + n] = v[n];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    v[n] = red[n];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v[n] += red[w * N + n];
   }
-  total = wave_sum(total);
-  sum = total > 0 ? (float)G / (float)total : 0.f;
-#pragma unroll
-  for (int i = 0; i < MAX_PER_LANE; ++i) f[i] = (float)n[i] * sum;
 }
 
-__global__ __launch_bounds__(256) void k_router_loss(RouterLaunch a) {
-  const int wave = threadIdx.x >> 6;
-  double balance = 0, z = 0;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.tokens; t += (int64_t)gridDim.x * 4) {
-    const int s = sequence_of(a, (int)t);
-    if (s < 0) continue;
+// Orders the wave's own LDS accesses, which execute in program order, for the compiler
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Parts of a sequence at most: a workgroup for each CU, and no more to join than 32768 columns' sums
+__host__ __device__ inline int most_parts(int experts, int sequences) {
+  const int a = (256 + sequences - 1) / sequences, b = 32768 / (experts < 128 ? 128 : experts);
+  return a < b ? a : b;
+}
+
+// The workspace: counters (zero between calls) of the sequences and of each sequence's parts, each sequence's {B, Z}, then each
+// part's Z, sums of p and counts
+struct Workspace {
+  uint32_t* counters;
+  double *seq, *part_z, *part_p;
+  int32_t* part_n;
+};
+__host__ __device__ inline int64_t counter_words(int experts, int sequences) {
+  return join_words(sequences) + sequences * join_words(most_parts(experts, sequences));
+}
+__host__ __device__ inline Workspace ws_of(void* p, int sequences, int parts, int experts) {
+  Workspace w;
+  w.counters = (uint32_t*)p;
+  w.seq = (double*)(w.counters + counter_words(experts, sequences));
+  w.part_z = w.seq + 2ll * sequences;
+  w.part_p = w.part_z + (int64_t)sequences * parts;
+  w.part_n = (int32_t*)(w.part_p + (int64_t)sequences * parts * experts);
+  return w;
+}
+
+template <int L, int NV>
+__global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts) {
+  constexpr int E = 4 * NV, RW = 64 / L, COLS = L * E;
+  constexpr int SLICES = COLS < BLOCK ? BLOCK / COLS : 1;  // of a sequence's parts, taken by threads of their own
+  constexpr int HELD = COLS <= 512 ? WAVES : WAVES / 2;    // waves whose columns' sums are in LDS at once
+  __shared__ double col[(HELD > SLICES ? HELD : SLICES) * COLS], red[WAVES * 4];
+  __shared__ int32_t hist[COLS], many[SLICES * COLS], flag;
+  const int lane = lane_id(), wave = threadIdx.x >> 6, l = lane % L, sub = lane / L, G = a.experts;
+  const Workspace ws = ws_of(a.workspace, a.sequences, parts, G);
+  for (int64_t u = blockIdx.x; u < (int64_t)a.sequences * parts; u += gridDim.x) {
+    const int s = (int)(u / parts), part = (int)(u % parts);
     int first, last;
     span_of(a, s, &first, &last);
-    float e[MAX_PER_LANE], f[MAX_PER_LANE], den, top, dot = 0.f;
-    softmax_row(a, (int)t, e, &den, &top);
-    if (den == 0.f) continue;
-    load_f(a, s, f);
+    const int len = last - first, from = first + (int)((int64_t)len * part / parts), to = first + (int)((int64_t)len * (part + 1) / parts);
+    // the probabilities; the next rows' loads go out before the current rows' sums
+    double p[E], z = 0;
+    float next[E];
 #pragma unroll
-    for (int i = 0; i < MAX_PER_LANE; ++i) dot = fmaf(e[i], f[i], dot);
-    dot = wave_sum_f(dot);
-    const double lse = top + logf(den);
-    balance += (double)(dot / den) / (double)(last - first);
-    z += lse * lse;
-  }
-  __shared__ double red[2][4];
-  if ((threadIdx.x & 63) == 0) {
-    red[0][wave] = balance;
-    red[1][wave] = z;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    const double* r = red[threadIdx.x];
-    ((double*)a.workspace)[2 * blockIdx.x + threadIdx.x] = r[0] + r[1] + r[2] + r[3];
-  }
-}
-
-__global__ __launch_bounds__(64) void k_router_finish(RouterLaunch a, int n) {
-  const double* p = (const double*)a.workspace;
-  double balance = 0, z = 0;
-  for (int i = threadIdx.x; i < n; i += 64) {
-    balance += p[2 * i];
-    z += p[2 * i + 1];
-  }
-  balance = wave_sum_d(balance) / max(a.means[0], 1);
-  z = wave_sum_d(z) / max(a.means[1], 1);
-  if (threadIdx.x == 0) {
-    a.losses[0] = (float)((double)a.balance * balance + (double)a.z * z);
-    a.losses[1] = (float)balance;
-    a.losses[2] = (float)z;
-  }
-}
-
-__global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a) {
-  const int lane = lane_id(), G = a.experts;
-  const float dl = a.d_loss ? *a.d_loss : 1.f;
-  const float cb = dl * a.balance / (float)max(a.means[0], 1), cz = 2.f * dl * a.z / (float)max(a.means[1], 1);
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.tokens; t += (int64_t)gridDim.x * 4) {
-    const int s = sequence_of(a, (int)t);
-    float o[MAX_PER_LANE];
+    for (int e = 0; e < E; ++e) p[e] = 0;
+    auto fetch = [&](int base) {
+      const int t = min(base + sub, to - 1);
 #pragma unroll
-    for (int i = 0; i < MAX_PER_LANE; ++i) o[i] = 0.f;
-    if (s >= 0) {
-      int first, last;
-      span_of(a, s, &first, &last);
-      float e[MAX_PER_LANE], den, top, dot = 0.f;
-      softmax_row(a, (int)t, e, &den, &top);
-      if (den != 0.f) {
-        load_f(a, s, o);
-        const float share = cb / (float)(last - first), inv = 1.f / den, lse = top + logf(den);
+      for (int j = 0; j < NV; ++j) load_cols(a.logits + (int64_t)t * G, (j * L + l) * 4, G, -INFINITY, next + 4 * j);
+    };
+    int base = from + wave * RW;
+    if (base < to) fetch(base);
+    for (int c = threadIdx.x; c < COLS; c += BLOCK) hist[c] = 0;
+    __syncthreads();
+    // the chosen experts
+    for (int64_t i = (int64_t)from * a.top_k + threadIdx.x; i < (int64_t)to * a.top_k; i += BLOCK) {
+      const int id = a.topk_idx[i];
+      if (id >= 0 && id < G) atomicAdd(&hist[id], 1);
+    }
+    for (; base < to; base += WAVES * RW) {
+      float e[E], den, top;
 #pragma unroll
-        for (int i = 0; i < MAX_PER_LANE; ++i) o[i] *= share;
-        if (a.d_weights)
-          for (int j = 0; j < a.top_k; ++j) {
-            const int id = a.topk_idx[t * a.top_k + j];
-            const float w = a.d_weights[t * a.top_k + j];
+      for (int i = 0; i < E; ++i) e[i] = next[i];
+      if (base + WAVES * RW < to) fetch(base + WAVES * RW);
+      softmax_row<L>(e, &den, &top);
+      if (base + sub < to && den != 0.f) {
+        const float inv = 1.f / den;
+        const double lse = top + logf(den);
 #pragma unroll
-            for (int i = 0; i < MAX_PER_LANE; ++i)
-              if (id == lane + 64 * i && id < G) o[i] += w;
-          }
-#pragma unroll
-        for (int i = 0; i < MAX_PER_LANE; ++i) {
-          e[i] *= inv;
-          dot = fmaf(e[i], o[i], dot);
-        }
-        dot = wave_sum_f(dot);
-#pragma unroll
-        for (int i = 0; i < MAX_PER_LANE; ++i) o[i] = e[i] * (o[i] - dot + cz * lse);
+        for (int i = 0; i < E; ++i) p[i] += e[i] * inv;
+        z += lse * lse;
       }
     }
 #pragma unroll
-    for (int i = 0; i < MAX_PER_LANE; ++i)
-      if (lane + 64 * i < G) {
-        const int64_t at = t * G + lane + 64 * i;
-        if (a.dtype == MOE_F32) ((float*)a.dlogits)[at] = o[i];
-        else ((bf16_t*)a.dlogits)[at] = f32_to_bf16(o[i]);
+    for (int o = L; o < 64; o *= 2)
+#pragma unroll
+      for (int e = 0; e < E; ++e) p[e] += __shfl_xor(p[e], o, 64);
+    if (l != 0) z = 0;  // a row's lanes all hold it
+    // column c's sum and count in thread c (of G > BLOCK also c + BLOCK), the waves in order
+    constexpr int PER = COLS > BLOCK ? COLS / BLOCK : 1;
+    double q[PER];
+    int n[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) q[k] = 0;
+    for (int w0 = 0; w0 < WAVES; w0 += HELD) {
+      if (w0 > 0) __syncthreads();
+      if (sub == 0 && wave >= w0 && wave < w0 + HELD)
+#pragma unroll
+        for (int e = 0; e < E; ++e) col[(wave - w0) * COLS + (e / 4 * L + l) * 4 + e % 4] = p[e];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int c = threadIdx.x + k * BLOCK;
+        if (c < COLS)
+#pragma unroll
+          for (int w = 0; w < HELD; ++w) q[k] += col[w * COLS + c];
       }
+    }
+#pragma unroll
+    for (int k = 0; k < PER; ++k) n[k] = (int)(threadIdx.x + k * BLOCK) < COLS ? hist[threadIdx.x + k * BLOCK] : 0;
+    if (parts > 1) {
+      double v[1] = {z};
+      block_sums(v, red);
+      if (threadIdx.x == 0) hand_out(&ws.part_z[u], v[0]);
+      if (to > from)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+          const int c = threadIdx.x + k * BLOCK;
+          if (c < G) {
+            hand_out(&ws.part_p[u * G + c], q[k]);
+            hand_out(&ws.part_n[u * G + c], n[k]);
+          }
+        }
+      if (!last_of(ws.counters + join_words(a.sequences) + s * join_words(most_parts(G, a.sequences)), part, parts, &flag)) continue;
+      // the parts' sums, in SLICES slices
+      const int slice = SLICES > 1 ? threadIdx.x / COLS : 0, used = min(parts, max(len, 1));
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int c = SLICES > 1 ? threadIdx.x % COLS : threadIdx.x + k * BLOCK;
+        double sum = 0;
+        int count = 0;
+        if (c < G)
+          for (int i = slice; i < parts; i += 8 * SLICES) {
+            double pq[8];
+            int pn[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              const int at = i + m * SLICES;
+              // parts without a row hand nothing out (a sequence of fewer rows than parts)
+              const bool any = at < parts && (used == parts || (int64_t)len * (at + 1) / parts > (int64_t)len * at / parts);
+              pq[m] = any ? take(&ws.part_p[((int64_t)s * parts + at) * G + c]) : 0.;
+              pn[m] = any ? take(&ws.part_n[((int64_t)s * parts + at) * G + c]) : 0;
+            }
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              sum += pq[m];
+              count += pn[m];
+            }
+          }
+        if (SLICES > 1) {
+          col[slice * COLS + c] = sum;
+          many[slice * COLS + c] = count;
+        } else {
+          q[k] = sum;
+          n[k] = count;
+        }
+      }
+      if (SLICES > 1) {
+        __syncthreads();
+        q[0] = 0;
+        n[0] = 0;
+        if (threadIdx.x < COLS)
+#pragma unroll
+          for (int w = 0; w < SLICES; ++w) {
+            q[0] += col[w * COLS + threadIdx.x];
+            n[0] += many[w * COLS + threadIdx.x];
+          }
+      }
+      z = 0;
+      for (int k = threadIdx.x; k < parts; k += BLOCK) z += take(&ws.part_z[(int64_t)s * parts + k]);
+    }
+    // the sequence: its counts, and its parts of B (f_g = G n_g / sum of n) and Z
+    double v[3] = {0, 0, z};
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int c = threadIdx.x + k * BLOCK;
+      if (c < G) {
+        a.counts[(int64_t)s * G + c] = n[k];
+        v[0] += n[k];
+        v[1] += n[k] * q[k];
+      }
+    }
+    block_sums(v, red);
+    const double b = v[0] > 0 && len > 0 ? G / v[0] * v[1] / len : 0.;
+    double t[4] = {(double)(len > 0), (double)len, b, v[2]};  // of the batch: sequences with rows, rows, B, Z
+    if (a.sequences > 1) {
+      if (threadIdx.x == 0) {
+        hand_out(&ws.seq[2 * (int64_t)s], b);
+        hand_out(&ws.seq[2 * (int64_t)s + 1], v[2]);
+      }
+      if (!last_of(ws.counters, s, a.sequences, &flag)) continue;
+      t[0] = t[1] = t[2] = t[3] = 0;
+      for (int k = threadIdx.x; k < a.sequences; k += BLOCK) {
+        int f, e;
+        span_of(a, k, &f, &e);
+        t[0] += e > f;
+        t[1] += e - f;
+        t[2] += take(&ws.seq[2 * (int64_t)k]);
+        t[3] += take(&ws.seq[2 * (int64_t)k + 1]);
+      }
+      block_sums(t, red);
+    }
+    if (threadIdx.x == 0) {
+      const double B = t[2] / fmax(t[0], 1.), Z = t[3] / fmax(t[1], 1.);
+      a.means[0] = (int)t[0];
+      a.means[1] = (int)t[1];
+      a.losses[0] = (float)((double)a.balance * B + (double)a.z * Z);
+      a.losses[1] = (float)B;
+      a.losses[2] = (float)Z;
+    }
   }
 }
 
-int row_blocks(int64_t tokens) { return (int)std::min<int64_t>((tokens + 3) / 4, MAX_BLOCKS); }
+// The gradient.  A wave takes `rows` rows in a row, so that it meets few sequences: f of the last one stays in registers
+template <int L, int NV, class O>
+__global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a, int rows) {
+  constexpr int E = 4 * NV, RW = 64 / L, COLS = L * E;
+  constexpr bool BY_LDS = NV > 1;  // where a row's slots' gradients find their columns: in LDS, or by comparing
+  __shared__ float slots[BY_LDS ? 4 * RW * COLS : 1];
+  const int lane = lane_id(), wave = threadIdx.x >> 6, l = lane % L, sub = lane / L, G = a.experts, K = a.top_k;
+  float* mine = slots + (BY_LDS ? (wave * RW + sub) * COLS : 0);
+  if (BY_LDS) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) *(float4*)(mine + (j * L + l) * 4) = float4{0, 0, 0, 0};
+    wave_order();
+  }
+  const float dl = a.d_loss ? *a.d_loss : 1.f;
+  const float cb = dl * a.balance / (float)max(a.means[0], 1), cz = 2.f * dl * a.z / (float)max(a.means[1], 1);
+  const int64_t begin = ((int64_t)blockIdx.x * 4 + wave) * rows, end = min(begin + rows, a.tokens);
+  int first = 0, last = 0;  // of the sequence whose f is held
+  bool found = false;
+  float f[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) f[i] = 0.f;
+  for (int64_t base = begin; base < end; base += RW) {
+    const int t = (int)min(base + sub, end - 1);  // rows past the end: the last one again, not stored
+    const bool live = base + sub < end;
+    float e[E], den, top, g[E];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load_cols(a.logits + (int64_t)t * G, (j * L + l) * 4, G, -INFINITY, e + 4 * j);
+    if (__ballot(!found || t < first || t >= last)) {
+      // the last sequence that begins at or before t; what lies between it and the next one is padding
+      int s;
+      if (!a.spans) s = t / ((int)a.tokens / a.sequences);
+      else {
+        int lo = 0, hi = a.sequences;
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (a.spans[2 * (int64_t)mid] <= t) lo = mid + 1;
+          else hi = mid;
+        }
+        s = lo - 1;
+      }
+      first = 0;
+      last = 0;
+      if (s >= 0) span_of(a, s, &first, &last);
+      found = true;
+      const int32_t* n = a.counts + (int64_t)max(s, 0) * G;
+      float total = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = (j * L + l) * 4 + i;
+          const int v = c < G ? n[c] : 0;
+          f[4 * j + i] = (float)v;
+          total += (float)v;
+        }
+      total = sum_row<L>(total);
+      const float share = total > 0.f && last > first ? cb / (float)(last - first) * ((float)G / total) : 0.f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) f[i] *= share;
+    }
+    const bool inside = t >= first && t < last;
+    softmax_row<L>(e, &den, &top);
+#pragma unroll
+    for (int i = 0; i < E; ++i) g[i] = f[i];
+    if (a.d_weights) {
+      const int64_t at = (int64_t)t * K;
+      if (BY_LDS) {
+        const int id = l < K ? a.topk_idx[at + l] : -1;
+        const float w = l < K ? a.d_weights[at + l] : 0.f;
+        const bool good = id >= 0 && id < G;
+        for (int j = 0; j < K; ++j)
+          if (l == j && good) mine[id] += w;
+        wave_order();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const float4 q = *(const float4*)(mine + (j * L + l) * 4);
+          g[4 * j] += q.x;
+          g[4 * j + 1] += q.y;
+          g[4 * j + 2] += q.z;
+          g[4 * j + 3] += q.w;
+        }
+        wave_order();
+        if (good) mine[id] = 0.f;
+        wave_order();
+      } else {
+        float q[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) q[i] = 0.f;
+        for (int j = 0; j < K; ++j) {
+          const int id = a.topk_idx[at + j];
+          const float w = a.d_weights[at + j];
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            if (id == l * 4 + i && id < G) q[i] += w;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) g[i] += q[i];
+      }
+    }
+    const bool none = !inside || den == 0.f;
+    const float inv = 1.f / den, lse = top + logf(den);
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      e[i] *= inv;
+      dot = fmaf(e[i], g[i], dot);
+    }
+    dot = sum_row<L>(dot);
+    const float off = fmaf(cz, lse, -dot);
+#pragma unroll
+    for (int i = 0; i < E; ++i) g[i] = none ? 0.f : e[i] * (g[i] + off);
+    if (!live) continue;
+    O* out = (O*)a.dlogits + (int64_t)t * G;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * L + l) * 4, n = G - c;
+      const float* v = g + 4 * j;
+      if constexpr (sizeof(O) == 4) {
+        if (n > 0) Chunk<float>::store((float*)out + c, Chunk<float>::pack(v), n);
+      } else if (n >= 4) {
+        const uint32_t q[2] = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        __builtin_memcpy(out + c, q, 8);
+      } else
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < n) out[c + i] = f32_to_bf16(v[i]);
+    }
+  }
+}
+
+// Lanes to a row and float4 in each: the fewest lanes that hold it in four, from quads on
+template <class F>
+void by_width(int G, F f) {
+  if (G <= 16) f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (G <= 64) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (G <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  else if (G <= 256) f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  else if (G <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+
+// Parts of a sequence, two rounds of a workgroup's rows in each at least
+int parts_of(int64_t tokens, int experts, int sequences) {
+  const int64_t rows = WAVES * (experts <= 16 ? 16 : experts <= 256 ? 4 : 1) * 2;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most_parts(experts, sequences), tokens / sequences / rows));
+}
 
 }  // namespace
 
-int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences) { return 16ll * MAX_BLOCKS; }
+int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences) {
+  const int64_t units = (int64_t)sequences * parts_of(tokens, experts, sequences);
+  return 4 * counter_words(experts, sequences) + 16ll * sequences + units * (8 + 12ll * experts);
+}
 
 int launch_router_loss(const RouterLaunch& a, hipStream_t st) {
-  const int64_t cells = (int64_t)a.sequences * a.experts, slots = a.tokens * a.top_k;
-  const int blocks = row_blocks(a.tokens);
-  hipLaunchKernelGGL(k_router_init, dim3((unsigned)std::min<int64_t>((cells + 255) / 256, 1024)), dim3(256), 0, st, a);
-  if (a.tokens > 0) {
-    hipLaunchKernelGGL(k_router_count, dim3((unsigned)((slots + 255) / 256)), dim3(256), 0, st, a);
-    hipLaunchKernelGGL(k_router_loss, dim3(blocks), dim3(256), 0, st, a);
-  }
-  hipLaunchKernelGGL(k_router_finish, dim3(1), dim3(64), 0, st, a, blocks);
+  const int parts = parts_of(a.tokens, a.experts, a.sequences);
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.sequences * parts, 1 << 16));
+  by_width(a.experts, [&](auto l, auto nv) {
+    hipLaunchKernelGGL((k_router_loss<decltype(l)::value, decltype(nv)::value>), grid, dim3(BLOCK), 0, st, a, parts);
+  });
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_router_backward(const RouterLaunch& a, hipStream_t st) {
   if (a.tokens == 0) return 0;
-  hipLaunchKernelGGL(k_router_bwd, dim3(row_blocks(a.tokens)), dim3(256), 0, st, a);
+  by_width(a.experts, [&](auto l, auto nv) {
+    constexpr int L = decltype(l)::value, NV = decltype(nv)::value, RW = 64 / L;
+    // as many rows to a wave as leave each SIMD four waves
+    const int64_t most = std::max<int64_t>(8, a.tokens >> 24);  // and few enough workgroups for a launch
+    const int rows = (int)std::min<int64_t>(std::max<int64_t>((a.tokens + 4096 * RW - 1) / (4096 * RW), 1), most) * RW;
+    const dim3 grid((unsigned)((a.tokens + 4 * rows - 1) / (4 * rows)));
+    if (a.dtype == MOE_F32) hipLaunchKernelGGL((k_router_bwd<L, NV, float>), grid, dim3(256), 0, st, a, rows);
+    else hipLaunchKernelGGL((k_router_bwd<L, NV, bf16_t>), grid, dim3(256), 0, st, a, rows);
+  });
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

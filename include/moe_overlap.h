@@ -608,8 +608,9 @@ typedef struct {
   float balance, z;   /* the losses' coefficients, finite */
 } moe_router_shape;
 
-/* Bytes of the workspace of moe_router_loss; -1 for an invalid shape.  It needs no initial contents; calls that may run at the
- * same time need one each. */
+/* Bytes of the workspace of moe_router_loss (partial sums, and the counters of finished workgroups); -1 for an invalid shape.  Zero it
+ * once before its first call; each call leaves it ready for the next, of any fewer tokens too.  Calls that may run at the same time need
+ * one each. */
 int64_t moe_router_loss_workspace_bytes(const moe_router_shape* s);
 
 /* logits (device) fp32 [T, G]; topk_idx (device) int32 [T, k]; spans (device) int32 [S][2], each sequence's first row and the row

@@ -117,8 +117,9 @@ def router_loss(logits, idx, sequences, balance, z, spans=None, d_weights=None, 
     e = torch.exp(l - top)
     den = e.sum(1, keepdim=True)
     p = torch.where(gone[:, None], 0.0, e / den)
-    # exp of a rounded difference (once more rounded to another base), within 2 steps; sums of at most 16 + 6 terms
-    rel = torch.where(torch.isinf(l), 0.0, E32 * (2 * (l - top).abs() + 6))
+    # exp(x) as 2^(x log2 e): x is a rounded difference, its product is rounded, log2 e in fp32 is off by 0.22 E32 of it, together
+    # 2.25 E32 |x| of the result; the power itself within 2 steps of 2 E32 each; sums of at most 16 + 6 terms
+    rel = torch.where(torch.isinf(l), 0.0, E32 * (2.25 * (l - top).abs() + 6))
     rel_den = (p * rel).sum(1, keepdim=True) + 24 * E32
     rel_p = rel + rel_den + 2 * E32
     lse = torch.where(gone[:, None], 0.0, top + torch.log(den))
