@@ -113,29 +113,35 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Parts of a sequence at most: a workgroup for each CU, and no more to join than 32768 columns' sums
-__host__ __device__ inline int most_parts(int experts, int sequences) {
-  const int a = (256 + sequences - 1) / sequences, b = 32768 / (experts < 128 ? 128 : experts);
-  return a < b ? a : b;
-}
+// Parts of a sequence at most: a workgroup for each CU.  Up to DIRECT of them are joined by the last one; of more, each GROUP by its
+// last, and the groups by theirs
+constexpr int DIRECT = 32, GROUP = 16;
+__host__ __device__ inline int most_parts(int sequences) { return (256 + sequences - 1) / sequences; }
+__host__ __device__ inline int groups_of(int parts) { return parts > DIRECT ? (parts + GROUP - 1) / GROUP : 0; }
 
-// The workspace: counters (zero between calls) of the sequences and of each sequence's parts, each sequence's {B, Z}, then each
-// part's Z, sums of p and counts
+// The workspace: counters (zero between calls) of the sequences and of each sequence's groups and parts, each sequence's {B, Z}, then
+// each part's Z, and sums of p and counts of the parts and of the groups
 struct Workspace {
-  uint32_t* counters;
-  double *seq, *part_z, *part_p;
-  int32_t* part_n;
+  uint32_t *counters, *part_counters;
+  double *seq, *part_z, *part_p, *group_p;
+  int32_t *part_n, *group_n;
 };
-__host__ __device__ inline int64_t counter_words(int experts, int sequences) {
-  return join_words(sequences) + sequences * join_words(most_parts(experts, sequences));
+__host__ __device__ inline int64_t seq_counter_words(int sequences) {
+  const int most = most_parts(sequences);
+  return most > 1 ? JOIN_STRIDE * (1 + groups_of(most)) : 0;
 }
-__host__ __device__ inline Workspace ws_of(void* p, int sequences, int parts, int experts) {
+__host__ __device__ inline int64_t counter_words(int sequences) { return join_words(sequences) + sequences * seq_counter_words(sequences); }
+__host__ __device__ inline Workspace ws_of(void* p, int64_t sequences, int parts, int experts) {
   Workspace w;
+  const int64_t groups = groups_of(parts);
   w.counters = (uint32_t*)p;
-  w.seq = (double*)(w.counters + counter_words(experts, sequences));
-  w.part_z = w.seq + 2ll * sequences;
-  w.part_p = w.part_z + (int64_t)sequences * parts;
-  w.part_n = (int32_t*)(w.part_p + (int64_t)sequences * parts * experts);
+  w.part_counters = w.counters + join_words(sequences);
+  w.seq = (double*)(w.counters + counter_words((int)sequences));
+  w.part_z = w.seq + 2 * sequences;
+  w.part_p = w.part_z + sequences * parts;
+  w.group_p = w.part_p + sequences * parts * experts;
+  w.part_n = (int32_t*)(w.group_p + sequences * groups * experts);
+  w.group_n = w.part_n + sequences * parts * experts;
   return w;
 }
 
@@ -150,35 +156,35 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
   const Workspace ws = ws_of(a.workspace, a.sequences, parts, G);
   for (int64_t u = blockIdx.x; u < (int64_t)a.sequences * parts; u += gridDim.x) {
     const int s = (int)(u / parts), part = (int)(u % parts);
-    int first, last;
-    span_of(a, s, &first, &last);
-    const int len = last - first, from = first + (int)((int64_t)len * part / parts), to = first + (int)((int64_t)len * (part + 1) / parts);
+    int first, end;
+    span_of(a, s, &first, &end);
+    const int len = end - first, r0 = first + (int)((int64_t)len * part / parts), r1 = first + (int)((int64_t)len * (part + 1) / parts);
     // the probabilities; the next rows' loads go out before the current rows' sums
     double p[E], z = 0;
     float next[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) p[e] = 0;
     auto fetch = [&](int base) {
-      const int t = min(base + sub, to - 1);
+      const int t = min(base + sub, r1 - 1);
 #pragma unroll
       for (int j = 0; j < NV; ++j) load_cols(a.logits + (int64_t)t * G, (j * L + l) * 4, G, -INFINITY, next + 4 * j);
     };
-    int base = from + wave * RW;
-    if (base < to) fetch(base);
+    int base = r0 + wave * RW;
+    if (base < r1) fetch(base);
     for (int c = threadIdx.x; c < COLS; c += BLOCK) hist[c] = 0;
     __syncthreads();
     // the chosen experts
-    for (int64_t i = (int64_t)from * a.top_k + threadIdx.x; i < (int64_t)to * a.top_k; i += BLOCK) {
+    for (int64_t i = (int64_t)r0 * a.top_k + threadIdx.x; i < (int64_t)r1 * a.top_k; i += BLOCK) {
       const int id = a.topk_idx[i];
       if (id >= 0 && id < G) atomicAdd(&hist[id], 1);
     }
-    for (; base < to; base += WAVES * RW) {
+    for (; base < r1; base += WAVES * RW) {
       float e[E], den, top;
 #pragma unroll
       for (int i = 0; i < E; ++i) e[i] = next[i];
-      if (base + WAVES * RW < to) fetch(base + WAVES * RW);
+      if (base + WAVES * RW < r1) fetch(base + WAVES * RW);
       softmax_row<L>(e, &den, &top);
-      if (base + sub < to && den != 0.f) {
+      if (base + sub < r1 && den != 0.f) {
         const float inv = 1.f / den;
         const double lse = top + logf(den);
 #pragma unroll
@@ -217,60 +223,76 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
       double v[1] = {z};
       block_sums(v, red);
       if (threadIdx.x == 0) hand_out(&ws.part_z[u], v[0]);
-      if (to > from)
+      // to the last of the parts, or of a group of them and on to the last of the groups
+      const int groups = groups_of(parts), group = part / GROUP;
+      uint32_t* counters = ws.part_counters + s * seq_counter_words(a.sequences);
+      double* to_p = ws.part_p + (int64_t)s * parts * G;
+      int32_t* to_n = ws.part_n + (int64_t)s * parts * G;
+      int place = part, from = groups > 0 ? group * GROUP : 0, count = groups > 0 ? min(GROUP, parts - from) : parts;
+      uint32_t* counter = groups > 0 ? counters + (1 + group) * JOIN_STRIDE : counters;
+      bool last;
+#pragma unroll 1
+      for (int level = groups > 0 ? 0 : 1; level < 2; ++level) {
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
           const int c = threadIdx.x + k * BLOCK;
           if (c < G) {
-            hand_out(&ws.part_p[u * G + c], q[k]);
-            hand_out(&ws.part_n[u * G + c], n[k]);
+            hand_out(&to_p[(int64_t)place * G + c], q[k]);
+            hand_out(&to_n[(int64_t)place * G + c], n[k]);
           }
         }
-      if (!last_of(ws.counters + join_words(a.sequences) + s * join_words(most_parts(G, a.sequences)), part, parts, &flag)) continue;
-      // the parts' sums, in SLICES slices
-      const int slice = SLICES > 1 ? threadIdx.x / COLS : 0, used = min(parts, max(len, 1));
+        last = last_of(counter, 0, count, &flag);
+        if (!last) break;
+        const int slice = SLICES > 1 ? threadIdx.x / COLS : 0;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const int c = SLICES > 1 ? threadIdx.x % COLS : threadIdx.x + k * BLOCK;
-        double sum = 0;
-        int count = 0;
-        if (c < G)
-          for (int i = slice; i < parts; i += 8 * SLICES) {
-            double pq[8];
-            int pn[8];
+        for (int k = 0; k < PER; ++k) {
+          const int c = SLICES > 1 ? threadIdx.x % COLS : threadIdx.x + k * BLOCK;
+          double sum = 0;
+          int total = 0;
+          if (c < G)
+#pragma unroll 1
+            for (int i = slice; i < count; i += 8 * SLICES) {
+              double pq[8];
+              int pn[8];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              const int at = i + m * SLICES;
-              // parts without a row hand nothing out (a sequence of fewer rows than parts)
-              const bool any = at < parts && (used == parts || (int64_t)len * (at + 1) / parts > (int64_t)len * at / parts);
-              pq[m] = any ? take(&ws.part_p[((int64_t)s * parts + at) * G + c]) : 0.;
-              pn[m] = any ? take(&ws.part_n[((int64_t)s * parts + at) * G + c]) : 0;
+              for (int m = 0; m < 8; ++m) {
+                const int at = i + m * SLICES;
+                pq[m] = at < count ? take(&to_p[(int64_t)(from + at) * G + c]) : 0.;
+                pn[m] = at < count ? take(&to_n[(int64_t)(from + at) * G + c]) : 0;
+              }
+#pragma unroll
+              for (int m = 0; m < 8; ++m) {
+                sum += pq[m];
+                total += pn[m];
+              }
             }
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-              sum += pq[m];
-              count += pn[m];
-            }
+          if (SLICES > 1) {
+            col[slice * COLS + c] = sum;
+            many[slice * COLS + c] = total;
+          } else {
+            q[k] = sum;
+            n[k] = total;
           }
+        }
         if (SLICES > 1) {
-          col[slice * COLS + c] = sum;
-          many[slice * COLS + c] = count;
-        } else {
-          q[k] = sum;
-          n[k] = count;
-        }
-      }
-      if (SLICES > 1) {
-        __syncthreads();
-        q[0] = 0;
-        n[0] = 0;
-        if (threadIdx.x < COLS)
+          __syncthreads();
+          q[0] = 0;
+          n[0] = 0;
+          if (threadIdx.x < COLS)
 #pragma unroll
-          for (int w = 0; w < SLICES; ++w) {
-            q[0] += col[w * COLS + threadIdx.x];
-            n[0] += many[w * COLS + threadIdx.x];
-          }
+            for (int w = 0; w < SLICES; ++w) {
+              q[0] += col[w * COLS + threadIdx.x];
+              n[0] += many[w * COLS + threadIdx.x];
+            }
+        }
+        to_p = ws.group_p + (int64_t)s * groups * G;
+        to_n = ws.group_n + (int64_t)s * groups * G;
+        place = group;
+        from = 0;
+        count = groups;
+        counter = counters;
       }
+      if (!last) continue;
       z = 0;
       for (int k = threadIdx.x; k < parts; k += BLOCK) z += take(&ws.part_z[(int64_t)s * parts + k]);
     }
@@ -460,14 +482,14 @@ void by_width(int G, F f) {
 // Parts of a sequence, two rounds of a workgroup's rows in each at least
 int parts_of(int64_t tokens, int experts, int sequences) {
   const int64_t rows = WAVES * (experts <= 16 ? 16 : experts <= 256 ? 4 : 1) * 2;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most_parts(experts, sequences), tokens / sequences / rows));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most_parts(sequences), tokens / sequences / rows));
 }
 
 }  // namespace
 
 int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences) {
-  const int64_t units = (int64_t)sequences * parts_of(tokens, experts, sequences);
-  return 4 * counter_words(experts, sequences) + 16ll * sequences + units * (8 + 12ll * experts);
+  const int parts = parts_of(tokens, experts, sequences);
+  return 4 * counter_words(sequences) + sequences * (16 + parts * 8ll + (parts + groups_of(parts)) * 12ll * experts);
 }
 
 int launch_router_loss(const RouterLaunch& a, hipStream_t st) {
