@@ -19,7 +19,7 @@ template <typename T>
 __device__ __forceinline__ void squares(const GradChunk& k, double (&s)[2]) {
   using K = Chunk<T>;
   constexpr int C = K::C, STEPS = GRAD_CHUNK / C / 256;
-  const T* g = (const T*)(__attribute__((address_space(1))) const T*)k.grad;
+  const T* g = (const T*)(__attribute__((address_space(1))) const T*)(uintptr_t)k.grad;
   u32x4 v[STEPS];
   if (k.n == GRAD_CHUNK) {
 #pragma unroll
@@ -74,12 +74,22 @@ __global__ __launch_bounds__(256) void k_grad_norm(GradLaunch a) {
   *a.scale = (float)(a.factor * (isinf(a.max_norm) || ratio >= 1 ? 1.0 : ratio));
 }
 
+// N bytes at any address, past the caches
+template <int N>
+__device__ __forceinline__ void put(void* to, const void* from) {
+  typedef uint32_t V __attribute__((ext_vector_type(N / 4 < 4 ? N / 4 : 4), aligned(2)));
+  V v[N / sizeof(V)];
+  __builtin_memcpy(v, from, N);
+#pragma unroll
+  for (int i = 0; i < (int)(N / sizeof(V)); ++i) __builtin_nontemporal_store(v[i], (V*)to + i);
+}
+
 template <typename T, typename O>
 __device__ __forceinline__ void scaled(const GradChunk& k, void* to, float f) {
   using K = Chunk<T>;
   constexpr int C = K::C, STEPS = GRAD_CHUNK / C / 256;
-  const T* g = (const T*)(__attribute__((address_space(1))) const T*)k.grad;
-  O* out = (O*)(__attribute__((address_space(1))) O*)to;
+  const T* g = (const T*)(__attribute__((address_space(1))) const T*)(uintptr_t)k.grad;
+  O* out = (O*)(__attribute__((address_space(1))) O*)(uintptr_t)to;
   u32x4 v[STEPS];
 #pragma unroll
   for (int j = 0; j < STEPS; ++j) {
@@ -100,12 +110,12 @@ __device__ __forceinline__ void scaled(const GradChunk& k, void* to, float f) {
           if constexpr (sizeof(O) == 4) out[at + i] = w[i];
           else out[at + i] = f32_to_bf16(w[i]);
         }
-    } else if constexpr (sizeof(O) == 4) __builtin_memcpy(out + at, w, 4 * C);
+    } else if constexpr (sizeof(O) == 4) put<4 * C>(out + at, w);
     else {
       uint32_t q[C / 2];
 #pragma unroll
       for (int i = 0; i < C / 2; ++i) q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i + 1]) << 16);
-      __builtin_memcpy(out + at, q, 2 * C);
+      put<2 * C>(out + at, q);
     }
   }
 }
