@@ -39,10 +39,10 @@ __device__ __forceinline__ void post_chunk(const ResidualLaunch& a, bool bf16, i
   }
 }
 
-// A row's statistics over the G threads that hold it; at(e): its element e of NV chunks of C, 0 past the row.  turn picks the one
+// A row's statistics over the G threads that hold it; chunk(j, v): its chunk j of NV, of C elements, 0 past the row.  turn picks the one
 // of red's two halves that the last sum did not use
-template <int G, int NV, int C, class At>
-__device__ __forceinline__ void row_stats(At at, int kind, int t, int d, float eps, float (*red)[2 * (G / 64)], int& turn,
+template <int G, int NV, int C, bool TAIL, class Get>
+__device__ __forceinline__ void row_stats(Get chunk, int kind, int t, int d, float eps, float (*red)[2 * (G / 64) + 1], int& turn,
                                           float* mean_out, float* rstd_out) {
   if (kind == MOE_NORM_NONE) {
     *mean_out = 0.f;
@@ -53,21 +53,29 @@ __device__ __forceinline__ void row_stats(At at, int kind, int t, int d, float e
   if (kind == MOE_NORM_LAYER) {
     float s[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < NV * C; ++e) s[0] += at(e);
+    for (int j = 0; j < NV; ++j) {
+      float v[C];
+      chunk(j, v);
+#pragma unroll
+      for (int i = 0; i < C; ++i) s[0] += v[i];
+    }
     group_total<G>(s, red[turn]);
     turn ^= 1;
     mean = s[0] / d;
     float q[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      float v[C];
+      chunk(j, v);
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const float e = at(j * C + i) - mean;
-        if ((j * G + t) * C + i < d) {
+        const float e = v[i] - mean;
+        if ((j * G + t) * C + (TAIL ? i : 0) < d) {
           q[0] = fmaf(e, e, q[0]);
           q[1] += e;
         }
       }
+    }
     group_total<G>(q, red[turn]);
     turn ^= 1;
     off = q[1] / d;  // the differences' own sum corrects the mean's rounding
@@ -76,7 +84,12 @@ __device__ __forceinline__ void row_stats(At at, int kind, int t, int d, float e
   } else {
     float q[1] = {0.f};
 #pragma unroll
-    for (int e = 0; e < NV * C; ++e) q[0] = fmaf(at(e), at(e), q[0]);
+    for (int j = 0; j < NV; ++j) {
+      float v[C];
+      chunk(j, v);
+#pragma unroll
+      for (int i = 0; i < C; ++i) q[0] = fmaf(v[i], v[i], q[0]);
+    }
     group_total<G>(q, red[turn]);
     turn ^= 1;
     *rstd_out = 1.0f / sqrtf(q[0] / d + eps);
@@ -94,6 +107,31 @@ struct Rows {
     if ((int)c >= d) return u32x4{0, 0, 0, 0};
     return TAIL ? K::load(p, d - (int)c) : load16(p);
   }
+  // The same without waiting for single elements' loads, for rows that are fetched ahead: a row's last chunk comes as its last 16 bytes,
+  // and settle moves them to their places
+  template <bool TINY>  // rows may be shorter than a chunk
+  static __device__ __forceinline__ u32x4 load_ahead(const T* row, uint32_t c, int d) {
+    const T* p = (const T*)((const char*)row + c * (uint32_t)sizeof(T));
+    if ((int)c >= d) return u32x4{0, 0, 0, 0};
+    if (!TAIL) return load16(p);
+    if (TINY && d < K::C) return K::load(p, d - (int)c);
+    return load16(p - max((int)c + K::C - d, 0));
+  }
+  // `end`: the column behind the G chunks that c's is one of
+  template <bool TINY>
+  static __device__ __forceinline__ void settle(u32x4& v, uint32_t c, int end, int d) {
+    if (!TAIL || end <= d || (TINY && d < K::C)) return;
+    const int over = (int)c < d ? max((int)c + K::C - d, 0) : 0, bits = over * (int)sizeof(T) * 8;
+    if (__ballot(over > 0) == 0) return;
+    const uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    const uint64_t a = bits >= 64 ? hi >> (bits & 63) : bits ? lo >> bits | hi << (64 - bits) : lo, b = bits >= 64 ? 0 : hi >> bits;
+    v = u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  }
+  template <int G, int NV>
+  static __device__ __forceinline__ void settle_all(int t, int d, u32x4* v) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) settle<G == 16>(v[j], (uint32_t)(j * G + t) * K::C, (j + 1) * G * K::C, d);
+  }
   static __device__ __forceinline__ void store(T* row, uint32_t c, int d, const float* f) {
     T* p = (T*)((char*)row + c * (uint32_t)sizeof(T));
     if ((int)c >= d) return;
@@ -110,10 +148,13 @@ struct Rows {
     }
     return v;
   }
-  template <int G, int NV>
+  template <int G, int NV, bool LATE = false>
   static __device__ __forceinline__ void load_all(const void* base, int64_t row, int64_t stride, int t, int d, u32x4* v) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = load((const T*)base + row * stride, (uint32_t)(j * G + t) * K::C, d);
+    for (int j = 0; j < NV; ++j) {
+      const T* p = (const T*)base + row * stride;
+      v[j] = LATE ? load_ahead<G == 16>(p, (uint32_t)(j * G + t) * K::C, d) : load(p, (uint32_t)(j * G + t) * K::C, d);
+    }
   }
 };
 
@@ -124,7 +165,7 @@ __device__ __forceinline__ void forget(u32x4& v) { asm volatile("" : "+v"(v)); }
 // The wave's number in the workgroup, as a number of the wave's
 __device__ __forceinline__ int wave_of() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// Forward.  SHARED: the parameters in LDS, once for all rows of the workgroup's eight waves, which hold a row each (G = 64: no
+// Forward.  SHARED: the parameters in LDS, once for all rows of the workgroup's eight waves, which hold a row or more each (G <= 64: no
 // barrier); else read for each row, as where there are few rows or wide ones.
 template <typename T, int G, int NV, bool SHARED, bool TAIL>
 __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a) {
@@ -132,11 +173,11 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
   using R = Rows<T, TAIL>;
   constexpr int C = K::C, PER = SHARED ? 512 / G : 1, E = NV * C;
   extern __shared__ float shared[];  // SHARED: A, pre_weight, then B and pre_bias where there is a bias; by four columns, then lanes
-  __shared__ float red[2][2 * (G / 64)];
+  __shared__ float red[2][2 * (G / 64) + 1];
   const int t = threadIdx.x % G, d = a.d;
   const bool pb = a.param_dtype == MOE_BF16, bias = a.p.post_bias || a.p.pre_bias;
   if (SHARED) {
-    for (int c = threadIdx.x; c < NV * 64; c += 512) {
+    for (int c = threadIdx.x; c < NV * G; c += 512) {
       float v[4][C];
       post_chunk<C>(a, pb, c * C, v[0], v[2]);
       param_chunk<C>(a.p.pre_weight, pb, c * C, d, 1.f, v[1]);
@@ -146,19 +187,20 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
         if (k < 2 || bias)
 #pragma unroll
           for (int q = 0; q < C / 4; ++q)
-            *(float4*)(shared + k * E * 64 + ((c / 64 * (C / 4) + q) * 64 + c % 64) * 4) =
+            *(float4*)(shared + k * E * G + ((c / G * (C / 4) + q) * G + c % G) * 4) =
                 float4{v[k][4 * q], v[k][4 * q + 1], v[k][4 * q + 2], v[k][4 * q + 3]};
     }
     __syncthreads();
   }
+  int here = t;  // a new number to the compiler for each row: else it would keep all of LDS in registers
   // chunk j of weight (0: A, 1: pre_weight) and of its bias
   auto weights = [&](int which, int j, float* w, float* b) {
     if (SHARED) {
 #pragma unroll
       for (int q = 0; q < C / 4; ++q) {
-        const int at = ((j * (C / 4) + q) * 64 + t) * 4;
-        *(float4*)(w + 4 * q) = *(const float4*)(shared + which * E * 64 + at);
-        if (bias) *(float4*)(b + 4 * q) = *(const float4*)(shared + (2 + which) * E * 64 + at);
+        const int at = ((j * (C / 4) + q) * G + here) * 4;
+        *(float4*)(w + 4 * q) = *(const float4*)(shared + which * E * G + at);
+        if (bias) *(float4*)(b + 4 * q) = *(const float4*)(shared + (2 + which) * E * G + at);
         else *(float4*)(b + 4 * q) = float4{0, 0, 0, 0};
       }
     } else if (which == 0) post_chunk<C>(a, pb, (j * G + t) * C, w, b);
@@ -168,13 +210,20 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
     }
   };
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * PER + (SHARED ? wave_of() : 0); r < a.rows; r += (int64_t)gridDim.x * PER) {
+  for (int64_t r = (int64_t)blockIdx.x * PER + (G < 64 ? threadIdx.x / G : SHARED ? wave_of() : 0); r < a.rows; r += (int64_t)gridDim.x * PER) {
     u32x4 h[NV], x[NV];
+    if (SHARED) asm volatile("" : "+v"(here));
     R::template load_all<G, NV>(a.h, r, a.h_stride, t, d, h);
     R::template load_all<G, NV>(a.x, r, a.x_stride, t, d, x);
     const float c = a.p.row_gate ? a.p.row_gate[r] : 1.f;
     float m1, r1, m2, r2, s[E];
-    row_stats<G, NV, C>([&](int e) { return K::at(h[e / C], e % C); }, a.post, t, d, a.eps, red, turn, &m1, &r1);
+    auto of_h = [&](int j, float* v) {
+      if (sizeof(T) == 2) forget(h[j]);
+      if (NV > 4) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = K::at(h[j], i);
+    };
+    row_stats<G, NV, C, TAIL>(of_h, a.post, t, d, a.eps, red, turn, &m1, &r1);
     T* to = (T*)a.s + r * a.s_stride;
     const float o1 = -m1 * r1;
 #pragma unroll
@@ -192,7 +241,11 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
       }
       R::store(to, at, d, s + j * C);
     }
-    row_stats<G, NV, C>([&](int e) { return s[e]; }, a.pre, t, d, a.eps, red, turn, &m2, &r2);
+    auto of_s = [&](int j, float* v) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = s[j * C + i];
+    };
+    row_stats<G, NV, C, TAIL>(of_s, a.pre, t, d, a.eps, red, turn, &m2, &r2);
     if (a.pre != MOE_NORM_NONE) {
       to = (T*)a.n + r * a.n_stride;
       const float o2 = -m2 * r2;
@@ -211,45 +264,62 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
   }
 }
 
-// dx and dh of a group's rows, and its sums of c D h^ and dn s^ (BIAS: also of c D and dn), which stay in registers over all of its
-// rows and go to the workspace at the end: partial [workgroup][2 or 4][d].
-template <typename T, int G, int NV, bool BIAS, bool TAIL>
-__global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaunch a) {
+// dx and dh of a group's rows, and its sums of c D h^ and dn s^ (SUMS = 4: also of c D and dn), which stay in registers over all of its
+// rows, as the parameters do, and go to the workspace at the end: partial [workgroup][SUMS][d].  WIDE, where registers do not hold all
+// that: the first two sums are in LDS, each thread's for itself, and the parameters are read (from the L2) for each row.
+template <typename T, int G, int NV, int SUMS, bool WIDE, bool TAIL>
+__global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaunch a) {
   using K = Chunk<T>;
   using R = Rows<T, TAIL>;
-  constexpr int C = K::C, PER = G == 64 ? 4 : 1, E = NV * C, SUMS = BIAS ? 4 : 2;
-  __shared__ float red[2][3 * (G / 64)];
+  constexpr int C = K::C, PER = G <= 64 ? 256 / G : 1, E = NV * C, HELD = WIDE ? C : E, REGS = WIDE ? SUMS - 2 : SUMS;
+  constexpr bool BIAS = SUMS == 4, AHEAD = !WIDE;  // AHEAD: registers hold the next row too
+  extern __shared__ float sums[];  // WIDE: [2][E][G]
+  __shared__ float red[2][3 * (G / 64) + 1];
   __shared__ float join[PER > 1 ? (PER - 1) * SUMS * E * G : 1];
   const int t = threadIdx.x % G, d = a.d;
   const bool pb = a.param_dtype == MOE_BF16, pre = a.pre != MOE_NORM_NONE;
-  float acc[SUMS][E], A[E], B[E], W[E];
+  float acc[REGS > 0 ? REGS : 1][E], A[HELD], B[HELD], W[HELD];
+  int here = t;  // WIDE: a new number to the compiler for each pass over the row: else it would keep the parameters for the second one
+  auto read_params = [&](int j, int to) {
+    post_chunk<C>(a, pb, (j * G + here) * C, A + to, B + to);
+    param_chunk<C>(a.p.pre_weight, pb, (j * G + here) * C, d, 1.f, W + to);
+  };
 #pragma unroll
-  for (int k = 0; k < SUMS; ++k)
+  for (int k = 0; k < REGS; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+  if (WIDE) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    post_chunk<C>(a, pb, (j * G + t) * C, A + j * C, B + j * C);
-    param_chunk<C>(a.p.pre_weight, pb, (j * G + t) * C, d, 1.f, W + j * C);
+    for (int e = 0; e < 2 * E; ++e) sums[e * G + t] = 0.f;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) read_params(j, WIDE ? 0 : j * C);
   }
+  // sum k of element e (0: c D h^, 1: dn s^, 2: c D, 3: dn) grows by u v, or by v
+  auto grow = [&](int k, int e, float u, float v) {
+    if (WIDE && k < 2) sums[(k * E + e) * G + t] = fmaf(u, v, sums[(k * E + e) * G + t]);
+    else if (WIDE) acc[REGS > 0 ? k - 2 : 0][e] = fmaf(u, v, acc[REGS > 0 ? k - 2 : 0][e]);
+    else acc[k][e] = fmaf(u, v, acc[k][e]);
+  };
   const int64_t step = (int64_t)gridDim.x * PER;
-  int64_t r = (int64_t)blockIdx.x * PER + (PER > 1 ? wave_of() : 0);
+  int64_t r = (int64_t)blockIdx.x * PER + (G < 64 ? threadIdx.x / G : PER > 1 ? wave_of() : 0);
   u32x4 nh[NV], nx[NV], ns[NV], nn[NV];
   float4 nst = {0, 0, 0, 0};
   float nc = 1.f;
   auto fetch = [&](int64_t row) {
-    R::template load_all<G, NV>(a.h, row, a.h_stride, t, d, nh);
-    R::template load_all<G, NV>(a.x, row, a.x_stride, t, d, nx);
-    if (a.ds) R::template load_all<G, NV>(a.ds, row, a.ds_stride, t, d, ns);
-    if (pre) R::template load_all<G, NV>(a.dn, row, a.dn_stride, t, d, nn);
+    R::template load_all<G, NV, true>(a.h, row, a.h_stride, t, d, nh);
+    R::template load_all<G, NV, true>(a.x, row, a.x_stride, t, d, nx);
+    if (a.ds) R::template load_all<G, NV, true>(a.ds, row, a.ds_stride, t, d, ns);
+    if (pre) R::template load_all<G, NV, true>(a.dn, row, a.dn_stride, t, d, nn);
     nst = *(const float4*)(a.stats + 4 * row);
     if (a.p.row_gate) nc = a.p.row_gate[row];
   };
 #pragma unroll
   for (int j = 0; j < NV; ++j) ns[j] = nn[j] = u32x4{0, 0, 0, 0};
-  if (r < a.rows) fetch(r);
+  if (AHEAD && r < a.rows) fetch(r);
   int turn = 0;
   for (; r < a.rows; r += step) {
+    if (!AHEAD) fetch(r);
     u32x4 h[NV], x[NV], g[NV], q[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -258,69 +328,82 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       g[j] = ns[j];
       q[j] = nn[j];
     }
+    R::template settle_all<G, NV>(t, d, h);
+    R::template settle_all<G, NV>(t, d, x);
+    R::template settle_all<G, NV>(t, d, g);
+    R::template settle_all<G, NV>(t, d, q);
     const float4 st = nst;
     const float c = nc, r1 = st.y, o1 = -st.x * r1, r2 = st.w, o2 = -st.z * r2;
-    if (r + step < a.rows) fetch(r + step);
+    if (AHEAD && r + step < a.rows) fetch(r + step);
+    // of element i of chunk j, whose parameters are held from p on
     auto n1 = [&](int j, int i) { return fmaf(K::at(h[j], i), r1, o1); };
-    auto z = [&](int j, int i, float n) { return BIAS ? fmaf(n, A[j * C + i], B[j * C + i]) : n * A[j * C + i]; };
-    auto n2 = [&](int j, int i, float n) { return fmaf(fmaf(a.rho, K::at(x[j], i), c * z(j, i, n)), r2, o2); };
+    auto z = [&](int p, int i, float n) { return BIAS ? fmaf(n, A[p + i], B[p + i]) : n * A[p + i]; };
+    auto n2 = [&](int j, int p, int i, float n) { return fmaf(fmaf(a.rho, K::at(x[j], i), c * z(p, i, n)), r2, o2); };
     float ma = 0.f, mn = 0.f;
     if (pre) {
       float v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) {
+        const int p = WIDE ? 0 : j * C;
+        if (WIDE) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_params(j, p);
+        }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-          const int e = j * C + i;
-          const float n = n2(j, i, n1(j, i)), y = K::at(q[j], i), w = y * W[e];
-          acc[1][e] = fmaf(y, n, acc[1][e]);
-          if (BIAS) acc[SUMS - 1][e] += y;
+          const float n = n2(j, p, i, n1(j, i)), y = K::at(q[j], i), w = y * W[p + i];
+          grow(1, j * C + i, y, n);
+          if (BIAS) grow(3, j * C + i, 1.f, y);
           v[0] += w;
           v[1] = fmaf(w, n, v[1]);
         }
+      }
       group_total<G>(v, red[turn]);
       turn ^= 1;
       if (a.pre == MOE_NORM_LAYER) ma = v[0] / d;
       mn = v[1] / d;
     }
+    if (sizeof(T) == 2) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      forget(h[j]);
-      forget(x[j]);
-      forget(q[j]);
+      for (int j = 0; j < NV; ++j) {
+        forget(h[j]);
+        forget(x[j]);
+        forget(q[j]);
+      }
     }
+    if (WIDE) asm volatile("" : "+v"(here));
     float D[E], v[3] = {0.f, 0.f, 0.f};
-    if (pre) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          const int e = j * C + i;
-          D[e] = fmaf(r2, fmaf(-n2(j, i, n1(j, i)), mn, fmaf(K::at(q[j], i), W[e], -ma)), K::at(g[j], i));
-        }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) D[e] = K::at(g[e / C], e % C);
-    }
     T* to = (T*)a.dx + r * a.dx_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int at = (j * G + t) * C;
+      const int at = (j * G + t) * C, p = WIDE ? 0 : j * C;
+      if (WIDE) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_params(j, p);
+        }
+      float y[C];
+      if (pre) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          y[i] = fmaf(r2, fmaf(-n2(j, p, i, n1(j, i)), mn, fmaf(K::at(q[j], i), W[p + i], -ma)), K::at(g[j], i));
+      } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) y[i] = K::at(g[j], i);
+      }
       float o[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const int e = j * C + i;
         const float n = n1(j, i);
-        float y = at + (TAIL ? i : 0) < d ? D[e] : 0.f;
-        o[i] = a.rho * y;
-        v[2] = fmaf(y, z(j, i, n), v[2]);
-        y *= c;
-        acc[0][e] = fmaf(y, n, acc[0][e]);
-        if (BIAS) acc[SUMS / 2][e] += y;
-        y *= A[e];
-        v[0] += y;
-        v[1] = fmaf(y, n, v[1]);
-        D[e] = y;
+        if (at + (TAIL ? i : 0) >= d) y[i] = 0.f;
+        o[i] = a.rho * y[i];
+        v[2] = fmaf(y[i], z(p, i, n), v[2]);
+        y[i] *= c;
+        grow(0, j * C + i, y[i], n);
+        if (BIAS) grow(2, j * C + i, 1.f, y[i]);
+        y[i] *= A[p + i];
+        v[0] += y[i];
+        v[1] = fmaf(y[i], n, v[1]);
+        D[j * C + i] = y[i];
       }
       R::store(to, at, d, o);
     }
@@ -328,8 +411,9 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       group_total<G>(v, red[turn]);
       turn ^= 1;
     }
+    if (sizeof(T) == 2)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) forget(h[j]);
+      for (int j = 0; j < NV; ++j) forget(h[j]);
     ma = a.post == MOE_NORM_LAYER ? v[0] / d : 0.f;
     mn = a.post == MOE_NORM_NONE ? 0.f : v[1] / d;
     to = (T*)a.dh + r * a.dh_stride;
@@ -355,6 +439,7 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaun
     }
     __syncthreads();
     if (w > 0) return;
+#pragma unroll 1
     for (int u = 0; u < PER - 1; ++u) {
       const float* from = join + u * SUMS * E * G;
 #pragma unroll
@@ -367,34 +452,46 @@ __global__ __launch_bounds__(G == 64 ? 256 : G) void k_residual_bwd(ResidualLaun
 #pragma unroll
   for (int k = 0; k < SUMS; ++k)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int c = (j * G + t) * C + i;
-        if (c < d) out[(int64_t)k * d + c] = acc[k][j * C + i];
-      }
+    for (int e = 0; e < E; ++e) {
+      const int c = (e / C * G + t) * C + e % C;
+      if (c < d) out[(int64_t)k * d + c] = !WIDE ? acc[k][e] : k < 2 ? sums[(k * E + e) * G + t] : acc[REGS > 0 ? k - 2 : 0][e];
+    }
 }
 
-// The parameters' gradients from the workgroups' partial sums, rows of `sums` sums: 64 columns per workgroup, its 16 waves take every
-// 16th partial row, and their sums are added in wave order.
+// The parameters' gradients from the workgroups' partial sums, `sums` of them in each: {c D h^, dn s^} or {c D h^, dn s^, c D, dn}.  64
+// columns of N1's (y = 0) or of N2's (1) per workgroup; its 16 waves take every 16th partial row, eight in flight, and their sums are
+// added in wave order.
 template <typename PT>
 __global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int n, int sums) {
-  __shared__ float red[15][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, d = a.d;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  __shared__ float red[15][2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, d = a.d, pre = blockIdx.y;
+  float s[2] = {0.f, 0.f};
   if (c < d)
-    for (int k = wave; k < n; k += 16)
+    for (int k = wave; k < n; k += 128) {
+      const float* p = a.partial + ((int64_t)k * sums + pre) * d + c;
+      float v[2][8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u < sums) s[u] += a.partial[((int64_t)k * sums + u) * d + c];
-  if (wave > 0)
+      for (int u = 0; u < 8; ++u) {
+        const int64_t at = (int64_t)16 * u * sums * d;
+        v[0][u] = k + 16 * u < n ? p[at] : 0.f;
+        v[1][u] = sums == 4 && k + 16 * u < n ? p[at + 2 * d] : 0.f;
+      }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) red[wave - 1][u][lane] = s[u];
+      for (int u = 0; u < 8; ++u) {
+        s[0] += v[0][u];
+        s[1] += v[1][u];
+      }
+    }
+  if (wave > 0) {
+    red[wave - 1][0][lane] = s[0];
+    red[wave - 1][1][lane] = s[1];
+  }
   __syncthreads();
   if (wave > 0 || c >= d) return;
-  for (int k = 0; k < 15; ++k)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) s[u] += red[k][u][lane];
+  for (int k = 0; k < 15; ++k) {
+    s[0] += red[k][0][lane];
+    s[1] += red[k][1][lane];
+  }
   auto param = [&](const void* p, float empty) {
     if (!p) return empty;
     return sizeof(PT) == 4 ? ((const float*)p)[c] : bf16_to_f32(((const bf16_t*)p)[c]);
@@ -404,13 +501,15 @@ __global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int 
     if (sizeof(PT) == 4) ((float*)p)[c] = v;
     else ((bf16_t*)p)[c] = f32_to_bf16(v);
   };
-  // {c D h^, dn s^}, or {c D h^, dn s^, c D, dn}
+  if (pre) {
+    put(a.d_pre_weight, s[0]);
+    put(a.d_pre_bias, s[1]);
+    return;
+  }
   const float gate = param(a.p.gate, 1.f);
   put(a.d_post_weight, gate * s[0]);
-  put(a.d_pre_weight, s[1]);
-  put(a.d_post_bias, gate * s[2]);
-  put(a.d_pre_bias, s[3]);
-  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), s[0], param(a.p.post_bias, 0.f) * s[2]));
+  put(a.d_post_bias, gate * s[1]);
+  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), s[0], param(a.p.post_bias, 0.f) * s[1]));
 }
 
 int chunks_of(int d, int dtype) { return (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16; }
@@ -426,9 +525,10 @@ template <typename T, int G, int NV, bool SHARED, bool TAIL>
 void forward(const ResidualLaunch& a, hipStream_t st) {
   constexpr int PER = SHARED ? 512 / G : 1;
   const int64_t groups = (a.rows + PER - 1) / PER, most = SHARED ? 512 : 256 * 2048 / G;
-  const int lds = SHARED ? (a.p.post_bias || a.p.pre_bias ? 4 : 2) * NV * Chunk<T>::C * 64 * 4 : 0;
-  if (lds > 65536)
-    (void)hipFuncSetAttribute((const void*)k_residual<T, G, NV, SHARED, TAIL>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  constexpr int MOST = 4 * NV * Chunk<T>::C * G * 4;
+  const int lds = SHARED ? (a.p.post_bias || a.p.pre_bias ? 4 : 2) * NV * Chunk<T>::C * G * 4 : 0;
+  if (SHARED && MOST > 65536 - 512)
+    (void)hipFuncSetAttribute((const void*)k_residual<T, G, NV, SHARED, TAIL>, hipFuncAttributeMaxDynamicSharedMemorySize, MOST);
   hipLaunchKernelGGL((k_residual<T, G, NV, SHARED, TAIL>), dim3((unsigned)std::min(groups, most)), dim3(SHARED ? 512 : G), lds, st, a);
 }
 
@@ -440,53 +540,86 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
     constexpr bool S = decltype(shared)::value;
     if (nv == 1) forward<T, G, 1, S, TAIL>(a, st);
     else if (nv == 2) forward<T, G, 2, S, TAIL>(a, st);
-    else if (nv == 4) forward<T, G, 4, S, TAIL>(a, st);
-    else if constexpr (G < 1024) {
-      if (nv == 8) forward<T, G, 8, S, TAIL>(a, st);
-      else forward<T, G, 16, S, TAIL>(a, st);
+    else if constexpr (G == 64 || (G == 1024 && sizeof(T) == 4)) {
+      if (nv == 4) forward<T, G, 4, S, TAIL>(a, st);
+      else if constexpr (G == 64) {
+        if (nv == 8) forward<T, G, 8, S, TAIL>(a, st);
+        else forward<T, G, 16, S, TAIL>(a, st);
+      }
     }
   };
-  if (a.rows >= 2048 && chunks <= 1024) with(integral_constant<int, 64>{}, std::true_type{}, per_thread(chunks, 64));
-  else if (a.rows >= 512 || chunks <= 256) with(integral_constant<int, 256>{}, std::false_type{}, per_thread(chunks, 256));
+  // A wave to a row where it can hold one and there are rows for all of eight waves on each CU: 16384 x 7168 bf16 195 us (4.8 TB/s), by
+  // 256 or 1024 threads 250; 1000 rows of them 19.3 us, by 1024 threads 17.5.  Wider rows by 1024: 8192 x 16384 bf16 264 us, by 512 373,
+  // by 256 (which spill) 714
+  if (a.rows >= 2048 && chunks <= 32) with(integral_constant<int, 16>{}, std::true_type{}, per_thread(chunks, 16));
+  else if (a.rows >= 2048 && chunks <= 1024) with(integral_constant<int, 64>{}, std::true_type{}, per_thread(chunks, 64));
+  else if (chunks <= 512) with(integral_constant<int, 256>{}, std::false_type{}, per_thread(chunks, 256));
   else with(integral_constant<int, 1024>{}, std::false_type{}, per_thread(chunks, 1024));
 }
 
-// Eight elements in each thread of the backward's groups (16 where a row is wider than 8192)
-void backward_plan(int d, int dtype, int* G, int* NV) {
-  const int c = dtype == MOE_BF16 ? 8 : 4;
-  *G = 64;
-  while (*G < 1024 && *G * 8 < d) *G *= 2;
-  *NV = (*G * 8 < d ? 16 : 8) / c;
+// The threads of the backward's groups.  Eight elements in a thread while registers hold what
+// belongs to them: up to 1024 threads with two sums in bf16.  With four, or in fp32, 512 threads of sixteen (16384 x 7168 bf16, four sums:
+// 320 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 285 and 310), but WIDE in fp32 with four (418; 726 and 887 otherwise);
+// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 513 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
+int backward_threads(int d, int dtype, bool bias) {
+  if (d > 8192) return 1024;
+  if (d > 4096) return (dtype == MOE_BF16) == bias ? 512 : 1024;
+  int G = d <= 128 ? 16 : 64;
+  while (G * 8 < d) G *= 2;
+  return G;
 }
+int groups_in_block(int G) { return G <= 64 ? 256 / G : 1; }
 
-int64_t backward_groups(int64_t rows, int G) { return std::min<int64_t>(std::max<int64_t>(rows / 4, std::min<int64_t>(rows, 256)), 256 * 1024 / G); }
+// Groups of a launch: four rows for each one's sums, while that leaves one for every CU, and no more than fill the chip (1000 x 7168 bf16:
+// 34 us by 256 groups, 41 by 128, 49 by 512; 10000 x 1024: 121, 67, 50 and 39 by 128, 256, 512 and 1024)
+int64_t backward_groups(int64_t rows, int G) {
+  return std::min<int64_t>(std::max<int64_t>(rows / 4, std::min<int64_t>(rows, 256)), 256 * 1024 / G);
+}
 
 template <typename T, bool TAIL>
 void backward(const ResidualLaunch& a, bool bias, int64_t groups, hipStream_t st) {
-  int G, NV;
-  backward_plan(a.d, a.dtype, &G, &NV);
   constexpr int V8 = 8 / Chunk<T>::C;
-  auto go = [&](auto g, auto nv) {
-    constexpr int GG = decltype(g)::value, N = decltype(nv)::value, PER = GG == 64 ? 4 : 1;
-    const dim3 grid((unsigned)((groups + PER - 1) / PER)), block(GG * PER);
-    if (bias) hipLaunchKernelGGL((k_residual_bwd<T, GG, N, true, TAIL>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_residual_bwd<T, GG, N, false, TAIL>), grid, block, 0, st, a);
+  constexpr bool BF16 = sizeof(T) == 2;
+  using one = integral_constant<int, V8>;
+  using two = integral_constant<int, 2 * V8>;
+  using none = std::false_type;
+  using wide = std::true_type;
+  auto go = [&](auto g, auto nv, auto sums, auto w) {
+    constexpr int G = decltype(g)::value, NV = decltype(nv)::value, SUMS = decltype(sums)::value;
+    constexpr bool WIDE = decltype(w)::value;
+    constexpr int lds = WIDE ? 2 * NV * Chunk<T>::C * G * 4 : 0;
+    const int per = groups_in_block(G);
+    const auto kernel = k_residual_bwd<T, G, NV, SUMS, WIDE, TAIL>;
+    if (lds > 65536 - 512) (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((groups + per - 1) / per)), dim3(G * per), lds, st, a);
   };
-  if (G == 64) go(integral_constant<int, 64>{}, integral_constant<int, V8>{});
-  else if (G == 128) go(integral_constant<int, 128>{}, integral_constant<int, V8>{});
-  else if (G == 256) go(integral_constant<int, 256>{}, integral_constant<int, V8>{});
-  else if (G == 512) go(integral_constant<int, 512>{}, integral_constant<int, V8>{});
-  else if (NV == V8) go(integral_constant<int, 1024>{}, integral_constant<int, V8>{});
-  else go(integral_constant<int, 1024>{}, integral_constant<int, 2 * V8>{});
+  auto both = [&](auto g, auto nv, auto w) {
+    if (bias) go(g, nv, integral_constant<int, 4>{}, w);
+    else go(g, nv, integral_constant<int, 2>{}, w);
+  };
+  const int G = backward_threads(a.d, a.dtype, bias);
+  if (a.d > 8192) both(integral_constant<int, 1024>{}, two{}, wide{});
+  else if (a.d > 4096) {  // as the plan has it
+    if (bias) go(integral_constant<int, BF16 ? 512 : 1024>{}, std::conditional_t<BF16, two, one>{}, integral_constant<int, 4>{},
+                 std::conditional_t<BF16, none, wide>{});
+    else go(integral_constant<int, BF16 ? 1024 : 512>{}, std::conditional_t<BF16, one, two>{}, integral_constant<int, 2>{}, none{});
+  } else if (G == 512) both(integral_constant<int, 512>{}, one{}, none{});
+  else if (G == 256) both(integral_constant<int, 256>{}, one{}, none{});
+  else if (G == 128) both(integral_constant<int, 128>{}, one{}, none{});
+  else if (G == 64) both(integral_constant<int, 64>{}, one{}, none{});
+  else both(integral_constant<int, 16>{}, one{}, none{});
 }
 
 }  // namespace
 
 int64_t residual_partial_floats(int64_t rows, int d, int dtype) {
-  int G, NV;
-  backward_plan(d, dtype, &G, &NV);
-  const int64_t per = G == 64 ? 4 : 1;
-  return (backward_groups(rows, G) + per - 1) / per * 4 * d;
+  int64_t most = 0;
+  for (const bool bias : {false, true}) {
+    const int G = backward_threads(d, dtype, bias);
+    const int64_t per = groups_in_block(G);
+    most = std::max(most, (backward_groups(rows, G) + per - 1) / per * (bias ? 4 : 2) * d);
+  }
+  return most;
 }
 
 int launch_residual(const ResidualLaunch& a, hipStream_t st) {
@@ -499,11 +632,10 @@ int launch_residual(const ResidualLaunch& a, hipStream_t st) {
     else forward<float, false>(a, st);
     return hipGetLastError() == hipSuccess ? 0 : -1;
   }
-  int G, NV;
-  backward_plan(a.d, a.dtype, &G, &NV);
-  const int64_t groups = backward_groups(a.rows, G), per = G == 64 ? 4 : 1;
   // sums of c D and dn too, for the biases' gradients and post_bias's part of the gate's
   const bool bias = a.p.post_bias || a.d_post_bias || a.d_pre_bias;
+  const int G = backward_threads(a.d, a.dtype, bias);
+  const int64_t groups = backward_groups(a.rows, G), per = groups_in_block(G);
   if (a.rows > 0) {
     if (tb && tail) backward<bf16_t, true>(a, bias, groups, st);
     else if (tb) backward<bf16_t, false>(a, bias, groups, st);
@@ -512,7 +644,7 @@ int launch_residual(const ResidualLaunch& a, hipStream_t st) {
   }
   if (a.d_post_weight || a.d_post_bias || a.d_gate || a.d_pre_weight || a.d_pre_bias) {
     const int n = (int)((groups + per - 1) / per);
-    const dim3 grid((unsigned)((a.d + 63) / 64));
+    const dim3 grid((unsigned)((a.d + 63) / 64), 2);
     if (a.param_dtype == MOE_BF16) hipLaunchKernelGGL(k_residual_params<bf16_t>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
     else hipLaunchKernelGGL(k_residual_params<float>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
   }
