@@ -19,9 +19,9 @@ __device__ __forceinline__ V take(const V* p) {
 }
 
 // Whether this workgroup, number id of n, is the last of them to come here; its own stores are complete then, and so are the
-// others'.  The counters, 64 bytes apart, are 0 before and after.  Beyond JOIN_GROUP workgroups each group of them has a counter of its
+// others'.  The counters, 256 bytes apart, are 0 before and after.  Beyond JOIN_GROUP workgroups each group of them has a counter of its
 // own and its last one goes on to the first: 2048 workgroups at one counter took 20 us.
-constexpr uint32_t JOIN_GROUP = 32, JOIN_STRIDE = 16;
+constexpr uint32_t JOIN_GROUP = 32, JOIN_STRIDE = 64;
 __host__ __device__ inline int64_t join_words(int64_t n) {
   return n <= 1 ? 0 : JOIN_STRIDE * (1 + (n <= JOIN_GROUP ? 0 : (n + JOIN_GROUP - 1) / JOIN_GROUP));
 }

@@ -193,9 +193,17 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
     __syncthreads();
   }
   int here = t;  // a new number to the compiler for each row: else it would keep all of LDS in registers
+  constexpr bool HELD = !SHARED && E <= 8;  // the parameters in registers, read while the first row is on its way
+  float held[HELD ? 4 : 1][HELD ? E : 1];    // weights, then biases
   // chunk j of weight (0: A, 1: pre_weight) and of its bias
   auto weights = [&](int which, int j, float* w, float* b) {
-    if (SHARED) {
+    if (HELD) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        w[i] = held[HELD ? which : 0][HELD ? j * C + i : 0];
+        b[i] = held[HELD ? 2 + which : 0][HELD ? j * C + i : 0];
+      }
+    } else if (SHARED) {
 #pragma unroll
       for (int q = 0; q < C / 4; ++q) {
         const int at = ((j * (C / 4) + q) * G + here) * 4;
@@ -210,11 +218,22 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
     }
   };
   int turn = 0;
+  bool first = true;
   for (int64_t r = (int64_t)blockIdx.x * PER + (G < 64 ? threadIdx.x / G : SHARED ? wave_of() : 0); r < a.rows; r += (int64_t)gridDim.x * PER) {
     u32x4 h[NV], x[NV];
     if (SHARED) asm volatile("" : "+v"(here));
     R::template load_all<G, NV>(a.h, r, a.h_stride, t, d, h);
     R::template load_all<G, NV>(a.x, r, a.x_stride, t, d, x);
+    if (HELD && first) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = (j * G + t) * C;
+        post_chunk<C>(a, pb, at, held[0] + (HELD ? j * C : 0), held[HELD ? 2 : 0] + (HELD ? j * C : 0));
+        param_chunk<C>(a.p.pre_weight, pb, at, d, 1.f, held[HELD ? 1 : 0] + (HELD ? j * C : 0));
+        param_chunk<C>(a.p.pre_bias, pb, at, d, 0.f, held[HELD ? 3 : 0] + (HELD ? j * C : 0));
+      }
+      first = false;
+    }
     const float c = a.p.row_gate ? a.p.row_gate[r] : 1.f;
     float m1, r1, m2, r2, s[E];
     auto of_h = [&](int j, float* v) {
@@ -535,26 +554,33 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
 template <typename T, bool TAIL>
 void forward(const ResidualLaunch& a, hipStream_t st) {
   const int chunks = chunks_of(a.d, a.dtype);
-  auto with = [&](auto g, auto shared, int nv) {
-    constexpr int G = decltype(g)::value;
-    constexpr bool S = decltype(shared)::value;
-    if (nv == 1) forward<T, G, 1, S, TAIL>(a, st);
-    else if (nv == 2) forward<T, G, 2, S, TAIL>(a, st);
-    else if constexpr (G == 64 || (G == 1024 && sizeof(T) == 4)) {
-      if (nv == 4) forward<T, G, 4, S, TAIL>(a, st);
-      else if constexpr (G == 64) {
-        if (nv == 8) forward<T, G, 8, S, TAIL>(a, st);
-        else forward<T, G, 16, S, TAIL>(a, st);
-      }
-    }
+  // A wave to a row (a quarter of one to rows of up to 32 chunks) where it can hold one and there are rows for all of eight waves on each CU:
+  // 16384 x 7168 bf16 195 us (4.8 TB/s), by 256 or 1024 threads 250; 65536 x 96 13 us, by whole waves 36.  Fewer rows by a thread to a chunk:
+  // 24 x 4096 bf16 6.0 us, by half as many threads 7.8; 1000 x 7168 17.5, by a wave to a row 19.3.  Rows of more than 1024 chunks by 1024
+  // threads: 8192 x 16384 bf16 258 us, by 512 373, by 256 (which spill) 714
+  const int wave = a.rows < 2048 ? 0 : chunks <= 32 ? 16 : chunks <= 1024 ? 64 : 0;
+  const int G = wave ? wave : chunks <= 256 ? 256 : chunks <= 512 ? 512 : 1024;
+  const int nv = per_thread(chunks, G);
+  auto go = [&](auto g, auto n, auto shared) {
+    forward<T, decltype(g)::value, decltype(n)::value, decltype(shared)::value, TAIL>(a, st);
   };
-  // A wave to a row where it can hold one and there are rows for all of eight waves on each CU: 16384 x 7168 bf16 195 us (4.8 TB/s), by
-  // 256 or 1024 threads 250; 1000 rows of them 19.3 us, by 1024 threads 17.5.  Wider rows by 1024: 8192 x 16384 bf16 264 us, by 512 373,
-  // by 256 (which spill) 714
-  if (a.rows >= 2048 && chunks <= 32) with(integral_constant<int, 16>{}, std::true_type{}, per_thread(chunks, 16));
-  else if (a.rows >= 2048 && chunks <= 1024) with(integral_constant<int, 64>{}, std::true_type{}, per_thread(chunks, 64));
-  else if (chunks <= 512) with(integral_constant<int, 256>{}, std::false_type{}, per_thread(chunks, 256));
-  else with(integral_constant<int, 1024>{}, std::false_type{}, per_thread(chunks, 1024));
+  using yes = std::true_type;
+  using no = std::false_type;
+  using g16 = integral_constant<int, 16>;
+  using g64 = integral_constant<int, 64>;
+  using g1024 = integral_constant<int, 1024>;
+  if (G == 16 && nv == 1) go(g16{}, integral_constant<int, 1>{}, yes{});
+  else if (G == 16) go(g16{}, integral_constant<int, 2>{}, yes{});
+  else if (G == 64 && nv == 1) go(g64{}, integral_constant<int, 1>{}, yes{});
+  else if (G == 64 && nv == 2) go(g64{}, integral_constant<int, 2>{}, yes{});
+  else if (G == 64 && nv == 4) go(g64{}, integral_constant<int, 4>{}, yes{});
+  else if (G == 64 && nv == 8) go(g64{}, integral_constant<int, 8>{}, yes{});
+  else if (G == 64) go(g64{}, integral_constant<int, 16>{}, yes{});
+  else if (G == 256) go(integral_constant<int, 256>{}, integral_constant<int, 1>{}, no{});
+  else if (G == 512) go(integral_constant<int, 512>{}, integral_constant<int, 1>{}, no{});
+  else if (nv == 1) go(g1024{}, integral_constant<int, 1>{}, no{});
+  else if (nv == 2) go(g1024{}, integral_constant<int, 2>{}, no{});
+  else if constexpr (sizeof(T) == 4) go(g1024{}, integral_constant<int, 4>{}, no{});
 }
 
 // The threads of the backward's groups.  Eight elements in a thread while registers hold what

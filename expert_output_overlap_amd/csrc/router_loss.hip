@@ -130,12 +130,12 @@ __host__ __device__ inline int64_t seq_counter_words(int sequences) {
   const int most = most_parts(sequences);
   return most > 1 ? JOIN_STRIDE * (1 + groups_of(most)) : 0;
 }
-__host__ __device__ inline int64_t counter_words(int sequences) { return join_words(sequences) + sequences * seq_counter_words(sequences); }
+__host__ __device__ inline int64_t counter_words(int sequences) { return join_words(512) + sequences * seq_counter_words(sequences); }
 __host__ __device__ inline Workspace ws_of(void* p, int64_t sequences, int parts, int experts) {
   Workspace w;
   const int64_t groups = groups_of(parts);
   w.counters = (uint32_t*)p;
-  w.part_counters = w.counters + join_words(sequences);
+  w.part_counters = w.counters + join_words(512);
   w.seq = (double*)(w.counters + counter_words((int)sequences));
   w.part_z = w.seq + 2 * sequences;
   w.part_p = w.part_z + sequences * parts;
@@ -145,8 +145,19 @@ __host__ __device__ inline Workspace ws_of(void* p, int64_t sequences, int parts
   return w;
 }
 
+// One thread: the means and the losses, from the sequences with rows, their rows, and the sums of their parts of B and Z
+__device__ __forceinline__ void finish(const RouterLaunch& a, double live, double rows, double B, double Z) {
+  B /= fmax(live, 1.);
+  Z /= fmax(rows, 1.);
+  a.means[0] = (int)live;
+  a.means[1] = (int)rows;
+  a.losses[0] = (float)((double)a.balance * B + (double)a.z * Z);
+  a.losses[1] = (float)B;
+  a.losses[2] = (float)Z;
+}
+
 template <int L, int NV>
-__global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts) {
+__global__ __launch_bounds__(BLOCK, 4) void k_router_loss(RouterLaunch a, int parts) {
   constexpr int E = 4 * NV, RW = 64 / L, COLS = L * E;
   constexpr int SLICES = COLS < BLOCK ? BLOCK / COLS : 1;  // of a sequence's parts, taken by threads of their own
   constexpr int HELD = COLS <= 512 ? WAVES : WAVES / 2;    // waves whose columns' sums are in LDS at once
@@ -154,6 +165,7 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
   __shared__ int32_t hist[COLS], many[SLICES * COLS], flag;
   const int lane = lane_id(), wave = threadIdx.x >> 6, l = lane % L, sub = lane / L, G = a.experts;
   const Workspace ws = ws_of(a.workspace, a.sequences, parts, G);
+  int mine = -1;  // the last sequence that this workgroup ended
   for (int64_t u = blockIdx.x; u < (int64_t)a.sequences * parts; u += gridDim.x) {
     const int s = (int)(u / parts), part = (int)(u % parts);
     int first, end;
@@ -223,6 +235,7 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
       double v[1] = {z};
       block_sums(v, red);
       if (threadIdx.x == 0) hand_out(&ws.part_z[u], v[0]);
+      z = 0;
       // to the last of the parts, or of a group of them and on to the last of the groups
       const int groups = groups_of(parts), group = part / GROUP;
       uint32_t* counters = ws.part_counters + s * seq_counter_words(a.sequences);
@@ -243,35 +256,41 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
         }
         last = last_of(counter, 0, count, &flag);
         if (!last) break;
+        if (level == 1 && (int)threadIdx.x < parts) z = take(&ws.part_z[(int64_t)s * parts + threadIdx.x]);  // parts <= 256
         const int slice = SLICES > 1 ? threadIdx.x / COLS : 0;
+        const int c0 = SLICES > 1 ? threadIdx.x % COLS : threadIdx.x;
+        double sum[PER];
+        int total[PER];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) sum[k] = total[k] = 0;
+#pragma unroll 1
+        for (int i = slice; i < count; i += 8 * SLICES) {
+          double pq[PER][8];
+          int pn[PER][8];
+#pragma unroll
+          for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              const int at = i + m * SLICES, c = c0 + k * BLOCK;
+              pq[k][m] = at < count && c < G ? take(&to_p[(int64_t)(from + at) * G + c]) : 0.;
+              pn[k][m] = at < count && c < G ? take(&to_n[(int64_t)(from + at) * G + c]) : 0;
+            }
+#pragma unroll
+          for (int k = 0; k < PER; ++k)
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+              sum[k] += pq[k][m];
+              total[k] += pn[k][m];
+            }
+        }
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-          const int c = SLICES > 1 ? threadIdx.x % COLS : threadIdx.x + k * BLOCK;
-          double sum = 0;
-          int total = 0;
-          if (c < G)
-#pragma unroll 1
-            for (int i = slice; i < count; i += 8 * SLICES) {
-              double pq[8];
-              int pn[8];
-#pragma unroll
-              for (int m = 0; m < 8; ++m) {
-                const int at = i + m * SLICES;
-                pq[m] = at < count ? take(&to_p[(int64_t)(from + at) * G + c]) : 0.;
-                pn[m] = at < count ? take(&to_n[(int64_t)(from + at) * G + c]) : 0;
-              }
-#pragma unroll
-              for (int m = 0; m < 8; ++m) {
-                sum += pq[m];
-                total += pn[m];
-              }
-            }
           if (SLICES > 1) {
-            col[slice * COLS + c] = sum;
-            many[slice * COLS + c] = total;
+            col[slice * COLS + c0] = sum[k];
+            many[slice * COLS + c0] = total[k];
           } else {
-            q[k] = sum;
-            n[k] = total;
+            q[k] = sum[k];
+            n[k] = total[k];
           }
         }
         if (SLICES > 1) {
@@ -293,8 +312,6 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
         counter = counters;
       }
       if (!last) continue;
-      z = 0;
-      for (int k = threadIdx.x; k < parts; k += BLOCK) z += take(&ws.part_z[(int64_t)s * parts + k]);
     }
     // the sequence: its counts, and its parts of B (f_g = G n_g / sum of n) and Z
     double v[3] = {0, 0, z};
@@ -309,33 +326,31 @@ __global__ __launch_bounds__(BLOCK) void k_router_loss(RouterLaunch a, int parts
     }
     block_sums(v, red);
     const double b = v[0] > 0 && len > 0 ? G / v[0] * v[1] / len : 0.;
-    double t[4] = {(double)(len > 0), (double)len, b, v[2]};  // of the batch: sequences with rows, rows, B, Z
-    if (a.sequences > 1) {
-      if (threadIdx.x == 0) {
-        hand_out(&ws.seq[2 * (int64_t)s], b);
-        hand_out(&ws.seq[2 * (int64_t)s + 1], v[2]);
-      }
-      if (!last_of(ws.counters, s, a.sequences, &flag)) continue;
-      t[0] = t[1] = t[2] = t[3] = 0;
-      for (int k = threadIdx.x; k < a.sequences; k += BLOCK) {
-        int f, e;
-        span_of(a, k, &f, &e);
-        t[0] += e > f;
-        t[1] += e - f;
-        t[2] += take(&ws.seq[2 * (int64_t)k]);
-        t[3] += take(&ws.seq[2 * (int64_t)k + 1]);
-      }
-      block_sums(t, red);
+    if (a.sequences == 1) {
+      if (threadIdx.x == 0) finish(a, len > 0, len, b, v[2]);
+      return;
     }
     if (threadIdx.x == 0) {
-      const double B = t[2] / fmax(t[0], 1.), Z = t[3] / fmax(t[1], 1.);
-      a.means[0] = (int)t[0];
-      a.means[1] = (int)t[1];
-      a.losses[0] = (float)((double)a.balance * B + (double)a.z * Z);
-      a.losses[1] = (float)B;
-      a.losses[2] = (float)Z;
+      hand_out(&ws.seq[2 * (int64_t)s], b);
+      hand_out(&ws.seq[2 * (int64_t)s + 1], v[2]);
     }
+    mine = s;
   }
+  // the batch: the last workgroup, or, where sequences have parts (and each workgroup one of them), the last to end a sequence
+  if (parts > 1 && mine < 0) return;
+  int f = 0, e = 0;
+  if ((int)threadIdx.x < a.sequences) span_of(a, threadIdx.x, &f, &e);  // on its way during the wait
+  if (!last_of(ws.counters, parts > 1 ? mine : blockIdx.x, parts > 1 ? a.sequences : gridDim.x, &flag)) return;
+  double t[4] = {0, 0, 0, 0};  // sequences with rows, rows, B, Z
+  for (int k = threadIdx.x; k < a.sequences; k += BLOCK) {
+    if (k >= BLOCK) span_of(a, k, &f, &e);
+    t[0] += e > f;
+    t[1] += e - f;
+    t[2] += take(&ws.seq[2 * (int64_t)k]);
+    t[3] += take(&ws.seq[2 * (int64_t)k + 1]);
+  }
+  block_sums(t, red);
+  if (threadIdx.x == 0) finish(a, t[0], t[1], t[2], t[3]);
 }
 
 // The gradient.  A wave takes `rows` rows in a row, so that it meets few sequences: f of the last one stays in registers
@@ -494,7 +509,7 @@ int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int seque
 
 int launch_router_loss(const RouterLaunch& a, hipStream_t st) {
   const int parts = parts_of(a.tokens, a.experts, a.sequences);
-  const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.sequences * parts, 1 << 16));
+  const dim3 grid((unsigned)std::min<int64_t>((int64_t)a.sequences * parts, 512));  // two on a CU; with parts there are fewer
   by_width(a.experts, [&](auto l, auto nv) {
     hipLaunchKernelGGL((k_router_loss<decltype(l)::value, decltype(nv)::value>), grid, dim3(BLOCK), 0, st, a, parts);
   });

@@ -436,17 +436,12 @@ class ResidualNorm:
                           if not (name.startswith("post") and post == "none" or name.startswith("pre") and pre == "none")}
             self.grads["row_gate"] = torch.empty(rows, dtype=torch.float32, device=self.device)
 
-    def _rows(self, n, matrices):
-        """Checks the matrices and gives their addresses and strides, as the argument structures take them."""
-        got = {}
-        for name, t in matrices.items():
-            if t is None:
-                continue
-            _need(t, name, (n, self.d), self.dtype, self.device, strided=True)
-            got[name] = t.data_ptr()
-            if n > 1:
-                got[name + "_stride"] = t.stride(0)
-        return got
+    def _put(self, args, n, name, t):
+        """A matrix's address and stride into the argument structure, after its check."""
+        _need(t, name, (n, self.d), self.dtype, self.device, strided=True)
+        setattr(args, name, t.data_ptr())
+        if n > 1:
+            setattr(args, name + "_stride", t.stride(0))
 
     def _params(self, n, w, row_gate):
         p = B.moe_residual_norm_params()
@@ -473,8 +468,14 @@ class ResidualNorm:
         T = self._count(x)
         s = _first(self.s, T) if s is None else s
         n = _first(self.n, T) if n is None and self.n is not None else n
-        a = B.moe_residual_norm_args(**self._rows(T, {"x": x, "h": h, "s": s, "n": n}),
-                                     stats=self.stats.data_ptr() if self.train and T else None)
+        a = B.moe_residual_norm_args()
+        self._put(a, T, "x", x)
+        self._put(a, T, "h", h)
+        self._put(a, T, "s", s)
+        if n is not None:
+            self._put(a, T, "n", n)
+        if self.train and T:
+            a.stats = self.stats.data_ptr()
         B.moe_residual_norm(self.shape, self._params(T, w, row_gate), a, stream)
         return s, n
 
@@ -487,8 +488,15 @@ class ResidualNorm:
         T = self._count(x)
         dx = _first(self.dx, T) if dx is None else dx
         dh = _first(self.dh, T) if dh is None else dh
-        b = B.moe_residual_norm_bwd_args(**self._rows(T, {"ds": ds, "dn": dn, "x": x, "h": h, "dx": dx, "dh": dh}),
-                                         stats=self.stats.data_ptr())
+        b = B.moe_residual_norm_bwd_args(stats=self.stats.data_ptr())
+        if ds is not None:
+            self._put(b, T, "ds", ds)
+        if dn is not None:
+            self._put(b, T, "dn", dn)
+        self._put(b, T, "x", x)
+        self._put(b, T, "h", h)
+        self._put(b, T, "dx", dx)
+        self._put(b, T, "dh", dh)
         for name in self.NAMES:
             if w.get(name) is not None and name in self.grads:
                 setattr(b, "d_" + name, self.grads[name].data_ptr())
