@@ -353,6 +353,25 @@ __global__ __launch_bounds__(BLOCK, 4) void k_router_loss(RouterLaunch a, int pa
   if (threadIdx.x == 0) finish(a, t[0], t[1], t[2], t[3]);
 }
 
+// The last sequence that begins at or before row t, by the row's L lanes: each step they look at L of what is left, so that a few dozen
+// sequences are one or two loads one after another
+template <int L>
+__device__ __forceinline__ int sequence_of(const RouterLaunch& a, int t, int l) {
+  const int shift = lane_id() / L * L;
+  int at = 0, left = a.sequences;  // it is one of [at, at + left), or there is none
+  bool none = false;
+  do {
+    const int step = (left + L - 1) / L, i = l * step;
+    const uint64_t m = __ballot(i < left && a.spans[2 * (int64_t)(at + i)] <= t) >> shift;
+    const int n = __popcll(L == 64 ? m : m & ((1ull << (L & 63)) - 1));
+    none |= n == 0;
+    const int skip = max(n - 1, 0) * step;
+    at += skip;
+    left = min(step, left - skip);
+  } while (__ballot(left > 1) != 0);
+  return none ? -1 : at;
+}
+
 // The gradient.  A wave takes `rows` rows in a row, so that it meets few sequences: f of the last one stays in registers
 template <int L, int NV, class O>
 __global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a, int rows) {
@@ -380,18 +399,18 @@ __global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a, int rows) {
     float e[E], den, top, g[E];
 #pragma unroll
     for (int j = 0; j < NV; ++j) load_cols(a.logits + (int64_t)t * G, (j * L + l) * 4, G, -INFINITY, e + 4 * j);
+    int id = -1;  // BY_LDS: lane l's slot; its loads too go out before the sequence is looked up
+    float w = 0.f;
+    if (BY_LDS && a.d_weights && l < K) {
+      id = a.topk_idx[(int64_t)t * K + l];
+      w = a.d_weights[(int64_t)t * K + l];
+    }
     if (__ballot(!found || t < first || t >= last)) {
       // the last sequence that begins at or before t; what lies between it and the next one is padding
       int s;
       if (!a.spans) s = t / ((int)a.tokens / a.sequences);
       else {
-        int lo = 0, hi = a.sequences;
-        while (lo < hi) {
-          const int mid = (lo + hi) / 2;
-          if (a.spans[2 * (int64_t)mid] <= t) lo = mid + 1;
-          else hi = mid;
-        }
-        s = lo - 1;
+        s = sequence_of<L>(a, t, l);
       }
       first = 0;
       last = 0;
@@ -420,11 +439,20 @@ __global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a, int rows) {
     if (a.d_weights) {
       const int64_t at = (int64_t)t * K;
       if (BY_LDS) {
-        const int id = l < K ? a.topk_idx[at + l] : -1;
-        const float w = l < K ? a.d_weights[at + l] : 0.f;
         const bool good = id >= 0 && id < G;
-        for (int j = 0; j < K; ++j)
-          if (l == j && good) mine[id] += w;
+        // all slots at once where no two of a row's have one expert, which their numbers at its place show; else one after another
+        if (good) mine[id] = __int_as_float(l);
+        wave_order();
+        const bool taken = good && __float_as_int(mine[id]) != l;
+        wave_order();
+        if (__ballot(taken) == 0) {
+          if (good) mine[id] = w;
+        } else {
+          if (good) mine[id] = 0.f;
+          wave_order();
+          for (int j = 0; j < K; ++j)
+            if (l == j && good) mine[id] += w;
+        }
         wave_order();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {

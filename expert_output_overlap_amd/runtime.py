@@ -520,6 +520,8 @@ class RouterLoss:
         self.shape = B.moe_router_shape(tokens, experts, k, sequences, MOE_DTYPES[dtype], balance, z)
         self.workspace = _workspace(B.moe_router_loss_workspace_bytes(self.shape), "moe_router_loss_workspace_bytes", self.device)
         self.workspace.zero_()
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).synchronize()  # zero before a call on any stream
         i32 = dict(dtype=torch.int32, device=self.device)
         self.counts, self.means = torch.empty(sequences, experts, **i32), torch.empty(2, **i32)
         self.losses = torch.empty(3, dtype=torch.float32, device=self.device)

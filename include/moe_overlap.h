@@ -600,7 +600,7 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* s, const moe_resid
  * its sequence's rows and its choices count.  A NaN or +inf makes its row's gradient and the losses NaN.  An id outside [0, G)
  * counts nowhere, its slot's gradient goes nowhere. */
 typedef struct {
-  int64_t tokens;     /* T >= 0, T top_k < 2^31 */
+  int64_t tokens;     /* T in [0, 2^30], T top_k < 2^31 */
   int32_t experts;    /* G, 1 .. 1024 */
   int32_t top_k;      /* 1 .. min(G, 16) */
   int32_t sequences;  /* S >= 1, S G < 2^31 */

@@ -117,10 +117,43 @@ def test_residual_norm_of_many_rows(rows, d, dtype, params):
         assert all(torch.equal(first[k], again[k]) for k in first)
 
 
+@pytest.mark.parametrize("d", [7, 64, 100, 127, 128, 129, 250, 500, 1000, 1023, 1500, 2900, 4096, 5003, 8190, 8192])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_residual_norm_of_rows_for_every_wave(d, dtype):
+    """Enough rows that the forward gives a wave, or a part of one, to each: every width class, whole chunks and not, with biases and
+    without."""
+    for bias in (False, True):
+        t, kinds = residual_case(2100, d, dtype, "f32", "layer" if bias else "rms", "layer", RHO, pad=d % 2, bias=bias, seed=d)
+        _, got = residual_run(t, kinds)
+        residual_check(got, residual_want(t, kinds), (d, dtype, bias))
+
+
+@pytest.mark.parametrize("rows,d", [(2500, 8192), (2048, 4100), (40, 16384)])
+def test_residual_norm_captured_with_much_lds(rows, d):
+    """Launches with more LDS than the default limit in a graph, replayed with new inputs between eager calls."""
+    t, kinds = residual_case(rows, d, "bf16", "f32", "layer", "layer")
+    op, _ = residual_run(t, kinds)
+    other = residual_run(t, kinds)[0]
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        _, got = residual_run(t, kinds, op)
+    rnd = gen(9)
+    for _ in range(3):
+        t["x"].copy_(rnd(rows, d))
+        t["dn"].copy_(rnd(rows, d))
+        torch.cuda.synchronize()
+        graph.replay()
+        _, want = residual_run(t, kinds, other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want)
+
+
 def test_residual_norm_in_place():
     from expert_output_overlap_amd.runtime import ResidualNorm
 
-    for rows, d in ((1, 7168), (150, 1536), (700, 7168)):
+    for rows, d in ((1, 7168), (150, 1536), (700, 7168), (2200, 100), (2200, 5001), (60, 16000)):
         t, kinds = residual_case(rows, d, "bf16", "f32", "rms", "layer")
         op, got = residual_run(t, kinds)
         keep = {k: v.clone() for k, v in got.items()}
@@ -411,18 +444,34 @@ def test_router_ids_that_repeat_or_are_none():
     """The same expert twice in a row's choices counts twice, and its slots' gradients add up; ids outside count nowhere."""
     from expert_output_overlap_amd.runtime import RouterLoss
 
-    logits, idx, _, dw = router_case(50, 9, 4, 1, False)
-    idx[3] = 5
-    idx[4, 1] = idx[4, 0]
-    idx[5] = -1
-    idx[6, 2], idx[7, 0] = 9, -(1 << 31)
-    op = RouterLoss(50, 9, 4, z=1e-3)
-    op.forward(logits, idx)
-    op.backward(logits, idx, dw)
-    counts, want = ref.router_loss(logits, idx, 1, float(np.float32(0.01)), float(np.float32(1e-3)), None, dw)
-    assert torch.equal(op.counts, counts) and counts.sum() == 50 * 4 - 6
-    within(op.losses, *want["losses"], "losses")
-    within(op.dlogits, *want["dlogits"], "dlogits")
+    for G in (9, 64, 100, 256, 600, 1024):
+        logits, idx, _, dw = router_case(50, G, 4, 1, False)
+        idx[3] = 5
+        idx[4, 1] = idx[4, 0]
+        idx[5] = -1
+        idx[6, 2], idx[7, 0] = G, -(1 << 31)
+        op = RouterLoss(50, G, 4, z=1e-3)
+        op.forward(logits, idx)
+        first = op.backward(logits, idx, dw).clone()
+        counts, want = ref.router_loss(logits, idx, 1, float(np.float32(0.01)), float(np.float32(1e-3)), None, dw)
+        assert torch.equal(op.counts, counts) and counts.sum() == 50 * 4 - 6
+        within(op.losses, *want["losses"], "losses")
+        within(op.dlogits, *want["dlogits"], "dlogits")
+        assert torch.equal(op.backward(logits, idx, dw), first)
+
+
+def test_router_workspace_serves_other_calls():
+    """Calls of fewer and more tokens in turn on one operator give what an operator of their own gives."""
+    from expert_output_overlap_amd.runtime import RouterLoss
+
+    for G, S in ((8, 1), (256, 3), (1000, 40), (16, 300)):
+        op = RouterLoss(9000, G, 2, S, z=1e-3)
+        for T in (9000, 10, 4500, 0, 9000, 700, 1, 9000):
+            logits, idx, spans, _ = router_case(T, G, 2, S, True, seed=T) if T else router_case(1, G, 2, S, True)
+            logits, idx = logits[:T], idx[:T]
+            own = RouterLoss(max(T, 1), G, 2, S, z=1e-3)
+            assert torch.equal(op.forward(logits, idx, spans), own.forward(logits, idx, spans)), (G, S, T)
+            assert torch.equal(op.counts, own.counts) and torch.equal(op.means, own.means)
 
 
 def test_router_gradient_against_differences():

@@ -118,7 +118,7 @@ def router_shape(**kw):
     return B.moe_router_shape(**{**dict(tokens=8, experts=16, top_k=2, sequences=2, dtype=B.MOE_F32, balance=0.01, z=0.001), **kw})
 
 
-@pytest.mark.parametrize("kw", [dict(tokens=-1), dict(tokens=1 << 30), dict(experts=0), dict(experts=1025), dict(top_k=0),
+@pytest.mark.parametrize("kw", [dict(tokens=-1), dict(tokens=1 << 30), dict(tokens=(1 << 30) + 2, top_k=1), dict(experts=0), dict(experts=1025), dict(top_k=0),
                                 dict(top_k=17), dict(experts=4, top_k=5), dict(sequences=0), dict(sequences=-1),
                                 dict(sequences=1 << 27), dict(dtype=2), dict(balance=NAN), dict(z=INF)])
 def test_router_shapes(kw):
@@ -211,3 +211,12 @@ def test_grad_arguments():
     refused(norm(a=P[7]), "overlaps")
     refused(L.moe_grad_clip(ctypes.byref(ok), None, None), "null")
     refused(L.moe_grad_clip(ctypes.byref(ok), P[7] + 1, None), "aligned")
+
+
+@pytest.mark.parametrize("experts", [1, 64, 1024])
+@pytest.mark.parametrize("sequences", [1, 3, 40, 255, 256, 3000])
+def test_router_workspace_serves_fewer_tokens(experts, sequences):
+    """A workspace of the largest call holds every smaller one's."""
+    sizes = [B.moe_router_loss_workspace_bytes(router_shape(tokens=sequences * t, experts=experts, top_k=1, sequences=sequences))
+             for t in (0, 1, 7, 16, 100, 1000, 5000, 20000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
