@@ -98,7 +98,7 @@ __device__ __forceinline__ void row_stats(Get chunk, int kind, int t, int d, flo
 }
 
 // Rows by chunks: a row's address is the wave's, a chunk's 32-bit offset the lane's.  TAIL: the row's last chunk may hold fewer
-// than C elements (its code for single elements costs registers: 40 to 60 of the backward's)
+// than C elements
 template <typename T, bool TAIL>
 struct Rows {
   using K = Chunk<T>;
@@ -111,11 +111,10 @@ struct Rows {
   // and settle moves them to their places
   template <bool TINY>  // rows may be shorter than a chunk
   static __device__ __forceinline__ u32x4 load_ahead(const T* row, uint32_t c, int d) {
-    const T* p = (const T*)((const char*)row + c * (uint32_t)sizeof(T));
     if ((int)c >= d) return u32x4{0, 0, 0, 0};
-    if (!TAIL) return load16(p);
-    if (TINY && d < K::C) return K::load(p, d - (int)c);
-    return load16(p - max((int)c + K::C - d, 0));
+    if (TINY && TAIL && d < K::C) return K::load(row, d);
+    const uint32_t from = TAIL ? min(c, (uint32_t)(d - K::C)) : c;
+    return load16((const char*)row + from * (uint32_t)sizeof(T));
   }
   // `end`: the column behind the G chunks that c's is one of
   template <bool TINY>
