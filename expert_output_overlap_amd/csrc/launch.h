@@ -173,7 +173,7 @@ int launch_adamw(const AdamwStep& a, int64_t n_chunks, bool read, hipStream_t st
 struct ResidualLaunch {
   int64_t rows, x_stride, h_stride, s_stride, n_stride, ds_stride, dn_stride, dx_stride, dh_stride;
   int d, dtype, param_dtype, post, pre;
-  bool backward;
+  bool backward, past;  // past: launch_residual's
   float eps, rho;
   moe_residual_norm_params p;
   const void *x, *h, *ds, *dn;
