@@ -8,7 +8,7 @@ namespace {
 
 // What a workgroup hands to another one inside the launch goes out with device-scope stores, which write through to the level that the
 // XCDs share, and is read with device-scope loads, past the caches that may hold an older call's: no cache has to be written back
-// or emptied (with such fences in every workgroup, the router's losses of 16384 x 256 logits by 256 of them took 65 us instead of ROUTER_US)
+// or emptied (with such fences in every workgroup, the router's losses of 16384 x 256 logits by 256 of them took 65 us instead of 24)
 template <class V>
 __device__ __forceinline__ void hand_out(V* p, V v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -2,7 +2,10 @@
 //
 // Both are bound by HBM: forward 4 row transfers per row, backward 6.  A row is held in registers by a group of G threads, NV
 // 16-byte chunks each, and is read once; a norm's variance is the mean of squared differences to the mean.  The gate and N1's
-// parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).
+// parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).  Rows stay as they
+// were loaded (bf16 pairs) and are unpacked where they are used, which is what lets 1024 threads of 128 registers hold a backward row of
+// 8192, its parameters, its sums and the next row's loads.
+// 16384 x 7168 bf16, RMS norms and gate: forward 189 us (4.97 TB/s), backward 286 (4.93); layer norms with biases 220 and 315.
 #include <algorithm>
 #include <type_traits>
 
