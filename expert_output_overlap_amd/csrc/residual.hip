@@ -222,13 +222,28 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
       param_chunk<C>(a.p.pre_bias, pb, (j * G + t) * C, d, 0.f, b);
     }
   };
+  constexpr bool AHEAD = !SHARED && NV <= 2;  // the next row's loads go out before the current row's sums
+  u32x4 nh[AHEAD ? NV : 1], nx[AHEAD ? NV : 1];
+  const int64_t step = (int64_t)gridDim.x * PER;
+  int64_t r = (int64_t)blockIdx.x * PER + (G < 64 ? threadIdx.x / G : SHARED ? wave_of() : 0);
+  auto fetch = [&](int64_t row, u32x4* h, u32x4* x) {
+    R::template load_all<G, NV>(a.h, row, a.h_stride, t, d, h);
+    R::template load_all<G, NV>(a.x, row, a.x_stride, t, d, x);
+  };
+  if (AHEAD && r < a.rows) fetch(r, nh, nx);
   int turn = 0;
   bool first = true;
-  for (int64_t r = (int64_t)blockIdx.x * PER + (G < 64 ? threadIdx.x / G : SHARED ? wave_of() : 0); r < a.rows; r += (int64_t)gridDim.x * PER) {
+  for (; r < a.rows; r += step) {
     u32x4 h[NV], x[NV];
     if (SHARED) asm volatile("" : "+v"(here));
-    R::template load_all<G, NV>(a.h, r, a.h_stride, t, d, h);
-    R::template load_all<G, NV>(a.x, r, a.x_stride, t, d, x);
+    if (AHEAD) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        h[j] = nh[AHEAD ? j : 0];
+        x[j] = nx[AHEAD ? j : 0];
+      }
+      if (r + step < a.rows) fetch(r + step, nh, nx);
+    } else fetch(r, h, x);
     if (HELD && first) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -595,7 +610,7 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
 int backward_threads(int d, int dtype, bool bias) {
   if (d > 8192) return 1024;
   if (d > 4096) return (dtype == MOE_BF16) == bias ? 512 : 1024;
-  int G = d <= 128 ? 16 : 64;
+  int G = 16;
   while (G * 8 < d) G *= 2;
   return G;
 }
@@ -638,6 +653,7 @@ void backward(const ResidualLaunch& a, bool bias, int64_t groups, hipStream_t st
   else if (G == 256) both(integral_constant<int, 256>{}, one{}, none{});
   else if (G == 128) both(integral_constant<int, 128>{}, one{}, none{});
   else if (G == 64) both(integral_constant<int, 64>{}, one{}, none{});
+  else if (G == 32) both(integral_constant<int, 32>{}, one{}, none{});
   else both(integral_constant<int, 16>{}, one{}, none{});
 }
 

@@ -112,20 +112,21 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* buf) {
 }
 
 // As group_sum for N <= 4, with fewer registers: the waves' sums meet in lanes of one wave, 16 to a value, instead of one register
-// each (48 for the three values of 16 waves); and for G = 16, four groups in a wave.
+// each (48 for the three values of 16 waves); and for G = 16 and 32, several groups in a wave.
 template <int G, int N>
 __device__ __forceinline__ void group_total(float (&v)[N], float* buf) {
   static_assert(N <= 4 && G <= 1024, "16 lanes to a value");
   auto dpp = [](float x, auto ctrl) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xf, 0xf, true));
   };
-  if (G == 16) {  // lane ^ 1, lane ^ 2, then the halves mirrored
+  if (G < 64) {  // lane ^ 1, lane ^ 2, then the halves mirrored, then lane ^ 16
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       v[n] += dpp(v[n], std::integral_constant<int, 0xB1>{});
       v[n] += dpp(v[n], std::integral_constant<int, 0x4E>{});
       v[n] += dpp(v[n], std::integral_constant<int, 0x141>{});
       v[n] += dpp(v[n], std::integral_constant<int, 0x140>{});
+      if (G == 32) v[n] += __shfl_xor(v[n], 16, 64);
     }
     return;
   }

@@ -171,11 +171,12 @@ def _need(t: torch.Tensor, name: str, shape: tuple, dtype, device, strided=False
     if t.dtype is not dtype or t.device != device or t.shape != shape:
         raise ValueError("%s: %s %s on %s, wanted %s %s on %s" % (name, t.dtype, tuple(t.shape), t.device, dtype, tuple(shape),
                                                                   device))
-    if strided:
-        if t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
-            raise ValueError("%s: rows must hold their elements side by side and not overlap" % name)
-    elif not t.is_contiguous():
+    if t.is_contiguous():
+        return
+    if not strided:
         raise ValueError("%s: not contiguous" % name)
+    if t.stride(1) != 1 and t.shape[1] > 1 or t.stride(0) < t.shape[1] and t.shape[0] > 1:
+        raise ValueError("%s: rows must hold their elements side by side and not overlap" % name)
 
 
 def _first(t: torch.Tensor, n: int) -> torch.Tensor:
