@@ -181,7 +181,7 @@ struct ResidualLaunch {
   float* stats;  // [rows][4]: mean and rstd of h, then of s
   void *d_post_weight, *d_post_bias, *d_gate, *d_pre_weight, *d_pre_bias;
   float* d_row_gate;
-  float* partial;  // backward: the workgroups' sums, or null where no [d] gradient is wanted
+  float* partial;  // backward: the workgroups' sums; not null where a [d] gradient is wanted, and only there
 };
 int64_t residual_partial_floats(int64_t rows, int d, int dtype);
 int launch_residual(const ResidualLaunch& a, hipStream_t st);

@@ -303,8 +303,31 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
   }
 }
 
+// Column c's gradients from its sums u1 of c D h^, u0 of c D (N1's, and the gate's), or of dn s^ and dn (N2's)
+__device__ __forceinline__ void put_params(const ResidualLaunch& a, bool pre, int c, float u1, float u0) {
+  const bool bf16 = a.param_dtype == MOE_BF16;
+  auto param = [&](const void* p, float empty) {
+    return !p ? empty : bf16 ? bf16_to_f32(((const bf16_t*)p)[c]) : ((const float*)p)[c];
+  };
+  auto put = [&](void* p, float v) {
+    if (!p) return;
+    if (bf16) ((bf16_t*)p)[c] = f32_to_bf16(v);
+    else ((float*)p)[c] = v;
+  };
+  if (pre) {
+    put(a.d_pre_weight, u1);
+    put(a.d_pre_bias, u0);
+    return;
+  }
+  const float gate = param(a.p.gate, 1.f);
+  put(a.d_post_weight, gate * u1);
+  put(a.d_post_bias, gate * u0);
+  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), u1, param(a.p.post_bias, 0.f) * u0));
+}
+
 // dx and dh of a group's rows, and its sums of c D h^ and dn s^ (SUMS = 4: also of c D and dn), which stay in registers over all of its
-// rows, as the parameters do, and go to the workspace at the end: partial [workgroup][SUMS][d].  WIDE, where registers do not hold all
+// rows, as the parameters do, and go to the workspace at the end: partial [workgroup][SUMS][d]; a workgroup that is alone writes the
+// parameters' gradients itself (where d <= 4096: in the wider rows' kernels that code costs the loop registers).  WIDE, where registers do not hold all
 // that: the first two sums are in LDS, each thread's for itself, and the parameters are read (from the L2) for each row.
 template <typename T, int G, int NV, int SUMS, bool WIDE, bool TAIL>
 __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaunch a) {
@@ -487,20 +510,28 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
         for (int e = 0; e < E; ++e) acc[k][e] += from[(k * E + e) * G + t];
     }
   }
+  auto sum = [&](int k, int e) { return !WIDE ? acc[WIDE ? 0 : k][e] : k < 2 ? sums[(k * E + e) * G + t] : acc[REGS > 0 && WIDE ? k - 2 : 0][e]; };
+  auto col = [&](int e) { return (e / C * G + t) * C + e % C; };
+  if (E == 8 && G <= 512 && gridDim.x == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (col(e) < d) {
+        put_params(a, false, col(e), sum(0, e), BIAS ? sum(BIAS ? 2 : 0, e) : 0.f);
+        put_params(a, true, col(e), sum(1, e), BIAS ? sum(SUMS - 1, e) : 0.f);
+      }
+    return;
+  }
   float* out = a.partial + (int64_t)blockIdx.x * SUMS * d;
 #pragma unroll
   for (int k = 0; k < SUMS; ++k)
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int c = (e / C * G + t) * C + e % C;
-      if (c < d) out[(int64_t)k * d + c] = !WIDE ? acc[k][e] : k < 2 ? sums[(k * E + e) * G + t] : acc[REGS > 0 ? k - 2 : 0][e];
-    }
+    for (int e = 0; e < E; ++e)
+      if (col(e) < d) out[(int64_t)k * d + col(e)] = sum(k, e);
 }
 
 // The parameters' gradients from the workgroups' partial sums, `sums` of them in each: {c D h^, dn s^} or {c D h^, dn s^, c D, dn}.  64
 // columns of N1's (y = 0) or of N2's (1) per workgroup; its 16 waves take every 16th partial row, eight in flight, and their sums are
 // added in wave order.
-template <typename PT>
 __global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int n, int sums) {
   __shared__ float red[15][2][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, d = a.d, pre = blockIdx.y;
@@ -531,24 +562,7 @@ __global__ __launch_bounds__(1024) void k_residual_params(ResidualLaunch a, int 
     s[0] += red[k][0][lane];
     s[1] += red[k][1][lane];
   }
-  auto param = [&](const void* p, float empty) {
-    if (!p) return empty;
-    return sizeof(PT) == 4 ? ((const float*)p)[c] : bf16_to_f32(((const bf16_t*)p)[c]);
-  };
-  auto put = [&](void* p, float v) {
-    if (!p) return;
-    if (sizeof(PT) == 4) ((float*)p)[c] = v;
-    else ((bf16_t*)p)[c] = f32_to_bf16(v);
-  };
-  if (pre) {
-    put(a.d_pre_weight, s[0]);
-    put(a.d_pre_bias, s[1]);
-    return;
-  }
-  const float gate = param(a.p.gate, 1.f);
-  put(a.d_post_weight, gate * s[0]);
-  put(a.d_post_bias, gate * s[1]);
-  put(a.d_gate, fmaf(param(a.p.post_weight, 1.f), s[0], param(a.p.post_bias, 0.f) * s[1]));
+  put_params(a, pre, c, s[0], s[1]);
 }
 
 int chunks_of(int d, int dtype) { return (d * (dtype == MOE_BF16 ? 2 : 4) + 15) / 16; }
@@ -618,7 +632,8 @@ int groups_in_block(int G) { return G <= 64 ? 256 / G : 1; }
 
 // Groups of a launch: four rows for each one's sums, while that leaves one for every CU, and no more than fill the chip (1000 x 7168 bf16:
 // 34 us by 256 groups, 41 by 128, 49 by 512; 10000 x 1024: 121, 67, 50 and 39 by 128, 256, 512 and 1024)
-int64_t backward_groups(int64_t rows, int G) {
+int64_t backward_groups(int64_t rows, int d, int G) {
+  if (d <= 4096 && rows <= 4 * groups_in_block(G)) return std::min<int64_t>(rows, groups_in_block(G));  // one workgroup: one launch
   return std::min<int64_t>(std::max<int64_t>(rows / 4, std::min<int64_t>(rows, 256)), 256 * 1024 / G);
 }
 
@@ -664,7 +679,7 @@ int64_t residual_partial_floats(int64_t rows, int d, int dtype) {
   for (const bool bias : {false, true}) {
     const int G = backward_threads(d, dtype, bias);
     const int64_t per = groups_in_block(G);
-    most = std::max(most, (backward_groups(rows, G) + per - 1) / per * (bias ? 4 : 2) * d);
+    most = std::max(most, (backward_groups(rows, d, G) + per - 1) / per * (bias ? 4 : 2) * d);
   }
   return most;
 }
@@ -687,18 +702,15 @@ int launch_residual(const ResidualLaunch& of, hipStream_t st) {
   // sums of c D and dn too, for the biases' gradients and post_bias's part of the gate's
   const bool bias = a.p.post_bias || a.d_post_bias || a.d_pre_bias;
   const int G = backward_threads(a.d, a.dtype, bias);
-  const int64_t groups = backward_groups(a.rows, G), per = groups_in_block(G);
+  const int64_t groups = backward_groups(a.rows, a.d, G), per = groups_in_block(G);
   if (a.rows > 0) {
     if (tb && tail) backward<bf16_t, true>(a, bias, groups, st);
     else if (tb) backward<bf16_t, false>(a, bias, groups, st);
     else if (tail) backward<float, true>(a, bias, groups, st);
     else backward<float, false>(a, bias, groups, st);
   }
-  if (a.d_post_weight || a.d_post_bias || a.d_gate || a.d_pre_weight || a.d_pre_bias) {
-    const int n = (int)((groups + per - 1) / per);
-    const dim3 grid((unsigned)((a.d + 63) / 64), 2);
-    if (a.param_dtype == MOE_BF16) hipLaunchKernelGGL(k_residual_params<bf16_t>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
-    else hipLaunchKernelGGL(k_residual_params<float>, grid, dim3(1024), 0, st, a, n, bias ? 4 : 2);
-  }
+  const int n = (int)((groups + per - 1) / per);
+  if ((a.d_post_weight || a.d_post_bias || a.d_gate || a.d_pre_weight || a.d_pre_bias) && !(n == 1 && a.d <= 4096))
+    hipLaunchKernelGGL(k_residual_params, dim3((unsigned)((a.d + 63) / 64), 2), dim3(1024), 0, st, a, n, bias ? 4 : 2);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }

@@ -79,7 +79,7 @@ def residual_check(got, want, tag):
         within(got[k], *want[k], (tag, k))
 
 
-SIZES = [(1, 64), (1, 7168), (3, 1), (5, 7), (17, 65), (300, 512), (70, 513), (33, 1024), (40, 1407), (64, 2048), (9, 2049),
+SIZES = [(2, 64), (16, 100), (64, 120), (65, 120), (33, 200), (16, 400), (17, 400), (4, 1000), (5, 1000), (4, 4096), (3, 4097), (1, 64), (1, 7168), (3, 1), (5, 7), (17, 65), (300, 512), (70, 513), (33, 1024), (40, 1407), (64, 2048), (9, 2049),
          (700, 4096), (21, 7168), (2000, 5000), (13, 8192), (7, 8193), (6, 16383), (5, 16384), (9000, 96)]
 
 
