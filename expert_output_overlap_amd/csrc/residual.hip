@@ -5,7 +5,7 @@
 // parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).  Rows stay as they
 // were loaded (bf16 pairs) and are unpacked where they are used, which is what lets 1024 threads of 128 registers hold a backward row of
 // 8192, its parameters, its sums and the next row's loads.
-// 16384 x 7168 bf16, RMS norms and gate: forward 189 us (4.97 TB/s), backward 286 (4.93); layer norms with biases 220 and 315.
+// 16384 x 7168 bf16, RMS norms and gate: forward 189 us (4.97 TB/s), backward 285 (4.94); layer norms with biases 209 and 311.
 #include <algorithm>
 #include <type_traits>
 
@@ -589,9 +589,9 @@ template <typename T, bool TAIL>
 void forward(const ResidualLaunch& a, hipStream_t st) {
   const int chunks = chunks_of(a.d, a.dtype);
   // A wave to a row (a quarter of one to rows of up to 32 chunks) where it can hold one and there are rows for all of eight waves on each CU:
-  // 16384 x 7168 bf16 195 us (4.8 TB/s), by 256 or 1024 threads 250; 65536 x 96 13 us, by whole waves 36.  Fewer rows by a thread to a chunk:
+  // 16384 x 7168 bf16 189 us (5.0 TB/s), by 256 or 1024 threads 250; 65536 x 96 13 us, by whole waves 36.  Fewer rows by a thread to a chunk:
   // 24 x 4096 bf16 6.0 us, by half as many threads 7.8; 1000 x 7168 17.5, by a wave to a row 19.3.  Rows of more than 1024 chunks by 1024
-  // threads: 8192 x 16384 bf16 258 us, by 512 373, by 256 (which spill) 714
+  // threads: 8192 x 16384 bf16 243 us, by 512 373, by 256 (which spill) 714
   const int wave = a.rows < 2048 ? 0 : chunks <= 32 ? 16 : chunks <= 1024 ? 64 : 0;
   const int G = wave ? wave : chunks <= 256 ? 256 : chunks <= 512 ? 512 : 1024;
   const int nv = per_thread(chunks, G);
@@ -619,8 +619,8 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
 
 // The threads of the backward's groups.  Eight elements in a thread while registers hold what
 // belongs to them: up to 1024 threads with two sums in bf16.  With four, or in fp32, 512 threads of sixteen (16384 x 7168 bf16, four sums:
-// 320 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 285 and 310), but WIDE in fp32 with four (418; 726 and 887 otherwise);
-// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 513 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
+// 311 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 278 and 310), but WIDE in fp32 with four (366; 726 and 887 otherwise);
+// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 507 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
 int backward_threads(int d, int dtype, bool bias) {
   if (d > 8192) return 1024;
   if (d > 4096) return (dtype == MOE_BF16) == bias ? 512 : 1024;
