@@ -1,9 +1,10 @@
 // The global norm of many gradients, and clipping (formulas in include/moe_overlap.h).
 //
 // Both are bound by HBM: 138.5 million gradients' norm takes 42 us in bf16 (6.6 TB/s, a part of them still in the last-level cache) and
-// 94 in fp32 (5.9); clipped from fp32 into bf16 another 126 (6.6 TB/s of 6 bytes read and written per element).  The tensors are cut into chunks of GRAD_CHUNK elements, each a record of the plan's table with its own
-// address, so that a launch of many small tensors has no search; a workgroup takes every grid-th chunk.  A square and its sum are
-// one fp64 instruction each on this chip at the fp32 rate: they hide behind the loads and need no care for the gradients' range.
+// 94 in fp32 (5.9); clipped from fp32 into bf16 another 126 (6.6 TB/s of 6 bytes read and written per element).  The tensors are cut
+// into chunks of GRAD_CHUNK elements, each a record of the plan's table with its own address, so that a launch of many small tensors
+// has no search; a workgroup takes every grid-th chunk.  A square and its sum are one fp64 instruction on this chip, at the fp32 rate:
+// they hide behind the loads and need no care for the gradients' range.
 #include <algorithm>
 
 #include "common.h"
@@ -116,7 +117,7 @@ __device__ __forceinline__ void scaled(const GradChunk& k, void* to, float f) {
     else {
       uint32_t q[C / 2];
 #pragma unroll
-      for (int i = 0; i < C / 2; ++i) q[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)w[2 * i + 1]) << 16);
+      for (int i = 0; i < C / 2; ++i) q[i] = bf16_bits(w[2 * i]) | bf16_bits(w[2 * i + 1]) << 16;
       put<2 * C>(out + at, q);
     }
   }

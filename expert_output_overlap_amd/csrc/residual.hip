@@ -12,6 +12,7 @@
 #include "common.h"
 #include "launch.h"
 #include "row_util.h"
+#include "tile_util.h"
 
 namespace {
 
@@ -149,7 +150,7 @@ struct Rows {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (sizeof(T) == 4) v[i] = __float_as_uint(f[i]);
-      else v[i] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * i]) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f[2 * i + 1]) << 16);
+      else v[i] = bf16_bits(f[2 * i]) | bf16_bits(f[2 * i + 1]) << 16;
     }
     return v;
   }

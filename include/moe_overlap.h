@@ -661,7 +661,7 @@ int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, 
 /* norm, scale (device) fp32 [1], written; max_norm > 0 (or infinite), factor > 0, both representable in fp32. */
 int moe_grad_norm(const moe_grad_plan* plan, double max_norm, double factor, float* norm, float* scale, void* stream);
 
-/* out = g times *scale (device), each rounded once; in place nothing is touched where *scale is 1. */
+/* out = g times *scale (device), in fp32 and then rounded to out's type; in place nothing is touched where *scale is 1. */
 int moe_grad_clip(const moe_grad_plan* plan, const float* scale, void* stream);
 
 /* While enabled (nonzero), every moe_expert_ffn_overlap and moe_expert_ffn_backward call of this process times
