@@ -1,7 +1,9 @@
 // The norms around a block with its gate and the residual's scale, forward and backward (formulas in include/moe_overlap.h).
 //
 // Both are bound by HBM: forward 4 row transfers per row, backward 6.  A row is held in registers by a group of G threads, NV
-// 16-byte chunks each, and is read once; a norm's variance is the mean of squared differences to the mean.  The gate and N1's
+// 16-byte chunks each, and is read once; a norm's variance is the mean of squared differences to the mean, and v^ = (v - mean) rstd from
+// the difference too: as one product, v rstd - mean rstd, it would carry the rounding of mean rstd, in every element of a row, which
+// for a row of equal elements is over sqrt(eps) and not 0.  The gate and N1's
 // parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).  Rows stay as they
 // were loaded (bf16 pairs) and are unpacked where they are used, which is what lets 1024 threads of 128 registers hold a backward row of
 // 8192, its parameters, its sums and the next row's loads.
@@ -265,7 +267,6 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
     };
     row_stats<G, NV, C, TAIL>(of_h, a.post, t, d, a.eps, red, turn, &m1, &r1);
     T* to = (T*)a.s + r * a.s_stride;
-    const float o1 = -m1 * r1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) forget(h[j]);
 #pragma unroll
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
       const int at = (j * G + t) * C;
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const float z = fmaf(fmaf(K::at(h[j], i), r1, o1), w[i], b[i]);
+        const float z = fmaf((K::at(h[j], i) - m1) * r1, w[i], b[i]);
         s[j * C + i] = at + (TAIL ? i : 0) < d ? fmaf(a.rho, K::at(x[j], i), c * z) : 0.f;
       }
       R::store(to, at, d, s + j * C, a.past);
@@ -288,7 +289,6 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
     row_stats<G, NV, C, TAIL>(of_s, a.pre, t, d, a.eps, red, turn, &m2, &r2);
     if (a.pre != MOE_NORM_NONE) {
       to = (T*)a.n + r * a.n_stride;
-      const float o2 = -m2 * r2;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         float w[C], b[C];
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
         weights(1, j, w, b);
         const int at = (j * G + t) * C;
 #pragma unroll
-        for (int i = 0; i < C; ++i) w[i] = fmaf(fmaf(s[j * C + i], r2, o2), w[i], b[i]);
+        for (int i = 0; i < C; ++i) w[i] = fmaf((s[j * C + i] - m2) * r2, w[i], b[i]);
         R::store(to, at, d, w, a.past);
       }
     }
@@ -336,6 +336,9 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
   using R = Rows<T, TAIL>;
   constexpr int C = K::C, PER = G <= 64 ? 256 / G : 1, E = NV * C, HELD = WIDE ? C : E, REGS = WIDE ? SUMS - 2 : SUMS;
   constexpr bool BIAS = SUMS == 4, AHEAD = !WIDE;  // AHEAD: registers hold the next row too
+  // h's and x's registers take the differences to the means (4096 x 16384 fp32, two sums: 422 us, made anew in each pass 467; with four sums
+  // 852, made anew 761)
+  constexpr bool KEEP = WIDE && sizeof(T) == 4 && SUMS == 2;
   extern __shared__ float sums[];  // WIDE: [2][E][G]
   __shared__ float red[2][3 * (G / 64) + 1];
   __shared__ float join[PER > 1 ? (PER - 1) * SUMS * E * G : 1];
@@ -396,12 +399,18 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
     R::template settle_all<G, NV>(t, d, g);
     R::template settle_all<G, NV>(t, d, q);
     const float4 st = nst;
-    const float c = nc, r1 = st.y, o1 = -st.x * r1, r2 = st.w, o2 = -st.z * r2;
+    const float c = nc, m1 = st.x, r1 = st.y, m2 = st.z, r2 = st.w;
     if (AHEAD && r + step < a.rows) fetch(r + step);
-    // of element i of chunk j, whose parameters are held from p on
-    auto n1 = [&](int j, int i) { return fmaf(K::at(h[j], i), r1, o1); };
+    if (KEEP) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < C; ++i) h[j][i] = __float_as_uint(__uint_as_float(h[j][i]) - m1);
+    }
+    // of element i of chunk j, whose parameters are held from p on: differences to the means, v^ = e rstd
+    auto e1 = [&](int j, int i) { return KEEP ? K::at(h[j], i) : K::at(h[j], i) - m1; };
     auto z = [&](int p, int i, float n) { return BIAS ? fmaf(n, A[p + i], B[p + i]) : n * A[p + i]; };
-    auto n2 = [&](int j, int p, int i, float n) { return fmaf(fmaf(a.rho, K::at(x[j], i), c * z(p, i, n)), r2, o2); };
+    auto e2 = [&](int j, int p, int i, float n) { return fmaf(a.rho, K::at(x[j], i), c * z(p, i, n)) - m2; };
     float ma = 0.f, mn = 0.f;
     if (pre) {
       float v[2] = {0.f, 0.f};
@@ -414,11 +423,12 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-          const float n = n2(j, p, i, n1(j, i)), y = K::at(q[j], i), w = y * W[p + i];
+          const float e = e2(j, p, i, e1(j, i) * r1), n = e * r2, y = K::at(q[j], i), w = y * W[p + i];
           grow(1, j * C + i, y, n);
           if (BIAS) grow(3, j * C + i, 1.f, y);
           v[0] += w;
           v[1] = fmaf(w, n, v[1]);
+          if (KEEP) x[j][i] = __float_as_uint(e);
         }
       }
       group_total<G>(v, red[turn]);
@@ -435,7 +445,7 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       }
     }
     if (WIDE) asm volatile("" : "+v"(here));
-    float D[E], v[3] = {0.f, 0.f, 0.f};
+    float D[E], v[3] = {0.f, 0.f, 0.f}, k = r2 * mn;
     T* to = (T*)a.dx + r * a.dx_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -448,7 +458,8 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       if (pre) {
 #pragma unroll
         for (int i = 0; i < C; ++i)
-          y[i] = fmaf(r2, fmaf(-n2(j, p, i, n1(j, i)), mn, fmaf(K::at(q[j], i), W[p + i], -ma)), K::at(g[j], i));
+          y[i] = fmaf(r2, fmaf(-(KEEP ? K::at(x[j], i) : e2(j, p, i, e1(j, i) * r1)), k, fmaf(K::at(q[j], i), W[p + i], -ma)),
+                      K::at(g[j], i));
       } else {
 #pragma unroll
         for (int i = 0; i < C; ++i) y[i] = K::at(g[j], i);
@@ -456,7 +467,7 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       float o[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) {
-        const float n = n1(j, i);
+        const float n = e1(j, i) * r1;
         if (at + (TAIL ? i : 0) >= d) y[i] = 0.f;
         o[i] = a.rho * y[i];
         v[2] = fmaf(y[i], z(p, i, n), v[2]);
@@ -478,14 +489,14 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
 #pragma unroll
       for (int j = 0; j < NV; ++j) forget(h[j]);
     ma = a.post == MOE_NORM_LAYER ? v[0] / d : 0.f;
-    mn = a.post == MOE_NORM_NONE ? 0.f : v[1] / d;
+    k = a.post == MOE_NORM_NONE ? 0.f : r1 * (r1 * (v[1] / d));
     to = (T*)a.dh + r * a.dh_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int at = (j * G + t) * C;
       float o[C];
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] = r1 * fmaf(-n1(j, i), mn, D[j * C + i] - ma);
+      for (int i = 0; i < C; ++i) o[i] = fmaf(-e1(j, i), k, r1 * (D[j * C + i] - ma));
       R::store(to, at, d, o, a.past);
     }
     if (t == 0 && a.d_row_gate) a.d_row_gate[r] = v[2];

@@ -240,6 +240,70 @@ def test_residual_norm_of_constant_and_bad_rows():
     assert (got["dh"].double() - 1e-5 ** -0.5).abs().max() < 1e-3 * 1e-5 ** -0.5
 
 
+# a group of 16 lanes, a wave of one and of sixteen chunks a lane, workgroups of every size, odd widths, rows in LDS in the backward
+LEVEL_SIZES = [(2100, 96), (2100, 100), (2051, 1000), (2048, 7168), (20, 33), (30, 512), (30, 1407), (30, 4096), (30, 7168), (9, 8200),
+               (6, 16384)]
+
+
+@pytest.mark.parametrize("rows,d", LEVEL_SIZES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_of_equal_elements_is_its_bias(rows, d, dtype):
+    """A row of equal elements v has v^ = 0, whatever v is: the row sum's rounding leaves the mean by at most ROW |v| off, the
+    differences are exact and their mean corrects it to that share of itself, less than half a step of v.  So s, n and the weights'
+    gradients, which are sums of v^, are what the biases alone make; the variance is off by at most 3 ROW (ROW v)^2, against eps."""
+    rnd, dt, eps = gen(rows + d), DT[dtype], 1e-5
+    v = torch.tensor([3.25, 1000.3, 30000.0, -700.7, 1e-3], device="cuda").repeat(rows)[:rows, None].expand(rows, d).to(dt)
+    w = {"post_weight": 1 + 0.2 * rnd(d), "post_bias": 0.1 * rnd(d), "gate": 1 + 0.2 * rnd(d)}
+    t = dict(x=rnd(rows, d).to(dt), h=v.contiguous(), w=w, row_gate=torch.sigmoid(rnd(rows)), ds=rnd(rows, d).to(dt), dn=None)
+    _, got = residual_run(t, dict(post="layer", pre="none", residual_scale=RHO))
+    W = {k: x.to(D) for k, x in w.items()}
+    c, x, ds, r = t["row_gate"].to(D)[:, None], t["x"].to(D), t["ds"].to(D), half_step(dt)
+    part = c * W["gate"] * W["post_bias"]
+    s = RHO * x + part
+    within(got["s"], s, 4 * E32 * part.abs() + 2 * E32 * ((RHO * x).abs() + s.abs()) + r * s.abs(), "s")
+    assert (got["post_weight"] == 0).all()
+    u0, e_u0 = (c * ds).sum(0), ((rows + 12) * E32 * (c * ds).abs()).sum(0)
+    within(got["post_bias"], W["gate"] * u0, W["gate"].abs() * (e_u0 + 2 * E32 * u0.abs()), "post_bias")
+    within(got["gate"], W["post_bias"] * u0, W["post_bias"].abs() * (e_u0 + 2 * E32 * u0.abs()), "gate")
+    a = c * W["gate"] * W["post_weight"] * ds
+    zero, e_r = torch.zeros_like(a), 1.5 * ref.ROW * (ref.ROW * v[:, :1].to(D)) ** 2 / eps + 8 * E32
+    dh, e = ref.norm_back(a, 4 * E32 * a.abs(), zero, zero, torch.full_like(a[:, :1], eps ** -0.5), e_r, "layer")
+    within(got["dh"], dh, e + r * dh.abs(), "dh")
+    # in front of the next block: s = v up to a factor
+    w = {"pre_weight": 1 + 0.2 * rnd(d), "pre_bias": 0.1 * rnd(d)}
+    t = dict(x=v.contiguous(), h=torch.zeros_like(t["h"]), w=w, row_gate=None, ds=None, dn=t["ds"])
+    _, got = residual_run(t, dict(post="none", pre="layer", residual_scale=RHO))
+    assert torch.equal(got["n"], w["pre_bias"].to(dt).expand(rows, d)) and (got["pre_weight"] == 0).all()
+    within(got["pre_bias"], ds.sum(0), ((rows + 12) * E32 * ds.abs()).sum(0), "pre_bias")
+
+
+@pytest.mark.parametrize("rows,d", LEVEL_SIZES)
+@pytest.mark.parametrize("dtype,level", [("bf16", 200.0), ("f32", 1000.0)])
+def test_layer_norm_far_from_zero(rows, d, dtype, level):
+    """Rows of level - 1 and level + 1 in equal numbers (and one of the level itself where d is odd): the row's sum, mean, differences and
+    their squares are exact, so v^ = (v - mean) rstd is off by the roundings of rstd and of one product alone, 8 E32 of itself,
+    and not by steps of the level."""
+    rnd, dt = gen(rows + d), DT[dtype]
+    e = torch.ones(rows, d, device="cuda")
+    e[:, 1::2] = -1
+    if d % 2:
+        e[:, -1] = 0
+    v, zero = (level + e).to(dt), torch.zeros(rows, d, device="cuda", dtype=dt)
+    assert torch.equal(v.float(), level + e)
+    rstd = torch.full((rows, 1), (d // 2 * 2 / d + 1e-5) ** -0.5, dtype=D, device="cuda")
+    n, g, r, k = e.to(D) * rstd, rnd(rows, d).to(dt), half_step(dt), (rows + 12) * E32
+    for post, pre in (("layer", "none"), ("none", "layer")):
+        w = {"post_weight" if pre == "none" else "pre_weight": torch.ones(d, device="cuda")}
+        t = dict(x=zero if pre == "none" else v, h=v if pre == "none" else zero, w=w, row_gate=None, ds=g if pre == "none" else None,
+                 dn=None if pre == "none" else g)
+        _, got = residual_run(t, dict(post=post, pre=pre, residual_scale=1.0))
+        within(got["s" if pre == "none" else "n"], n, (8 * E32 + r) * n.abs(), (post, pre))
+        a = g.to(D)
+        back, e_b = ref.norm_back(a, 0 * a, n, 8 * E32 * n.abs(), rstd, torch.full_like(rstd, 8 * E32), "layer")
+        within(got["dh" if pre == "none" else "dx"], back, e_b + (E32 + r) * back.abs(), (post, pre))
+        within(got[next(iter(w))], (a * n).sum(0), ((k + 8 * E32) * (a * n).abs()).sum(0), (post, pre, "weight"))
+
+
 def test_residual_norm_gradients_against_differences():
     """A step e along a direction changes the loss by e times the gradient's product with it: central differences of the operator's own
     fp32 forward.  The loss is a sum of 2 x 6 x 40 products, each known to 40 E32 of its size or so (row sums of 40, some products);
