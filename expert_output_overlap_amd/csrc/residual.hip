@@ -485,9 +485,13 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
       group_total<G>(v, red[turn]);
       turn ^= 1;
     }
-    if (sizeof(T) == 2)
+    if (a.post == MOE_NORM_NONE) {  // dh = D: h may hold infinities, which no product with 0 takes away
 #pragma unroll
-      for (int j = 0; j < NV; ++j) forget(h[j]);
+      for (int j = 0; j < NV; ++j) h[j] = u32x4{0, 0, 0, 0};
+    }
+    // in fp32 too: else both of h's registers would be held (8192 x 7168, two sums: 326 us instead of 277)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) forget(h[j]);
     ma = a.post == MOE_NORM_LAYER ? v[0] / d : 0.f;
     k = a.post == MOE_NORM_NONE ? 0.f : r1 * (r1 * (v[1] / d));
     to = (T*)a.dh + r * a.dh_stride;

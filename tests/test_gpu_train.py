@@ -304,6 +304,34 @@ def test_layer_norm_far_from_zero(rows, d, dtype, level):
         within(got[next(iter(w))], (a * n).sum(0), ((k + 8 * E32) * (a * n).abs()).sum(0), (post, pre, "weight"))
 
 
+@pytest.mark.parametrize("rows,d", [(40, 100), (7, 1000), (2100, 96), (5, 5000), (5, 9000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pre", ["none", "rms"])
+def test_residual_norm_without_a_post_norm_keeps_bad_values_out_of_dh(rows, d, dtype, pre):
+    """Without N1, dh = c gate D, whatever h is: an infinity or a NaN in it reaches its row's other gradients through a pre norm alone, and
+    the gate's in its column.  Rows without one are as ever."""
+    t, kinds = residual_case(rows, d, dtype, "f32", "none", pre, RHO, row_gate=True, bias=False, seed=d)
+    bad = {0: (d - 1, float("inf")), 2: (0, float("nan")), 4: (d // 2, -float("inf"))}
+    for row, (col, value) in bad.items():
+        t["h"][row, col] = value
+    _, got = residual_run(t, kinds)
+    clean = {**t, "h": torch.where(torch.isfinite(t["h"]), t["h"], 1.0)}
+    want = residual_want(clean, kinds)
+    rest = [k for k in range(rows) if k not in bad]
+    for k in ("s", "dx", "dh", "row_gate"):
+        within(got[k][rest], want[k][0][rest], want[k][1][rest], k)
+    for row, (col, _) in bad.items():
+        assert not torch.isfinite(got["s"][row, col]) and not torch.isfinite(got["row_gate"][row])
+        assert not torch.isfinite(got["gate"][col])
+    cols = [k for k in range(d) if k not in [col for col, _ in bad.values()]]
+    if pre == "none":
+        for k in ("dx", "dh"):
+            within(got[k], want[k][0], want[k][1], k)
+        within(got["gate"][cols], want["gate"][0][cols], want["gate"][1][cols], "gate")
+    else:
+        assert not torch.isfinite(got["dh"][[0, 2, 4]]).any()
+
+
 def test_residual_norm_gradients_against_differences():
     """A step e along a direction changes the loss by e times the gradient's product with it: central differences of the operator's own
     fp32 forward.  The loss is a sum of 2 x 6 x 40 products, each known to 40 E32 of its size or so (row sums of 40, some products);
