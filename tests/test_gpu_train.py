@@ -566,6 +566,30 @@ def test_router_workspace_serves_other_calls():
             assert torch.equal(op.counts, own.counts) and torch.equal(op.means, own.means)
 
 
+@pytest.mark.parametrize("G", [2, 16, 60, 100, 250, 500, 1000])
+def test_router_experts_far_below_the_top(G):
+    """A slot's gradient of an expert x below its row's top logit: the others are so far down that the sum of exp is 1 to the last bit, and
+    the logit's gradient is p (1 - p) dw with p = exp(x), off by the exponential's two steps (2 E32 each) and three roundings: 8 E32 of
+    itself, however far down."""
+    from expert_output_overlap_amd.runtime import RouterLoss
+
+    T = 57
+    x = -(30.0 + torch.arange(T, device="cuda"))  # to exp(-86), above the smallest normal number
+    logits = torch.full((T, G), -float("inf"), device="cuda")
+    logits[:, 0] = 5.0
+    at = 1 + torch.arange(T, device="cuda") * 7 % (G - 1)
+    rows = torch.arange(T, device="cuda")
+    logits[rows, at] = 5.0 + x
+    idx, dw = at.int()[:, None].contiguous(), gen(G)(T, 1)
+    op = RouterLoss(T, G, 1, balance=0.0, z=0.0)
+    op.forward(logits, idx)
+    got = op.backward(logits, idx, dw)
+    p = torch.exp(x.to(D))
+    want = p * (1 - p) * dw[:, 0].to(D)
+    off = (got[rows, at].to(D) / want - 1).abs()
+    assert off.max() <= 8 * E32, (int(off.argmax()), off.max().item() / E32)
+
+
 def test_router_gradient_against_differences():
     """Central differences of the operator's own losses (fp32, 3 roundings of its size, its rows' products within 60 E32), and e^2
     of third derivatives of the order of the gradient."""
