@@ -462,8 +462,10 @@ __global__ __launch_bounds__(256) void k_router_bwd(RouterLaunch a, int rows) {
         } else {
           if (good) mine[id] = 0.f;
           wave_order();
-          for (int j = 0; j < K; ++j)
+          for (int j = 0; j < K; ++j) {
             if (l == j && good) mine[id] += w;
+            wave_order();  // for a lane by itself the loop is one addition: the next lane's comes after it
+          }
         }
         wave_order();
 #pragma unroll

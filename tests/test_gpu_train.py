@@ -590,6 +590,25 @@ def test_router_experts_far_below_the_top(G):
     assert off.max() <= 8 * E32, (int(off.argmax()), off.max().item() / E32)
 
 
+@pytest.mark.parametrize("G", [66, 128, 256, 500, 1024])
+def test_router_slots_of_one_expert_add_up(G):
+    """All slots of a row at one expert, in pairs, and one twice among others: the gradients add up whichever lanes hold them."""
+    from expert_output_overlap_amd.runtime import RouterLoss
+
+    T, k = 203, 16
+    logits, idx, _, dw = router_case(T, G, k, 1, False, seed=G)
+    idx[0::5] = idx[0::5, :1]
+    idx[1::5] = idx[1::5, :8].repeat(1, 2)
+    idx[2::5] = idx[2::5, :8].repeat_interleave(2, 1)
+    idx[3::5, 15] = idx[3::5, 0]
+    op = RouterLoss(T, G, k, z=1e-3)
+    op.forward(logits, idx)
+    got = op.backward(logits, idx, dw)
+    counts, want = ref.router_loss(logits, idx, 1, float(np.float32(0.01)), float(np.float32(1e-3)), None, dw)
+    assert torch.equal(op.counts, counts)
+    within(got, *want["dlogits"], "dlogits")
+
+
 def test_router_gradient_against_differences():
     """Central differences of the operator's own losses (fp32, 3 roundings of its size, its rows' products within 60 E32), and e^2
     of third derivatives of the order of the gradient."""
