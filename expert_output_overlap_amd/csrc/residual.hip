@@ -180,7 +180,7 @@ __global__ __launch_bounds__(SHARED ? 512 : G) void k_residual(ResidualLaunch a)
   using K = Chunk<T>;
   using R = Rows<T, TAIL>;
   constexpr int C = K::C, PER = SHARED ? 512 / G : 1, E = NV * C;
-  extern __shared__ float shared[];  // SHARED: A, pre_weight, then B and pre_bias where there is a bias; by four columns, then lanes
+  extern __shared__ __align__(16) float shared[];  // SHARED: A, pre_weight, then B and pre_bias where there is a bias; by four columns, then lanes
   __shared__ float red[2][2 * (G / 64) + 1];
   const int t = threadIdx.x % G, d = a.d;
   const bool pb = a.param_dtype == MOE_BF16, bias = a.p.post_bias || a.p.pre_bias;

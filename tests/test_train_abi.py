@@ -220,3 +220,20 @@ def test_router_workspace_serves_fewer_tokens(experts, sequences):
     sizes = [B.moe_router_loss_workspace_bytes(router_shape(tokens=sequences * t, experts=experts, top_k=1, sequences=sequences))
              for t in (0, 1, 7, 16, 100, 1000, 5000, 20000)]
     assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_dynamic_lds_is_aligned_to_its_vector_accesses():
+    """Dynamic LDS starts behind a kernel's static LDS, at its own type's alignment unless it is declared with more."""
+    import glob
+    import os
+    import re
+
+    seen = 0
+    for path in glob.glob(os.path.join(os.path.dirname(B.__file__), "csrc", "*.hip")):
+        text = open(path).read()
+        for m in re.finditer(r"extern __shared__ (__align__\((\d+)\) )?[\w ]+? (\w+)\[\];", text):
+            body = text[m.end(): text.find("extern __shared__", m.end())]
+            if re.search(r"\(const float4\*\)\(%s|\(float4\*\)\(%s" % (m.group(3), m.group(3)), body):
+                assert int(m.group(2) or 4) >= 16, (path, m.group(0))
+                seen += 1
+    assert seen > 0
