@@ -663,21 +663,27 @@ class MoeBlock:
         dn = p.bwd_buffers()["dx"][: p.T]
         return self.shared.backward(d_out, self.n, w["shared_gate_up"], w["shared_down"], residual=dn, dx=dn, stream=stream)
 
+    @staticmethod
+    def _made(op, name):
+        if op is None:
+            raise RuntimeError("made without %s=" % name)
+        return op
+
     def router_loss(self, logits, spans=None, stream=None):
         """{loss, B, Z} of the logits that ``experts`` took (and ``losses_op.counts``)."""
-        return self.losses_op.forward(logits, self.path.topk_idx[: self.path.T], spans, stream)
+        return self._made(self.losses_op, "losses").forward(logits, self.path.topk_idx[: self.path.T], spans, stream)
 
     def router_backward(self, logits, d_loss=None, spans=None, stream=None):
         """The logits' gradient: of the losses, and of the routing weights through the experts' outputs."""
         T = self.path.T
-        return self.losses_op.backward(logits, self.path.topk_idx[:T], self.path.bwd_buffers()["dw_route"][:T], d_loss, spans,
-                                       stream=stream)
+        op = self._made(self.losses_op, "losses")
+        return op.backward(logits, self.path.topk_idx[:T], self.path.bwd_buffers()["dw_route"][:T], d_loss, spans, stream=stream)
 
     def join(self, x, out, w, row_gate=None, stream=None):
-        return self.join_op.forward(x, out, w, row_gate, stream=stream)
+        return self._made(self.join_op, "join").forward(x, out, w, row_gate, stream=stream)
 
     def join_backward(self, ds, dn, x, out, w, row_gate=None, stream=None):
-        return self.join_op.backward(ds, dn, x, out, w, row_gate, stream=stream)
+        return self._made(self.join_op, "join").backward(ds, dn, x, out, w, row_gate, stream=stream)
 
     @_on_own_device
     def norm_backward(self, dn, x, w, residual=None, stream=None):

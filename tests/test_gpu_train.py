@@ -951,3 +951,14 @@ def test_block_with_losses_and_a_join_for_serving():
     for call in (lambda: b.router_backward(logits), lambda: b.join_backward(x, x, x, out, w)):
         with pytest.raises(RuntimeError, match="train"):
             call()
+
+
+def test_block_without_losses_or_a_join_says_so():
+    from expert_output_overlap_amd.runtime import MoeBlock, MoePath
+
+    b = MoeBlock(MoePath(1, 16, 4, 4, 2, 128, 128, 16), 64)
+    x = torch.zeros(16, 128, device="cuda", dtype=torch.bfloat16)
+    for call, name in ((lambda: b.router_loss(x), "losses"), (lambda: b.router_backward(x), "losses"), (lambda: b.join(x, x, {}), "join"),
+                       (lambda: b.join_backward(x, x, x, x, {}), "join")):
+        with pytest.raises(RuntimeError, match="made without %s=" % name):
+            call()
