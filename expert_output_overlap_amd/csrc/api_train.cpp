@@ -69,7 +69,8 @@ const char* check_router(const moe_router_shape* s) {
   if (s->top_k < 1 || s->top_k > std::min(s->experts, 16)) return "top_k must be in [1, min(G, 16)]";
   if (s->tokens < 0 || s->tokens > 1 << 30 || s->tokens * s->top_k >= 1ll << 31)
     return "tokens must be in [0, 2^30], tokens x top_k below 2^31";
-  if (s->sequences < 1 || (int64_t)s->sequences * s->experts >= (1ll << 31)) return "sequences must be >= 1, sequences x experts below 2^31";
+  if (s->sequences < 1 || s->sequences > 1 << 30 || (int64_t)s->sequences * s->experts >= (1ll << 31))
+    return "sequences must be in [1, 2^30], sequences x experts below 2^31";
   if (!is_dtype(s->dtype)) return "dtype must be MOE_BF16 or MOE_F32";
   if (!std::isfinite(s->balance) || !std::isfinite(s->z)) return "balance and z must be finite";
   return nullptr;

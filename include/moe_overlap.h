@@ -603,7 +603,7 @@ typedef struct {
   int64_t tokens;     /* T in [0, 2^30], T top_k < 2^31 */
   int32_t experts;    /* G, 1 .. 1024 */
   int32_t top_k;      /* 1 .. min(G, 16) */
-  int32_t sequences;  /* S >= 1, S G < 2^31 */
+  int32_t sequences;  /* S in [1, 2^30], S G < 2^31 */
   int32_t dtype;      /* moe_dtype of dlogits */
   float balance, z;   /* the losses' coefficients, finite */
 } moe_router_shape;

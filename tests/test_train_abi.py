@@ -128,6 +128,16 @@ def test_router_shapes(kw):
     assert B.lib().moe_router_backward(ctypes.byref(s), *P[:8], None) == B.MOE_EINVAL
 
 
+@pytest.mark.parametrize("sequences", [(1 << 30) + 1, (1 << 31) - 512, (1 << 31) - 4, (1 << 31) - 1])
+def test_router_sequences_that_the_kernels_cannot_count(sequences):
+    """One expert leaves the product below 2^31; the kernels step over the sequences in 32 bits, by up to 512 and from up to 2^30."""
+    s = router_shape(tokens=8, experts=1, top_k=1, sequences=sequences)
+    assert B.moe_router_loss_workspace_bytes(s) == -1
+    refused(B.lib().moe_router_loss(ctypes.byref(s), *P[:7], 1 << 60, None), "sequences")
+    refused(B.lib().moe_router_backward(ctypes.byref(s), *P[:8], None), "sequences")
+    assert B.moe_router_loss_workspace_bytes(router_shape(tokens=8, experts=1, top_k=1, sequences=1 << 30)) > 0
+
+
 def test_router_arguments():
     L, s = B.lib(), router_shape()
     need = B.moe_router_loss_workspace_bytes(s)
