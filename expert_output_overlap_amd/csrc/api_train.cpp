@@ -127,6 +127,15 @@ GradLaunch grad_of(const moe_grad_plan* p) {
   return a;
 }
 
+int64_t plan_bytes(int64_t n_chunks) {
+  return table_bytes(n_chunks) + 4 * grad_counter_words(n_chunks) + 8 * grad_partial_doubles(n_chunks);
+}
+
+// A device number of a call inside the plan's workspace, whose records hold addresses
+bool in_plan(const moe_grad_plan* p, const void* number) {
+  return meet(Span{p->table, plan_bytes(p->n_chunks)}, Span{number, 4});
+}
+
 }  // namespace
 
 extern "C" {
@@ -290,8 +299,7 @@ int moe_router_backward(const moe_router_shape* s, const float* logits, const in
 
 int64_t moe_grad_workspace_bytes(const moe_grad_tensor* t, int32_t n_tensors) {
   if (check_grads(t, n_tensors)) return -1;
-  const int64_t n = grad_chunks(t, n_tensors);
-  return table_bytes(n) + 4 * grad_counter_words(n) + 8 * grad_partial_doubles(n);
+  return plan_bytes(grad_chunks(t, n_tensors));
 }
 
 int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes, moe_grad_plan* plan,
@@ -351,6 +359,7 @@ int moe_grad_norm(const moe_grad_plan* plan, double max_norm, double factor, flo
   if (!norm || !scale) return moe_fail(MOE_EINVAL, "null pointer");
   if (off(norm, 4) || off(scale, 4)) return moe_fail(MOE_EINVAL, "a device number must be aligned to its size");
   if (norm == scale) return moe_fail(MOE_EINVAL, "an output overlaps another output");
+  if (in_plan(plan, norm) || in_plan(plan, scale)) return moe_fail(MOE_EINVAL, "an output overlaps the plan's workspace");
   GradLaunch a = grad_of(plan);
   a.max_norm = max_norm;
   a.factor = factor;
@@ -363,6 +372,7 @@ int moe_grad_clip(const moe_grad_plan* plan, const float* scale, void* stream) {
   if (const char* e = check_grad_plan(plan)) return moe_fail(MOE_EINVAL, e);
   if (!scale) return moe_fail(MOE_EINVAL, "null pointer");
   if (off(scale, 4)) return moe_fail(MOE_EINVAL, "a device number must be aligned to its size");
+  if (in_plan(plan, scale)) return moe_fail(MOE_EINVAL, "scale overlaps the plan's workspace");
   GradLaunch a = grad_of(plan);
   a.scale = (float*)scale;
   return launch_grad_clip(a, (hipStream_t)stream) ? moe_fail(MOE_EHIP, "gradient clip launch failed") : MOE_OK;

@@ -658,10 +658,12 @@ int64_t moe_grad_workspace_bytes(const moe_grad_tensor* t, int32_t n_tensors);
 int moe_grad_bind(const moe_grad_tensor* t, int32_t n_tensors, void* workspace, int64_t workspace_bytes, moe_grad_plan* plan,
                   void* stream);
 
-/* norm, scale (device) fp32 [1], written; max_norm > 0 (or infinite), factor > 0, both representable in fp32. */
+/* norm, scale (device) fp32 [1], written, in none of the tensors or the plan's workspace; max_norm > 0 (or infinite), factor > 0, both
+ * representable in fp32. */
 int moe_grad_norm(const moe_grad_plan* plan, double max_norm, double factor, float* norm, float* scale, void* stream);
 
-/* out = g times *scale (device), in fp32 and then rounded to out's type; in place nothing is touched where *scale is 1. */
+/* out = g times *scale (device; in none of the tensors that are written), in fp32 and then rounded to out's type; in place nothing is
+ * touched where *scale is 1. */
 int moe_grad_clip(const moe_grad_plan* plan, const float* scale, void* stream);
 
 /* While enabled (nonzero), every moe_expert_ffn_overlap and moe_expert_ffn_backward call of this process times

@@ -223,6 +223,18 @@ def test_grad_arguments():
     refused(L.moe_grad_clip(ctypes.byref(ok), P[7] + 1, None), "aligned")
 
 
+@pytest.mark.parametrize("chunks", [0, 1, 3, 5000])
+def test_grad_numbers_in_the_plans_workspace(chunks):
+    """Its records hold the addresses that the next call reads and writes."""
+    L, plan = B.lib(), B.moe_grad_plan(P[5], chunks, 1, 0)
+    t = grads(*([dict(n=chunks * 8192)] if chunks else []))
+    end = P[5] + B.moe_grad_workspace_bytes(t)
+    for at in {P[5], P[5] + 4, (P[5] + end) // 8 * 4, end - 4}:
+        refused(L.moe_grad_norm(ctypes.byref(plan), 1.0, 1.0, at, P[7], None), "workspace")
+        refused(L.moe_grad_norm(ctypes.byref(plan), 1.0, 1.0, P[7], at, None), "workspace")
+        refused(L.moe_grad_clip(ctypes.byref(plan), at, None), "workspace")
+
+
 @pytest.mark.parametrize("experts", [1, 64, 1024])
 @pytest.mark.parametrize("sequences", [1, 3, 40, 255, 256, 3000])
 def test_router_workspace_serves_fewer_tokens(experts, sequences):
