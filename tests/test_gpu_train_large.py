@@ -41,6 +41,42 @@ def test_residual_norm_far_rows():
         assert torch.equal(t[at: at + k], t[:k])
 
 
+@pytest.mark.parametrize("rows,d,depth", [(131100, 16384, 513 + 16 + 15), (600000, 128, 37 + 15 + 64 + 15), (300000, 4096, 586 + 32 + 15)])
+def test_residual_norm_parameter_gradients_of_many_rows(rows, d, depth):
+    """Sums over very many rows in fp32, at the depth that they have instead of one addition after another: a group's rows, the groups of a
+    workgroup, then every 16th workgroup's sums in each of 16 waves, and those."""
+    from expert_output_overlap_amd.runtime import ResidualNorm
+
+    k = 300
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    part = [rnd(k, d).bfloat16() for _ in range(4)]
+    x, h, ds, dn = (repeated(t, rows) for t in part)
+    w = {n: 1 + 0.1 * rnd(d) for n in ("post_weight", "gate", "pre_weight")}
+    op = ResidualNorm(rows, d, post="rms", pre="layer")
+    op.forward(x, h, w)
+    op.backward(ds, dn, x, h, w)
+    px, ph, pds, pdn = (t.to(D) for t in part)
+    w1, gate, w2 = (w[n].to(D) for n in ("post_weight", "gate", "pre_weight"))
+    zero = torch.zeros_like(px)
+    n1, e_n1, _, _ = ref.norm(ph, zero, "rms", 1e-5)
+    s = px + gate * n1 * w1
+    e_s = (gate * w1).abs() * (e_n1 + 4 * E32 * n1.abs()) + 2 * E32 * (px.abs() + s.abs())
+    n2, e_n2, r2, e_r2 = ref.norm(s, e_s, "layer", 1e-5)
+    back, e_b = ref.norm_back(pdn * w2, E32 * (pdn * w2).abs(), n2, e_n2, r2, e_r2, "layer")
+    total = pds + back
+    e_t = e_b + E32 * total.abs()
+    times = torch.full((k, 1), rows // k, dtype=D, device="cuda")
+    times[: rows % k] += 1
+    u1 = (times * total * n1).sum(0)
+    e_u1 = (times * ((depth + 3) * E32 * (total * n1).abs() + e_t * n1.abs() + total.abs() * e_n1)).sum(0)
+    e_w2 = (times * ((depth + 3) * E32 * (pdn * n2).abs() + pdn.abs() * e_n2)).sum(0)
+    for name, value, bound in (("post_weight", gate * u1, gate.abs() * (e_u1 + 2 * E32 * u1.abs())),
+                               ("gate", w1 * u1, w1.abs() * (e_u1 + 2 * E32 * u1.abs())),
+                               ("pre_weight", (times * pdn * n2).sum(0), e_w2)):
+        within(op.grads[name], value, bound + E32 * value.abs(), name)
+
+
 def test_router_far_rows():
     from expert_output_overlap_amd.runtime import RouterLoss
 
