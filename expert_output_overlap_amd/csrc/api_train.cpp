@@ -237,7 +237,7 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* s, const moe_resid
 }
 
 int64_t moe_router_loss_workspace_bytes(const moe_router_shape* s) {
-  return check_router(s) ? -1 : router_workspace_bytes(s->tokens, s->experts, s->top_k, s->sequences);
+  return check_router(s) ? -1 : router_workspace_bytes(s->tokens, s->experts, s->sequences);
 }
 
 int moe_router_loss(const moe_router_shape* s, const float* logits, const int32_t* topk_idx, const int32_t* spans,

@@ -199,7 +199,7 @@ struct RouterLaunch {
   void* dlogits;
   void* workspace;
 };
-int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences);
+int64_t router_workspace_bytes(int64_t tokens, int experts, int sequences);
 int launch_router_loss(const RouterLaunch& a, hipStream_t st);
 int launch_router_backward(const RouterLaunch& a, hipStream_t st);
 

@@ -544,7 +544,7 @@ int parts_of(int64_t tokens, int experts, int sequences) {
 
 }  // namespace
 
-int64_t router_workspace_bytes(int64_t tokens, int experts, int top_k, int sequences) {
+int64_t router_workspace_bytes(int64_t tokens, int experts, int sequences) {
   const int parts = parts_of(tokens, experts, sequences);
   return 4 * counter_words(sequences) + sequences * (16 + parts * 8ll + (parts + groups_of(parts)) * 12ll * experts);
 }
