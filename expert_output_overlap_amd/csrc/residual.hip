@@ -336,9 +336,9 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
   using R = Rows<T, TAIL>;
   constexpr int C = K::C, PER = G <= 64 ? 256 / G : 1, E = NV * C, HELD = WIDE ? C : E, REGS = WIDE ? SUMS - 2 : SUMS;
   constexpr bool BIAS = SUMS == 4, AHEAD = !WIDE;  // AHEAD: registers hold the next row too
-  // h's and x's registers take the differences to the means (4096 x 16384 fp32, two sums: 422 us, made anew in each pass 467; with four sums
-  // 852, made anew 761)
-  constexpr bool KEEP = WIDE && sizeof(T) == 4 && SUMS == 2;
+  // h's and x's registers take the differences to the means (4096 x 16384 fp32, two sums: 403 us, made anew in each pass 469; with four 759
+  // and 768)
+  constexpr bool KEEP = WIDE && sizeof(T) == 4;
   extern __shared__ float sums[];  // WIDE: [2][E][G]
   __shared__ float red[2][3 * (G / 64) + 1];
   __shared__ float join[PER > 1 ? (PER - 1) * SUMS * E * G : 1];
