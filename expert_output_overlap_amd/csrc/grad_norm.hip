@@ -1,7 +1,7 @@
 // The global norm of many gradients, and clipping (formulas in include/moe_overlap.h).
 //
-// Both are bound by HBM: 138.5 million gradients' norm takes 42 us in bf16 (6.6 TB/s, a part of them still in the last-level cache) and
-// 94 in fp32 (5.9); clipped from fp32 into bf16 another 126 (6.6 TB/s of 6 bytes read and written per element).  The tensors are cut
+// Both are bound by HBM: 138.5 million gradients' norm takes 44 us in bf16 (6.3 TB/s) and 94 in fp32 (5.9); clipped from fp32 into bf16
+// another 131 (6.3 TB/s of 6 bytes read and written per element), in place in bf16 82, in fp32 193.  The tensors are cut
 // into chunks of GRAD_CHUNK elements, each a record of the plan's table with its own address, so that a launch of many small tensors
 // has no search; a workgroup takes every grid-th chunk.  A square and its sum are one fp64 instruction on this chip, at the fp32 rate:
 // they hide behind the loads and need no care for the gradients' range.
@@ -14,7 +14,7 @@
 
 namespace {
 
-// Three workgroups on a CU: 138.5 million bf16 gradients 42 us, by two 44, by four 43, by eight 47, by one 71
+// Three workgroups on a CU: 138.5 million bf16 gradients 43.3 us, by two 43.6, by four 45, by eight 48, by one 68
 constexpr int MAX_BLOCKS = 768;
 
 // Sum of squares of a thread's part of a chunk
@@ -123,8 +123,8 @@ __device__ __forceinline__ void scaled(const GradChunk& k, void* to, float f) {
   }
 }
 
-// The chunks backwards: the last ones that k_grad_norm read are still in the last-level cache, where results that go past the caches leave
-// them (138.5 million fp32 gradients into bf16: norm and this 228 us, 250 with results through the caches and flat accesses)
+// The chunks backwards: what k_grad_norm read last may still be in the last-level cache, where results that go past the caches leave
+// it (138.5 million fp32 gradients into bf16: norm and this 225 us, 250 with results through the caches and flat accesses)
 __global__ __launch_bounds__(256) void k_grad_clip(GradLaunch a) {
   const float f = *a.scale;
   const GradChunk k = a.chunks[a.n_chunks - 1 - blockIdx.x];

@@ -7,7 +7,7 @@
 // parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).  Rows stay as they
 // were loaded (bf16 pairs) and are unpacked where they are used, which is what lets 1024 threads of 128 registers hold a backward row of
 // 8192, its parameters, its sums and the next row's loads.
-// 16384 x 7168 bf16, RMS norms and gate: forward 189 us (4.97 TB/s), backward 285 (4.94); layer norms with biases 209 and 311.
+// 16384 x 7168 bf16, RMS norms and gate: forward 188 us (5.00 TB/s), backward 283 (4.98); layer norms with biases 202 and 315.
 #include <algorithm>
 #include <type_traits>
 
@@ -605,9 +605,10 @@ template <typename T, bool TAIL>
 void forward(const ResidualLaunch& a, hipStream_t st) {
   const int chunks = chunks_of(a.d, a.dtype);
   // A wave to a row (a quarter of one to rows of up to 32 chunks) where it can hold one and there are rows for all of eight waves on each CU:
-  // 16384 x 7168 bf16 189 us (5.0 TB/s), by 256 or 1024 threads 250; 65536 x 96 13 us, by whole waves 36.  Fewer rows by a thread to a chunk:
-  // 24 x 4096 bf16 6.0 us, by half as many threads 7.8; 1000 x 7168 17.5, by a wave to a row 19.3.  Rows of more than 1024 chunks by 1024
-  // threads: 8192 x 16384 bf16 243 us, by 512 373, by 256 (which spill) 714
+  // 16384 x 7168 bf16 with layer norms and biases 201 us, by a workgroup to a row 253; with RMS norms, which read fewer parameters, 188 and
+  // 179, 8192 rows 81 and 82, 65536 x 1024 92 and 121; 65536 x 96 14, by workgroups 107, by whole waves 36.  Fewer rows by a thread to a
+  // chunk: 24 x 4096 bf16 6.4 us, by half as many threads 7.8; 1000 x 7168 17.5, by a wave to a row 19.3.  Rows of more than 1024 chunks
+  // by 1024 threads: 8192 x 16384 bf16 246 us, by 512 373, by 256 (which spill) 714
   const int wave = a.rows < 2048 ? 0 : chunks <= 32 ? 16 : chunks <= 1024 ? 64 : 0;
   const int G = wave ? wave : chunks <= 256 ? 256 : chunks <= 512 ? 512 : 1024;
   const int nv = per_thread(chunks, G);
@@ -635,8 +636,8 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
 
 // The threads of the backward's groups.  Eight elements in a thread while registers hold what
 // belongs to them: up to 1024 threads with two sums in bf16.  With four, or in fp32, 512 threads of sixteen (16384 x 7168 bf16, four sums:
-// 311 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 278 and 310), but WIDE in fp32 with four (366; 726 and 887 otherwise);
-// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 507 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
+// 315 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 278 and 310), but WIDE in fp32 with four (363; 726 and 887 otherwise);
+// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 510 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
 int backward_threads(int d, int dtype, bool bias) {
   if (d > 8192) return 1024;
   if (d > 4096) return (dtype == MOE_BF16) == bias ? 512 : 1024;
@@ -704,8 +705,8 @@ int launch_residual(const ResidualLaunch& of, hipStream_t st) {
   ResidualLaunch a = of;
   const bool tb = a.dtype == MOE_BF16, tail = a.d % (tb ? 8 : 4) != 0;
   // Stores past the caches where the rows that the call moves are more than the 256 MB last-level cache: its inputs, just written by the
-  // calls before, are then not driven out by results that would not stay either (16384 x 7168 bf16 forward 195 -> 187 us, 8192 x 7168
-  // 106 -> 79; backward 285 -> 283 and 151 -> 148).  Below that the next call finds the results there
+  // calls before, are then not driven out by results that would not stay either (16384 x 7168 bf16 forward 196 -> 188 us, 8192 x 7168
+  // 107 -> 80; backward 285 -> 283 and 152 both).  Below that the next call finds the results there
   a.past = (a.backward ? 6 : 4) * a.rows * a.d * (tb ? 2 : 4) > 256ll << 20;
   if (!a.backward) {
     if (a.rows == 0) return 0;
