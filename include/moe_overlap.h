@@ -596,9 +596,9 @@ int moe_residual_norm_backward(const moe_residual_norm_shape* s, const moe_resid
  *   e_g = dL balance f[s][g] / (S' N_s) + sum over slots j with expert g of dw[t][j],
  *   dlogits_g = p_g (e_g - sum over h of p_h e_h) + dL z 2 lse p_g / N.
  * Everything in fp32, the sums over rows in 64 bits, in a fixed order: equal calls give equal bits.  An expert with a logit of -inf is not
- * there for its row (p = 0), and a p below 2^-126 is 0; a row without any expert (all -inf) adds 0 to both losses and its gradient is 0, but it is one of
- * its sequence's rows and its choices count.  A NaN or +inf makes its row's gradient and the losses NaN.  An id outside [0, G)
- * counts nowhere, its slot's gradient goes nowhere. */
+ * there for its row (p = 0), and a p below 2^-126 is 0; a row without any expert (all -inf) adds 0 to both losses and its gradient is 0,
+ * but it is one of its sequence's rows and its choices count.  A NaN or +inf makes its row's gradient and the losses NaN.  An id outside
+ * [0, G) counts nowhere, its slot's gradient goes nowhere. */
 typedef struct {
   int64_t tokens;     /* T in [0, 2^30], T top_k < 2^31 */
   int32_t experts;    /* G, 1 .. 1024 */
