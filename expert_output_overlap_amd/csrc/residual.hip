@@ -7,7 +7,7 @@
 // parameters meet the rows as two products, A = gate post_weight and B = gate post_bias: s = rho x + c (A h^ + B).  Rows stay as they
 // were loaded (bf16 pairs) and are unpacked where they are used, which is what lets 1024 threads of 128 registers hold a backward row of
 // 8192, its parameters, its sums and the next row's loads.
-// 16384 x 7168 bf16, RMS norms and gate: forward 188 us (5.00 TB/s), backward 283 (4.98); layer norms with biases 202 and 315.
+// 16384 x 7168 bf16, RMS norms and gate: forward 188 us (5.00 TB/s), backward 283 (4.98); layer norms with biases 202 and 314.
 #include <algorithm>
 #include <type_traits>
 
@@ -336,9 +336,9 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
   using R = Rows<T, TAIL>;
   constexpr int C = K::C, PER = G <= 64 ? 256 / G : 1, E = NV * C, HELD = WIDE ? C : E, REGS = WIDE ? SUMS - 2 : SUMS;
   constexpr bool BIAS = SUMS == 4, AHEAD = !WIDE;  // AHEAD: registers hold the next row too
-  // h's and x's registers take the differences to the means (4096 x 16384 fp32, two sums: 403 us, made anew in each pass 469; with four 759
-  // and 768)
-  constexpr bool KEEP = WIDE && sizeof(T) == 4;
+  // h's and x's registers take the differences to the means (4096 x 16384 fp32, two sums: 397 us, made anew in each pass 471; with four sums
+  // 781, made anew 735)
+  constexpr bool KEEP = WIDE && sizeof(T) == 4 && SUMS == 2;
   extern __shared__ float sums[];  // WIDE: [2][E][G]
   __shared__ float red[2][3 * (G / 64) + 1];
   __shared__ float join[PER > 1 ? (PER - 1) * SUMS * E * G : 1];
@@ -398,8 +398,12 @@ __global__ __launch_bounds__(G <= 64 ? 256 : G) void k_residual_bwd(ResidualLaun
     R::template settle_all<G, NV>(t, d, x);
     R::template settle_all<G, NV>(t, d, g);
     R::template settle_all<G, NV>(t, d, q);
-    const float4 st = nst;
-    const float c = nc, m1 = st.x, r1 = st.y, m2 = st.z, r2 = st.w;
+    // a wave's row is its own from 64 threads on: its numbers go to scalar registers (8192 x 16384 bf16 with biases 1023 us, 1135 without;
+    // 16384 x 7167 452 and 505)
+    auto of_row = [](float v) {
+      return G >= 64 ? __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v))) : v;
+    };
+    const float c = of_row(nc), m1 = of_row(nst.x), r1 = of_row(nst.y), m2 = of_row(nst.z), r2 = of_row(nst.w);
     if (AHEAD && r + step < a.rows) fetch(r + step);
     if (KEEP) {
 #pragma unroll
@@ -636,8 +640,8 @@ void forward(const ResidualLaunch& a, hipStream_t st) {
 
 // The threads of the backward's groups.  Eight elements in a thread while registers hold what
 // belongs to them: up to 1024 threads with two sums in bf16.  With four, or in fp32, 512 threads of sixteen (16384 x 7168 bf16, four sums:
-// 315 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 278 and 310), but WIDE in fp32 with four (363; 726 and 887 otherwise);
-// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 510 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
+// 314 us, 510 by 1024 of eight, which spill; 8192 x 7168 fp32, two: 278 and 310), but WIDE in fp32 with four (366; 726 and 887 otherwise);
+// WIDE with sixteen beyond 8192 (8192 x 16384 bf16, two sums: 490 us, 796 with the next row's loads ahead, 702 by 512 threads of 32)
 int backward_threads(int d, int dtype, bool bias) {
   if (d > 8192) return 1024;
   if (d > 4096) return (dtype == MOE_BF16) == bias ? 512 : 1024;
